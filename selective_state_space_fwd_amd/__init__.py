@@ -14,6 +14,9 @@ ABI of include/ssm_scan.h. PyTorch supplies device memory and the current stream
                                       delta_softplus=False, h0=None, mask=None)
                        # differentiable: scan_train forward, scan_backward under autograd
 
+and, from ``block.py``, the operators around the scan: ``conv``, ``causal_conv``, ``conv_step``,
+``scan_step``, ``ssd_step``, ``norm``, ``gated_norm``.
+
 Inputs may be strided views: the functions above copy them to contiguous tensors first
 (outputs passed in must be contiguous). The ``ssm_scan_*`` functions are the raw C entry
 points (pointers as ints). If the library has not been built this module raises on first
@@ -49,7 +52,10 @@ SSM_CKPT_INTERVAL = 256
 EXPORTED = ("ssm_scan_fwd", "ssm_scan_strerror", "ssm_scan_abi_version",
             "ssm_scan_debug_wave_combine", "ssm_scan_ckpt_count", "ssm_scan_fwd_ckpt",
             "ssm_scan_fwd_masked", "ssm_scan_bwd", "ssm_scan_bwd_workspace_bytes",
-            "ssm_ssd_workspace_bytes", "ssm_ssd_fwd", "ssm_ssd_fwd_noalloc")
+            "ssm_ssd_workspace_bytes", "ssm_ssd_fwd", "ssm_ssd_fwd_noalloc",
+            "ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes", "ssm_conv_step",
+            "ssm_scan_step", "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd",
+            "ssm_norm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -508,3 +514,11 @@ def ssd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
     if status != SSM_OK:
         raise SsmScanError(status)
     return out, final_state
+
+
+# The operators around the scan (after the names they take from this module).
+from .block import (SSM_CONV_SILU, SSM_NORM_BEFORE_GATE, causal_conv, conv,  # noqa: E402,F401
+                    conv_backward, conv_step, gated_norm, norm, norm_backward, norm_train,
+                    scan_step, ssd_step, ssm_conv_bwd, ssm_conv_bwd_workspace_bytes,
+                    ssm_conv_fwd, ssm_conv_step, ssm_norm_bwd, ssm_norm_bwd_workspace_bytes,
+                    ssm_norm_fwd, ssm_scan_step, ssm_ssd_step)

@@ -1,0 +1,541 @@
+"""The operators around the scan in a Mamba block: the short causal convolution before it, the
+single-token steps against a cache of request states, and the gated RMS norm after it.
+
+Argument marshalling only, over the C ABI of include/ssm_conv.h, ssm_step.h and ssm_norm.h. The
+package exports every function here.
+
+    out, final_state = conv(x, weight, bias=None, silu=False, initial_state=None, lengths=None)
+    grads = conv_backward(x, weight, dout, bias=None, silu=False, initial_state=None,
+                          lengths=None, dfinal=None)
+    out, final_state = causal_conv(...as conv...)                 # differentiable
+    out = conv_step(x, state, weight, bias=None, silu=False, slots=None)
+    out = scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None,
+                    delta_softplus=False, slots=None)             # Mamba-1
+    out = ssd_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=False,
+                   slots=None)                                    # Mamba-2
+    out = norm(y, weight, z=None, eps=1e-5, groups=1, norm_before_gate=False,
+               token_major=False)
+    out, rstd = norm_train(...as norm...)
+    grads = norm_backward(y, weight, rstd, dout, z=None, groups=1, norm_before_gate=False,
+                          token_major=False)
+    out = gated_norm(...as norm...)                               # differentiable
+
+Tensors of [batch, dim, seqlen] values (x, y, z) may be views with either the steps or the
+channels contiguous: the scan's output, or ``proj[:, :, a:b].transpose(1, 2)`` of a
+token-major projection. Both are read in place; any other view is copied first. The calls run
+on the current stream of the tensors' device, whichever device is current.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Dict, Optional, Tuple
+
+from . import (SSM_DELTA_SOFTPLUS, SSM_ERR_UNSUPPORTED, SSM_IO_BF16, SSM_IO_F32, SSM_OK,
+               SsmScanError, _dense, _ptr, lib)
+
+SSM_CONV_SILU = 1 << 11
+SSM_NORM_BEFORE_GATE = 1 << 12
+
+_Strides = ctypes.c_int64 * 3
+_bound = False
+
+
+def _lib() -> ctypes.CDLL:
+    """libssmscan.so with the argument types of the entry points below."""
+    global _bound
+    L = lib()
+    if not _bound:
+        vp, i64, u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32
+        L.ssm_conv_fwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, i64, i64, i64, i64, vp]
+        L.ssm_conv_bwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                   i64, i64, i64, i64, i64, vp]
+        L.ssm_conv_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+        L.ssm_conv_step.argtypes = [vp, i64, vp, vp, vp, vp, u32, vp, i64, i64, i64, i64, vp]
+        L.ssm_scan_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
+                                    u32, vp, vp, i64, i64, i64, i64, vp]
+        L.ssm_ssd_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
+                                   u32, vp, vp, i64, i64, i64, i64, i64, vp]
+        L.ssm_norm_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, u32, vp, vp, vp, i64, i64,
+                                   i64, i64, vp]
+        L.ssm_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp,
+                                   i64, i64, i64, i64, i64, vp]
+        L.ssm_norm_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+        for name in ("ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_step", "ssm_scan_step",
+                     "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd"):
+            getattr(L, name).restype = ctypes.c_int
+        L.ssm_conv_bwd_workspace_bytes.restype = i64
+        L.ssm_norm_bwd_workspace_bytes.restype = i64
+        _bound = True
+    return L
+
+
+# ------------------------------------------------------------------ raw C entry points
+
+def ssm_conv_fwd(*args) -> int:
+    return _lib().ssm_conv_fwd(*args)
+
+
+def ssm_conv_bwd(*args) -> int:
+    return _lib().ssm_conv_bwd(*args)
+
+
+def ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags) -> int:
+    return _lib().ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags)
+
+
+def ssm_conv_step(*args) -> int:
+    return _lib().ssm_conv_step(*args)
+
+
+def ssm_scan_step(*args) -> int:
+    return _lib().ssm_scan_step(*args)
+
+
+def ssm_ssd_step(*args) -> int:
+    return _lib().ssm_ssd_step(*args)
+
+
+def ssm_norm_fwd(*args) -> int:
+    return _lib().ssm_norm_fwd(*args)
+
+
+def ssm_norm_bwd(*args) -> int:
+    return _lib().ssm_norm_bwd(*args)
+
+
+def ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
+    return _lib().ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags)
+
+
+# ------------------------------------------------------------------ checks and the call
+
+def _io_flag(name, t) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return SSM_IO_BF16
+    if t.dtype == torch.float32:
+        return SSM_IO_F32
+    raise TypeError(f"unsupported storage dtype {t.dtype} of {name}")
+
+
+def _check(name, t, shape, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _check_out(name, t, shape, dtype, device):
+    _check(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+
+
+def _run(fn, device, *args):
+    """fn(*args, stream) on the current stream of `device`, with that device current."""
+    import torch
+
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != SSM_OK:
+        raise SsmScanError(status)
+
+
+def _in_place(t):
+    """t, or a contiguous copy of a view with neither steps nor channels contiguous."""
+    b, d, L = t.shape
+    return t if L <= 1 or t.stride(2) == 1 or (d > 1 and t.stride(1) == 1) else t.contiguous()
+
+
+def _strides(t):
+    return _Strides(*t.stride())
+
+
+def _empty_like_order(t):
+    """An uninitialised tensor of t's shape with t's contiguous axis (dense)."""
+    import torch
+
+    b, d, L = t.shape
+    if L <= 1 or t.stride(2) == 1:
+        return torch.empty((b, d, L), device=t.device, dtype=t.dtype)
+    return torch.empty((b, L, d), device=t.device, dtype=t.dtype).transpose(1, 2)
+
+
+def _workspace(workspace, need, device):
+    import torch
+
+    if need < 0:
+        raise SsmScanError(SSM_ERR_UNSUPPORTED)
+    if workspace is None:
+        return torch.empty((max(need, 1),), device=device, dtype=torch.uint8)
+    if (workspace.dtype != torch.uint8 or workspace.device != device
+            or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+# ------------------------------------------------------------------ the short convolution
+
+def _conv_inputs(x, weight, bias, initial_state, lengths):
+    import torch
+
+    _check_device("x", x)
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [batch, dim, seqlen] and weight [dim, width]")
+    flags, dev = _io_flag("x", x), x.device
+    batch, dim, seqlen = x.shape
+    width = weight.shape[1]
+    _check("weight", weight, (dim, width), torch.float32, dev)
+    if bias is not None:
+        _check("bias", bias, (dim,), torch.float32, dev)
+    if initial_state is not None:
+        _check("initial_state", initial_state, (batch, dim, width - 1), x.dtype, dev)
+    if lengths is not None:
+        _check("lengths", lengths, (batch,), torch.int32, dev)
+    return flags, _in_place(x), _dense(weight, bias, initial_state, lengths), width
+
+
+def conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=None, out=None,
+         final_state=None, return_final_state: bool = True
+         ) -> Tuple["torch.Tensor", Optional["torch.Tensor"]]:
+    """Causal depthwise convolution over the last ``width`` (2, 3 or 4) steps.
+
+    x: [batch, dim, seqlen] float32 or bfloat16, steps or channels contiguous; weight: [dim,
+    width], bias: [dim] (float32); silu: out = p sigmoid(p); initial_state: [batch, dim,
+    width-1], the inputs before the first step, oldest first (None: zero); lengths: [batch]
+    int32, the steps of each row (clamped to [0, seqlen]; behind them out is 0 and x is not
+    read). Returns (out [batch, dim, seqlen] contiguous, final_state [batch, dim, width-1]: the
+    last inputs of each row, the initial_state of a next call), in x's dtype.
+    """
+    import torch
+
+    flags, x, (weight, bias, initial_state, lengths), width = _conv_inputs(
+        x, weight, bias, initial_state, lengths)
+    batch, dim, seqlen = x.shape
+    dev = x.device
+    if out is None:
+        out = torch.empty((batch, dim, seqlen), device=dev, dtype=x.dtype)
+    else:
+        _check_out("out", out, (batch, dim, seqlen), x.dtype, dev)
+    if final_state is not None:
+        _check_out("final_state", final_state, (batch, dim, width - 1), x.dtype, dev)
+    elif return_final_state:
+        final_state = torch.empty((batch, dim, max(width - 1, 0)), device=dev, dtype=x.dtype)
+    _run(_lib().ssm_conv_fwd, dev, x.data_ptr(), _strides(x), weight.data_ptr(), _ptr(bias),
+         _ptr(initial_state), _ptr(lengths), flags | (SSM_CONV_SILU if silu else 0),
+         out.data_ptr(), _ptr(final_state), batch, dim, width, seqlen)
+    return out, final_state
+
+
+def conv_backward(x, weight, dout, bias=None, silu: bool = False, initial_state=None,
+                  lengths=None, dfinal=None, want_dinitial: Optional[bool] = None,
+                  workspace=None) -> Dict[str, Optional["torch.Tensor"]]:
+    """Gradients of sum(dout * out) + sum(dfinal * final_state) for ``conv`` on the same
+    inputs: dx (x's dtype and contiguous axis), dweight and dbias (float32; dbias None without
+    a bias), dinitial (x's dtype; by default where an initial_state is given, None else).
+    Bitwise reproducible. workspace: a uint8 device tensor of at least
+    ssm_conv_bwd_workspace_bytes(...) bytes, allocated here when None."""
+    import torch
+
+    flags, x, (weight, bias, initial_state, lengths), width = _conv_inputs(
+        x, weight, bias, initial_state, lengths)
+    batch, dim, seqlen = x.shape
+    dev = x.device
+    _check("dout", dout, (batch, dim, seqlen), x.dtype, dev)
+    if dfinal is not None:
+        _check("dfinal", dfinal, (batch, dim, width - 1), x.dtype, dev)
+    dout, dfinal = _dense(dout, dfinal)
+    if want_dinitial is None:
+        want_dinitial = initial_state is not None
+    flags |= SSM_CONV_SILU if silu else 0
+    need = _lib().ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags)
+    workspace = _workspace(workspace, need, dev)
+    f32 = dict(device=dev, dtype=torch.float32)
+    g = {"dx": _empty_like_order(x), "dweight": torch.empty((dim, width), **f32),
+         "dbias": None if bias is None else torch.empty((dim,), **f32),
+         "dinitial": (torch.empty((batch, dim, width - 1), device=dev, dtype=x.dtype)
+                      if want_dinitial else None)}
+    _run(_lib().ssm_conv_bwd, dev, x.data_ptr(), _strides(x), weight.data_ptr(), _ptr(bias),
+         _ptr(initial_state), _ptr(lengths), flags, dout.data_ptr(), _ptr(dfinal),
+         g["dx"].data_ptr(), _strides(g["dx"]), g["dweight"].data_ptr(), _ptr(g["dbias"]),
+         _ptr(g["dinitial"]), workspace.data_ptr(), workspace.numel(), batch, dim, width, seqlen)
+    return g
+
+
+def conv_step(x, state, weight, bias=None, silu: bool = False, slots=None, out=None):
+    """One token of ``conv`` for a batch of requests against a cache of their past inputs.
+
+    x: [batch, dim] (channels contiguous, any row stride); state: [nslots, dim, width-1]
+    contiguous, x's dtype, updated in place; slots: [batch] int32, the slot of each row (None:
+    row i is slot i). A row whose slot lies outside [0, nslots) gives 0 and changes nothing;
+    rows naming one slot are successive tokens of it. Returns out [batch, dim]."""
+    import torch
+
+    _check_device("x", x)
+    if x.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be [batch, dim] and state [nslots, dim, width - 1]")
+    flags, dev = _io_flag("x", x), x.device
+    batch, dim = x.shape
+    nslots, width = state.shape[0], state.shape[2] + 1
+    _check_out("state", state, (nslots, dim, width - 1), x.dtype, dev)
+    _check("weight", weight, (dim, width), torch.float32, dev)
+    if bias is not None:
+        _check("bias", bias, (dim,), torch.float32, dev)
+    if slots is not None:
+        _check("slots", slots, (batch,), torch.int32, dev)
+    weight, bias, slots = _dense(weight, bias, slots)
+    x = _rows(x)
+    if out is None:
+        out = torch.empty((batch, dim), device=dev, dtype=x.dtype)
+    else:
+        _check_out("out", out, (batch, dim), x.dtype, dev)
+    _run(_lib().ssm_conv_step, dev, x.data_ptr(), x.stride(0), state.data_ptr(),
+         weight.data_ptr(), _ptr(bias), _ptr(slots), flags | (SSM_CONV_SILU if silu else 0),
+         out.data_ptr(), batch, nslots, dim, width)
+    return out
+
+
+# ------------------------------------------------------------------ the state step
+
+def _rows(t):
+    """t, or a copy with its last axis contiguous."""
+    return t if t.shape[1] <= 1 or t.stride(1) == 1 else t.contiguous()
+
+
+def _step(fn, heads, x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, out, names):
+    import torch
+
+    f32 = torch.float32
+    _check_device(names[0], x)
+    if x.dim() != 2 or state.dim() != 3 or B.dim() != 2:
+        raise ValueError(f"{names[0]} must be [batch, dim], B and C [batch, dstate] and state "
+                         "[nslots, dim, dstate]")
+    flags, dev, io = _io_flag(names[0], x), x.device, x.dtype
+    batch, dim = x.shape
+    nslots, dstate = state.shape[0], state.shape[2]
+    steps = dim if heads is None else heads
+    _check_out("state", state, (nslots, dim, dstate), f32, dev)
+    _check(names[1], dt, (batch, steps), io, dev)
+    _check("B", B, (batch, dstate), io, dev)
+    _check("C", C, (batch, dstate), io, dev)
+    _check("A", A, (dim, dstate) if heads is None else (heads,), f32, dev)
+    if D is not None:
+        _check("D", D, (dim,), f32, dev)
+    if z is not None:
+        _check("z", z, (batch, dim), io, dev)
+        z = _rows(z)
+    if dt_bias is not None:
+        _check(names[2], dt_bias, (steps,), f32, dev)
+    if slots is not None:
+        _check("slots", slots, (batch,), torch.int32, dev)
+    A, D, dt_bias, slots = _dense(A, D, dt_bias, slots)
+    x, dt, B, C = _rows(x), _rows(dt), _rows(B), _rows(C)
+    if out is None:
+        out = torch.empty((batch, dim), device=dev, dtype=io)
+    else:
+        _check_out("out", out, (batch, dim), io, dev)
+    sizes = (dim,) if heads is None else (heads, dim // heads if heads else 0)
+    _run(fn, dev, x.data_ptr(), x.stride(0), dt.data_ptr(), dt.stride(0), A.data_ptr(),
+         B.data_ptr(), B.stride(0), C.data_ptr(), C.stride(0), _ptr(D), _ptr(z),
+         0 if z is None else z.stride(0), _ptr(dt_bias), _ptr(slots),
+         flags | (SSM_DELTA_SOFTPLUS if softplus else 0), state.data_ptr(), out.data_ptr(),
+         batch, nslots, *sizes, dstate)
+    return out
+
+
+def scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None,
+              delta_softplus: bool = False, slots=None, out=None):
+    """One token of the selective scan for a batch of requests against a cache of states.
+
+    u, delta, z: [batch, dim]; B, C: [batch, dstate] (float32 or bfloat16, any row stride);
+    A: [dim, dstate], D and delta_bias: [dim] (float32); state: [nslots, dim, dstate] float32
+    contiguous, updated in place (dstate at most 256); slots: [batch] int32, the slot of each
+    row (None: row i is slot i). A row whose slot lies outside [0, nslots) gives 0 and changes
+    nothing; rows naming one slot are successive tokens of it. Returns out [batch, dim]."""
+    if A.dim() != 2:
+        raise ValueError("A must be [dim, dstate]")
+    return _step(_lib().ssm_scan_step, None, u, delta, A, B, C, state, D, z, delta_bias,
+                 delta_softplus, slots, out, ("u", "delta", "delta_bias"))
+
+
+def ssd_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+             slots=None, out=None):
+    """One token of the Mamba-2 recurrence (``ssd``), as ``scan_step``: x, z: [batch,
+    nheads*headdim]; dt: [batch, nheads]; A, dt_bias: [nheads]; D: [nheads*headdim]."""
+    if A.dim() != 1:
+        raise ValueError("A must be [nheads]")
+    heads = A.shape[0]
+    if heads == 0 or x.dim() != 2 or x.shape[1] % heads:
+        raise ValueError("x must be [batch, channels], the channels a multiple of the head count")
+    return _step(_lib().ssm_ssd_step, heads, x, dt, A, B, C, state, D, z, dt_bias, dt_softplus,
+                 slots, out, ("x", "dt", "dt_bias"))
+
+
+# ------------------------------------------------------------------ the gated norm
+
+def _norm_inputs(y, weight, z, groups):
+    import torch
+
+    _check_device("y", y)
+    if y.dim() != 3:
+        raise ValueError("y must be [batch, dim, seqlen]")
+    flags, dev = _io_flag("y", y), y.device
+    batch, dim, seqlen = y.shape
+    if groups < 1 or dim % groups:
+        raise ValueError("the channel count must be a multiple of groups")
+    _check("weight", weight, (dim,), torch.float32, dev)
+    if z is not None:
+        _check("z", z, y.shape, y.dtype, dev)
+        z = _in_place(z)
+    return flags, _in_place(y), z, _dense(weight)[0]
+
+
+def _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out, save):
+    import torch
+
+    flags, y, z, weight = _norm_inputs(y, weight, z, groups)
+    batch, dim, seqlen = y.shape
+    dev = y.device
+    shape = (batch, seqlen, dim) if token_major else (batch, dim, seqlen)
+    if out is None:
+        out = torch.empty(shape, device=dev, dtype=y.dtype)
+    else:
+        _check_out("out", out, shape, y.dtype, dev)
+    rstd = (torch.empty((batch, groups, seqlen), device=dev, dtype=torch.float32) if save
+            else None)
+    _run(_lib().ssm_norm_fwd, dev, y.data_ptr(), _strides(y), _ptr(z),
+         None if z is None else _strides(z), weight.data_ptr(), eps,
+         flags | (SSM_NORM_BEFORE_GATE if norm_before_gate else 0), out.data_ptr(),
+         _strides(out.transpose(1, 2)) if token_major else None, _ptr(rstd), batch, dim, groups,
+         seqlen)
+    return out, rstd
+
+
+def norm(y, weight, z=None, eps: float = 1e-5, groups: int = 1, norm_before_gate: bool = False,
+         token_major: bool = False, out=None):
+    """RMS norm over the channels of each of ``groups`` equal groups, with a gate.
+
+    y, z: [batch, dim, seqlen] float32 or bfloat16, steps or channels contiguous; weight: [dim]
+    float32. out = weight v / sqrt(mean(v^2) + eps) with v = y silu(z), or, with
+    norm_before_gate, v = y and the result times silu(z); z None: no gate. Returns out in y's
+    dtype, contiguous: [batch, dim, seqlen], or [batch, seqlen, dim] with token_major (the
+    order an output projection reads)."""
+    return _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out, False)[0]
+
+
+def norm_train(y, weight, z=None, eps: float = 1e-5, groups: int = 1,
+               norm_before_gate: bool = False, token_major: bool = False, out=None):
+    """``norm`` that also returns 1 / sqrt(mean + eps) of every token and group, [batch,
+    groups, seqlen] float32, which ``norm_backward`` takes."""
+    return _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out, True)
+
+
+def norm_backward(y, weight, rstd, dout, z=None, groups: int = 1, norm_before_gate: bool = False,
+                  token_major: bool = False, workspace=None
+                  ) -> Dict[str, Optional["torch.Tensor"]]:
+    """Gradients of sum(dout * out) for ``norm`` on the same inputs: dy, dz (y's dtype, each with
+    its input's contiguous axis; dz None without a gate) and dweight (float32). rstd:
+    ``norm_train``'s; dout: of out's shape, steps or channels contiguous. Bitwise
+    reproducible. workspace: a uint8 device tensor of at least
+    ssm_norm_bwd_workspace_bytes(...) bytes, allocated here when None."""
+    import torch
+
+    flags, y, z, weight = _norm_inputs(y, weight, z, groups)
+    batch, dim, seqlen = y.shape
+    dev = y.device
+    _check_out("rstd", rstd, (batch, groups, seqlen), torch.float32, dev)
+    _check("dout", dout, (batch, seqlen, dim) if token_major else (batch, dim, seqlen), y.dtype,
+           dev)
+    dout = _in_place(dout.transpose(1, 2) if token_major else dout)
+    flags |= SSM_NORM_BEFORE_GATE if norm_before_gate else 0
+    need = _lib().ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags)
+    workspace = _workspace(workspace, need, dev)
+    g = {"dy": _empty_like_order(y), "dz": None if z is None else _empty_like_order(z),
+         "dweight": torch.empty((dim,), device=dev, dtype=torch.float32)}
+    _run(_lib().ssm_norm_bwd, dev, y.data_ptr(), _strides(y), _ptr(z),
+         None if z is None else _strides(z), weight.data_ptr(), rstd.data_ptr(), dout.data_ptr(),
+         _strides(dout), flags, g["dy"].data_ptr(), _strides(g["dy"]), _ptr(g["dz"]),
+         None if z is None else _strides(g["dz"]), g["dweight"].data_ptr(), workspace.data_ptr(),
+         workspace.numel(), batch, dim, groups, seqlen)
+    return g
+
+
+# ------------------------------------------------------------------ autograd
+
+_functions = None
+
+
+def _autograd():
+    """The torch.autograd.Functions behind ``causal_conv`` and ``gated_norm`` (built on first
+    use, so that importing this module does not import torch)."""
+    global _functions
+    if _functions is not None:
+        return _functions
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class CausalConv(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, initial_state, lengths, silu):
+            out, fin = conv(x, weight, bias=bias, silu=silu, initial_state=initial_state,
+                            lengths=lengths)
+            ctx.save_for_backward(x, weight, bias, initial_state, lengths)
+            ctx.silu = silu
+            ctx.set_materialize_grads(False)
+            return out, fin
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dout, dfin):
+            x, weight, bias, initial_state, lengths = ctx.saved_tensors
+            dout = x.new_zeros(x.shape) if dout is None else dout
+            g = conv_backward(x, weight, dout, bias=bias, silu=ctx.silu,
+                              initial_state=initial_state, lengths=lengths, dfinal=dfin)
+            return g["dx"], g["dweight"], g["dbias"], g["dinitial"], None, None
+
+    class GatedNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, y, weight, z, eps, groups, norm_before_gate, token_major):
+            out, rstd = norm_train(y, weight, z=z, eps=eps, groups=groups,
+                                   norm_before_gate=norm_before_gate, token_major=token_major)
+            ctx.save_for_backward(y, weight, z, rstd)
+            ctx.options = dict(groups=groups, norm_before_gate=norm_before_gate,
+                               token_major=token_major)
+            return out
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dout):
+            y, weight, z, rstd = ctx.saved_tensors
+            g = norm_backward(y, weight, rstd, dout, z=z, **ctx.options)
+            return g["dy"], g["dweight"], g["dz"], None, None, None, None
+
+    _functions = (CausalConv, GatedNorm)
+    return _functions
+
+
+def causal_conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=None
+                ) -> Tuple["torch.Tensor", "torch.Tensor"]:
+    """Differentiable ``conv``: (out, final_state), with gradients for x, weight, bias and
+    initial_state through autograd (``conv_backward``)."""
+    return _autograd()[0].apply(x, weight, bias, initial_state, lengths, bool(silu))
+
+
+def gated_norm(y, weight, z=None, eps: float = 1e-5, groups: int = 1,
+               norm_before_gate: bool = False, token_major: bool = False) -> "torch.Tensor":
+    """Differentiable ``norm``, with gradients for y, weight and z through autograd
+    (``norm_backward``)."""
+    return _autograd()[1].apply(y, weight, z, float(eps), int(groups), bool(norm_before_gate),
+                                bool(token_major))

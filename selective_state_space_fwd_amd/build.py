@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, "libssmscan.so")
 PROBE_SOURCE = os.path.join(PKG, "probes", "alu_probe.hip")
 PROBE_LIB_PATH = os.path.join(PKG, "libssmprobe.so")
 SOURCES = ["scan_kernels.hip", "scan_short.hip", "scan_bwd.hip", "ssd_kernels.hip", "scan_api.cpp",
-           "ssd_api.cpp", "ssd_noalloc.hip"]
+           "ssd_api.cpp", "ssd_noalloc.hip", "conv_kernels.hip", "conv_api.cpp", "step_kernels.hip",
+           "step_api.cpp", "norm_kernels.hip", "norm_api.cpp"]
 # A test-only build of the Mamba-1 scan with a second launch shape of the chunked kernel (the
 # same 16 steps per lane, other channels per workgroup and states per LDS stage), which the
 # parity tests run against the oracle and against the default build.

@@ -1,0 +1,192 @@
+// Internal interface between the C-ABI layer of the operators around the scan (conv_api.cpp,
+// step_api.cpp, norm_api.cpp) and their kernels. Not installed; the public ABI is
+// include/ssm_conv.h, ssm_step.h and ssm_norm.h.
+#pragma once
+#include <stdint.h>
+
+#include "scan_launch.h"
+
+namespace ssm {
+
+// Element strides of a [batch, dim, seqlen] array.
+struct Strides {
+  int64_t batch, channel, step;
+};
+
+// Which of a tensor's axes is contiguous in memory. Time: runs of steps of one channel (what
+// the scan takes); Channel: runs of channels of one step (a projection's output).
+enum class Order : int { Time = 0, Channel = 1 };
+
+// ---------------------------------------------------------------- short causal convolution
+
+constexpr int kConvMinWidth = 2;
+constexpr int kConvMaxWidth = 4;
+// Steps per lane.
+constexpr int kConvSteps = 8;
+// Waves per workgroup.
+constexpr int kConvWaves = 4;
+
+// Everything a convolution launch needs, already validated by the C-ABI layer.
+struct ConvArgs {
+  const void* x;
+  Strides xs;
+  Order order;              // of x and dx
+  const float* weight;      // [dim, width]
+  const float* bias;        // nullable
+  const void* initial;      // nullable: [batch, dim, width - 1]
+  const int32_t* lengths;   // nullable: [batch]
+  void* out;                // [batch, dim, seqlen]
+  void* final_state;        // nullable: [batch, dim, width - 1]
+  // backward
+  const void* dout;         // [batch, dim, seqlen]
+  const void* dfinal;       // nullable
+  void* dx;
+  Strides dxs;
+  float* dweight;
+  float* dbias;             // nullable
+  void* dinitial;           // nullable
+  float* workspace;         // conv_partials(...) x dim x (width + 1) floats
+  int64_t batch, dim, width, seqlen;
+  Io io;
+  bool silu;
+};
+
+// Lanes along one row in the time-ordered kernels: the power of two, at most a wave, that
+// covers the row with kConvSteps steps per lane.
+inline int conv_row_lanes_log2(int64_t seqlen) {
+  int lg = 0;
+  while (lg < 6 && (int64_t(kConvSteps) << lg) < seqlen) ++lg;
+  return lg;
+}
+
+// Steps one workgroup of the channel-ordered kernels covers (its waves lie along time).
+inline int64_t conv_channel_tile_steps(Io io) {
+  return int64_t(kConvSteps) * (io == Io::BF16 ? 8 : 4) * kConvWaves;
+}
+
+// Tiles of one row that one wave of the time-ordered backward walks.
+constexpr int kConvBwdTiles = 4;
+
+// Partial sums of dweight and dbias per channel: one per batch row and run of steps.
+inline int64_t conv_partials(int64_t batch, int64_t seqlen, Io io, Order order) {
+  const int64_t run = order == Order::Channel
+                          ? conv_channel_tile_steps(io)
+                          : int64_t(kConvBwdTiles) * (int64_t(kConvSteps) << conv_row_lanes_log2(seqlen));
+  return batch * (seqlen > 0 ? seqlen / run + (seqlen % run != 0) : 1);
+}
+
+int launch_conv_fwd(const ConvArgs& a, void* stream);
+int launch_conv_bwd(const ConvArgs& a, void* stream);
+
+struct ConvStepArgs {
+  const void* x;            // [batch, dim], rows x_stride apart
+  int64_t x_stride;
+  void* state;              // [nslots, dim, width - 1]
+  const float* weight;
+  const float* bias;        // nullable
+  const int32_t* slots;     // nullable: row i is slot i
+  void* out;                // [batch, dim]
+  int64_t batch, nslots, dim, width;
+  Io io;
+  bool silu;
+};
+int launch_conv_step(const ConvStepArgs& a, void* stream);
+
+// ---------------------------------------------------------------- single-token state step
+
+// One step of the recurrence for `batch` rows against a cache of states. headdim 0: Mamba-1
+// (A [dim, dstate], dt and dt_bias per channel); else Mamba-2 (A, dt and dt_bias per head of
+// headdim channels).
+struct StepArgs {
+  const void* x;            // [batch, dim], rows x_stride apart; likewise dt, B, C, z
+  const void* dt;
+  const void* B;
+  const void* C;
+  const void* z;            // nullable
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+  const float* A;
+  const float* D;           // nullable
+  const float* dt_bias;     // nullable
+  float* state;             // [nslots, dim, dstate]
+  const int32_t* slots;     // nullable
+  void* out;                // [batch, dim]
+  int64_t batch, nslots, dim, dstate, headdim;
+  Io io;
+  bool softplus;
+};
+constexpr int64_t kStepMaxState = 256;
+int launch_state_step(const StepArgs& a, void* stream);
+
+// ---------------------------------------------------------------- gated RMS norm
+
+// A tensor of [batch, dim, seqlen] values in either memory order.
+struct View {
+  const void* p;  // written through for outputs
+  Strides s;
+  Order order;
+};
+
+struct NormArgs {
+  View y, z, out;           // z.p nullable (no gate)
+  const float* weight;      // [dim]
+  float* rstd;              // of every token and group: forward nullable, written; backward read
+  Strides rs;               // of rstd, with the group in the place of the channel
+  float eps;
+  // backward (out unused)
+  View dout, dy, dz;        // dz.p required when z is given
+  float* dweight;           // [dim]
+  float* workspace;         // norm_partials(...) x dim floats
+  int64_t batch, dim, groups, seqlen;
+  Io io;
+  bool norm_first;
+};
+
+// How a launch covers the tensors: a lane holds 16 bytes of channels by `steps` steps (1 when
+// every tensor has channels contiguous, else as many steps as channels); 2^lanes_log2 lanes
+// of a wave lie along the channels of one group, the others along time; `waves` waves of a
+// workgroup along the channels, which cover the group in `blocks` rounds.
+struct NormShape {
+  int steps, lanes_log2, waves;
+  int64_t blocks, tiles;    // tiles: workgroups along time
+};
+
+// Most waves of a workgroup, forward and backward (the backward holds one tensor more).
+constexpr int kNormFwdWaves = 16;
+constexpr int kNormBwdWaves = 8;
+
+inline NormShape norm_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel,
+                            int most_waves) {
+  const int64_t cv = io == Io::BF16 ? 8 : 4;
+  const int64_t g = dim / groups;
+  NormShape s;
+  s.steps = all_channel ? 1 : int(cv);
+  // Lanes along channels: all that the group has work for, then fewer, down to eight, while
+  // half the most waves still cover the group and the sequence has steps for the lanes freed.
+  int lg = 0;
+  while (lg < 6 && (cv << lg) < g) ++lg;
+  while (!all_channel && lg > 3 &&
+         (g + (cv << (lg - 1)) - 1) / (cv << (lg - 1)) <= most_waves / 2 &&
+         int64_t(s.steps) * (64 >> lg) < seqlen)
+    --lg;
+  s.lanes_log2 = lg;
+  const int64_t w = (g + (cv << lg) - 1) / (cv << lg);
+  s.waves = int(w < most_waves ? w : most_waves);
+  s.blocks = (w + s.waves - 1) / s.waves;
+  const int64_t run = int64_t(s.steps) * (64 >> lg);
+  s.tiles = seqlen / run + (seqlen % run != 0);
+  return s;
+}
+
+// Partial sums of dweight per channel: one per batch row and tile of steps.
+inline int64_t norm_partials(int64_t batch, const NormShape& s) { return batch * s.tiles; }
+
+// The backward takes squares of channels by steps whatever the orders (a lane of one step
+// would leave a partial sum of dweight per token).
+inline NormShape norm_bwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io) {
+  return norm_shape(dim, groups, seqlen, io, false, kNormBwdWaves);
+}
+
+int launch_norm_fwd(const NormArgs& a, void* stream);
+int launch_norm_bwd(const NormArgs& a, void* stream);
+
+}  // namespace ssm
