@@ -31,41 +31,42 @@ import ctypes
 from typing import Dict, Optional, Tuple
 
 from . import (SSM_DELTA_SOFTPLUS, SSM_ERR_UNSUPPORTED, SSM_IO_BF16, SSM_IO_F32, SSM_OK,
-               SsmScanError, _dense, _ptr, lib)
+               SsmScanError, _ptr, lib)
 
 SSM_CONV_SILU = 1 << 11
 SSM_NORM_BEFORE_GATE = 1 << 12
 
 _Strides = ctypes.c_int64 * 3
-_bound = False
+_bound = None
 
 
 def _lib() -> ctypes.CDLL:
     """libssmscan.so with the argument types of the entry points below."""
     global _bound
+    if _bound is not None:
+        return _bound
     L = lib()
-    if not _bound:
-        vp, i64, u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32
-        L.ssm_conv_fwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, i64, i64, i64, i64, vp]
-        L.ssm_conv_bwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, vp,
-                                   i64, i64, i64, i64, i64, vp]
-        L.ssm_conv_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
-        L.ssm_conv_step.argtypes = [vp, i64, vp, vp, vp, vp, u32, vp, i64, i64, i64, i64, vp]
-        L.ssm_scan_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
-                                    u32, vp, vp, i64, i64, i64, i64, vp]
-        L.ssm_ssd_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
-                                   u32, vp, vp, i64, i64, i64, i64, i64, vp]
-        L.ssm_norm_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, u32, vp, vp, vp, i64, i64,
-                                   i64, i64, vp]
-        L.ssm_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp,
-                                   i64, i64, i64, i64, i64, vp]
-        L.ssm_norm_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
-        for name in ("ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_step", "ssm_scan_step",
-                     "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd"):
-            getattr(L, name).restype = ctypes.c_int
-        L.ssm_conv_bwd_workspace_bytes.restype = i64
-        L.ssm_norm_bwd_workspace_bytes.restype = i64
-        _bound = True
+    vp, i64, u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32
+    L.ssm_conv_fwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, i64, i64, i64, i64, vp]
+    L.ssm_conv_bwd.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, vp,
+                               i64, i64, i64, i64, i64, vp]
+    L.ssm_conv_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+    L.ssm_conv_step.argtypes = [vp, i64, vp, vp, vp, vp, u32, vp, i64, i64, i64, i64, vp]
+    L.ssm_scan_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
+                                u32, vp, vp, i64, i64, i64, i64, vp]
+    L.ssm_ssd_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
+                               u32, vp, vp, i64, i64, i64, i64, i64, vp]
+    L.ssm_norm_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, u32, vp, vp, vp, i64, i64,
+                               i64, i64, vp]
+    L.ssm_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp,
+                               i64, i64, i64, i64, i64, vp]
+    L.ssm_norm_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+    for name in ("ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_step", "ssm_scan_step",
+                 "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd"):
+        getattr(L, name).restype = ctypes.c_int
+    L.ssm_conv_bwd_workspace_bytes.restype = i64
+    L.ssm_norm_bwd_workspace_bytes.restype = i64
+    _bound = L
     return L
 
 
@@ -108,47 +109,74 @@ def ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
 
 
 # ------------------------------------------------------------------ checks and the call
+#
+# A decode loop makes these calls once per layer and token, so the checks are written for their
+# cost: one look at each tensor, the message formed only for one that fails, devices as ints.
 
 def _io_flag(name, t) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _torch().bfloat16:
         return SSM_IO_BF16
-    if t.dtype == torch.float32:
+    if dtype is _torch().float32:
         return SSM_IO_F32
-    raise TypeError(f"unsupported storage dtype {t.dtype} of {name}")
+    raise TypeError(f"unsupported storage dtype {dtype} of {name}")
 
 
-def _check(name, t, shape, dtype, device):
+def _check(name, t, shape, dtype, dev):
+    """t has this shape and dtype and is on device number dev."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    raise ValueError(f"{name} must be on cuda:{dev}")
 
 
-def _check_out(name, t, shape, dtype, device):
-    _check(name, t, shape, dtype, device)
+def _check_out(name, t, shape, dtype, dev):
+    _check(name, t, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_device(name, t):
+def _param(name, t, shape, dtype, dev):
+    """An optional array that the C ABI takes contiguous (a strided one is copied)."""
+    if t is None:
+        return None
+    _check(name, t, shape, dtype, dev)
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _device(name, t) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
 
 
-def _run(fn, device, *args):
-    """fn(*args, stream) on the current stream of `device`, with that device current."""
-    import torch
+_torch_module = _raw_stream = _current_device = None
 
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream)
+
+def _torch():
+    """torch, imported on first use; with it, the cheapest ways to its current stream's handle
+    and device number that it offers."""
+    global _torch_module, _raw_stream, _current_device
+    if _torch_module is None:
+        import torch
+
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _torch_module = torch
+    return _torch_module
+
+
+def _run(fn, dev, *args):
+    """fn(*args, stream) on the current stream of device `dev`, with that device current."""
+    if _current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream)
+        with _torch().cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
     if status != SSM_OK:
         raise SsmScanError(status)
 
@@ -159,52 +187,49 @@ def _in_place(t):
     return t if L <= 1 or t.stride(2) == 1 or (d > 1 and t.stride(1) == 1) else t.contiguous()
 
 
+def _rows(t):
+    """t, or a copy with its last axis contiguous."""
+    return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
+
+
 def _strides(t):
     return _Strides(*t.stride())
 
 
 def _empty_like_order(t):
     """An uninitialised tensor of t's shape with t's contiguous axis (dense)."""
-    import torch
-
     b, d, L = t.shape
     if L <= 1 or t.stride(2) == 1:
-        return torch.empty((b, d, L), device=t.device, dtype=t.dtype)
-    return torch.empty((b, L, d), device=t.device, dtype=t.dtype).transpose(1, 2)
+        return t.new_empty((b, d, L))
+    return t.new_empty((b, L, d)).transpose(1, 2)
 
 
-def _workspace(workspace, need, device):
-    import torch
-
+def _workspace(workspace, need, like):
+    torch = _torch()
     if need < 0:
         raise SsmScanError(SSM_ERR_UNSUPPORTED)
     if workspace is None:
-        return torch.empty((max(need, 1),), device=device, dtype=torch.uint8)
-    if (workspace.dtype != torch.uint8 or workspace.device != device
+        return like.new_empty((max(need, 1),), dtype=torch.uint8)
+    if (workspace.dtype != torch.uint8 or workspace.get_device() != like.get_device()
             or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
     return workspace
 
 
 # ------------------------------------------------------------------ the short convolution
 
 def _conv_inputs(x, weight, bias, initial_state, lengths):
-    import torch
-
-    _check_device("x", x)
+    torch = _torch()
+    dev = _device("x", x)
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [batch, dim, seqlen] and weight [dim, width]")
-    flags, dev = _io_flag("x", x), x.device
+    flags, f32 = _io_flag("x", x), torch.float32
     batch, dim, seqlen = x.shape
     width = weight.shape[1]
-    _check("weight", weight, (dim, width), torch.float32, dev)
-    if bias is not None:
-        _check("bias", bias, (dim,), torch.float32, dev)
-    if initial_state is not None:
-        _check("initial_state", initial_state, (batch, dim, width - 1), x.dtype, dev)
-    if lengths is not None:
-        _check("lengths", lengths, (batch,), torch.int32, dev)
-    return flags, _in_place(x), _dense(weight, bias, initial_state, lengths), width
+    return (flags, dev, _in_place(x), _param("weight", weight, (dim, width), f32, dev),
+            _param("bias", bias, (dim,), f32, dev),
+            _param("initial_state", initial_state, (batch, dim, width - 1), x.dtype, dev),
+            _param("lengths", lengths, (batch,), torch.int32, dev), batch, dim, width, seqlen)
 
 
 def conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=None, out=None,
@@ -219,20 +244,16 @@ def conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=N
     read). Returns (out [batch, dim, seqlen] contiguous, final_state [batch, dim, width-1]: the
     last inputs of each row, the initial_state of a next call), in x's dtype.
     """
-    import torch
-
-    flags, x, (weight, bias, initial_state, lengths), width = _conv_inputs(
-        x, weight, bias, initial_state, lengths)
-    batch, dim, seqlen = x.shape
-    dev = x.device
+    (flags, dev, x, weight, bias, initial_state, lengths, batch, dim, width,
+     seqlen) = _conv_inputs(x, weight, bias, initial_state, lengths)
     if out is None:
-        out = torch.empty((batch, dim, seqlen), device=dev, dtype=x.dtype)
+        out = x.new_empty((batch, dim, seqlen))
     else:
         _check_out("out", out, (batch, dim, seqlen), x.dtype, dev)
     if final_state is not None:
         _check_out("final_state", final_state, (batch, dim, width - 1), x.dtype, dev)
     elif return_final_state:
-        final_state = torch.empty((batch, dim, max(width - 1, 0)), device=dev, dtype=x.dtype)
+        final_state = x.new_empty((batch, dim, max(width - 1, 0)))
     _run(_lib().ssm_conv_fwd, dev, x.data_ptr(), _strides(x), weight.data_ptr(), _ptr(bias),
          _ptr(initial_state), _ptr(lengths), flags | (SSM_CONV_SILU if silu else 0),
          out.data_ptr(), _ptr(final_state), batch, dim, width, seqlen)
@@ -247,26 +268,20 @@ def conv_backward(x, weight, dout, bias=None, silu: bool = False, initial_state=
     a bias), dinitial (x's dtype; by default where an initial_state is given, None else).
     Bitwise reproducible. workspace: a uint8 device tensor of at least
     ssm_conv_bwd_workspace_bytes(...) bytes, allocated here when None."""
-    import torch
-
-    flags, x, (weight, bias, initial_state, lengths), width = _conv_inputs(
-        x, weight, bias, initial_state, lengths)
-    batch, dim, seqlen = x.shape
-    dev = x.device
-    _check("dout", dout, (batch, dim, seqlen), x.dtype, dev)
-    if dfinal is not None:
-        _check("dfinal", dfinal, (batch, dim, width - 1), x.dtype, dev)
-    dout, dfinal = _dense(dout, dfinal)
+    f32 = _torch().float32
+    (flags, dev, x, weight, bias, initial_state, lengths, batch, dim, width,
+     seqlen) = _conv_inputs(x, weight, bias, initial_state, lengths)
+    io = x.dtype
+    dout = _param("dout", dout, (batch, dim, seqlen), io, dev)
+    dfinal = _param("dfinal", dfinal, (batch, dim, width - 1), io, dev)
     if want_dinitial is None:
         want_dinitial = initial_state is not None
     flags |= SSM_CONV_SILU if silu else 0
-    need = _lib().ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags)
-    workspace = _workspace(workspace, need, dev)
-    f32 = dict(device=dev, dtype=torch.float32)
-    g = {"dx": _empty_like_order(x), "dweight": torch.empty((dim, width), **f32),
-         "dbias": None if bias is None else torch.empty((dim,), **f32),
-         "dinitial": (torch.empty((batch, dim, width - 1), device=dev, dtype=x.dtype)
-                      if want_dinitial else None)}
+    workspace = _workspace(
+        workspace, _lib().ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags), x)
+    g = {"dx": _empty_like_order(x), "dweight": x.new_empty((dim, width), dtype=f32),
+         "dbias": None if bias is None else x.new_empty((dim,), dtype=f32),
+         "dinitial": x.new_empty((batch, dim, width - 1)) if want_dinitial else None}
     _run(_lib().ssm_conv_bwd, dev, x.data_ptr(), _strides(x), weight.data_ptr(), _ptr(bias),
          _ptr(initial_state), _ptr(lengths), flags, dout.data_ptr(), _ptr(dfinal),
          g["dx"].data_ptr(), _strides(g["dx"]), g["dweight"].data_ptr(), _ptr(g["dbias"]),
@@ -281,77 +296,63 @@ def conv_step(x, state, weight, bias=None, silu: bool = False, slots=None, out=N
     contiguous, x's dtype, updated in place; slots: [batch] int32, the slot of each row (None:
     row i is slot i). A row whose slot lies outside [0, nslots) gives 0 and changes nothing;
     rows naming one slot are successive tokens of it. Returns out [batch, dim]."""
-    import torch
-
-    _check_device("x", x)
+    torch = _torch()
+    dev = _device("x", x)
     if x.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be [batch, dim] and state [nslots, dim, width - 1]")
-    flags, dev = _io_flag("x", x), x.device
+    flags, io, f32 = _io_flag("x", x), x.dtype, torch.float32
     batch, dim = x.shape
-    nslots, width = state.shape[0], state.shape[2] + 1
-    _check_out("state", state, (nslots, dim, width - 1), x.dtype, dev)
-    _check("weight", weight, (dim, width), torch.float32, dev)
-    if bias is not None:
-        _check("bias", bias, (dim,), torch.float32, dev)
-    if slots is not None:
-        _check("slots", slots, (batch,), torch.int32, dev)
-    weight, bias, slots = _dense(weight, bias, slots)
+    nslots, _, past = state.shape
+    _check_out("state", state, (nslots, dim, past), io, dev)
+    weight = _param("weight", weight, (dim, past + 1), f32, dev)
+    bias = _param("bias", bias, (dim,), f32, dev)
+    slots = _param("slots", slots, (batch,), torch.int32, dev)
     x = _rows(x)
     if out is None:
-        out = torch.empty((batch, dim), device=dev, dtype=x.dtype)
+        out = x.new_empty((batch, dim))
     else:
-        _check_out("out", out, (batch, dim), x.dtype, dev)
+        _check_out("out", out, (batch, dim), io, dev)
     _run(_lib().ssm_conv_step, dev, x.data_ptr(), x.stride(0), state.data_ptr(),
          weight.data_ptr(), _ptr(bias), _ptr(slots), flags | (SSM_CONV_SILU if silu else 0),
-         out.data_ptr(), batch, nslots, dim, width)
+         out.data_ptr(), batch, nslots, dim, past + 1)
     return out
 
 
 # ------------------------------------------------------------------ the state step
 
-def _rows(t):
-    """t, or a copy with its last axis contiguous."""
-    return t if t.shape[1] <= 1 or t.stride(1) == 1 else t.contiguous()
-
-
 def _step(fn, heads, x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, out, names):
-    import torch
-
-    f32 = torch.float32
-    _check_device(names[0], x)
+    torch = _torch()
+    dev = _device(names[0], x)
     if x.dim() != 2 or state.dim() != 3 or B.dim() != 2:
         raise ValueError(f"{names[0]} must be [batch, dim], B and C [batch, dstate] and state "
                          "[nslots, dim, dstate]")
-    flags, dev, io = _io_flag(names[0], x), x.device, x.dtype
+    flags, io, f32 = _io_flag(names[0], x), x.dtype, torch.float32
     batch, dim = x.shape
-    nslots, dstate = state.shape[0], state.shape[2]
+    nslots, _, dstate = state.shape
     steps = dim if heads is None else heads
     _check_out("state", state, (nslots, dim, dstate), f32, dev)
     _check(names[1], dt, (batch, steps), io, dev)
     _check("B", B, (batch, dstate), io, dev)
     _check("C", C, (batch, dstate), io, dev)
-    _check("A", A, (dim, dstate) if heads is None else (heads,), f32, dev)
-    if D is not None:
-        _check("D", D, (dim,), f32, dev)
+    A = _param("A", A, (dim, dstate) if heads is None else (heads,), f32, dev)
+    D = _param("D", D, (dim,), f32, dev)
+    dt_bias = _param(names[2], dt_bias, (steps,), f32, dev)
+    slots = _param("slots", slots, (batch,), torch.int32, dev)
+    z_ptr = z_stride = 0
     if z is not None:
         _check("z", z, (batch, dim), io, dev)
         z = _rows(z)
-    if dt_bias is not None:
-        _check(names[2], dt_bias, (steps,), f32, dev)
-    if slots is not None:
-        _check("slots", slots, (batch,), torch.int32, dev)
-    A, D, dt_bias, slots = _dense(A, D, dt_bias, slots)
+        z_ptr, z_stride = z.data_ptr(), z.stride(0)
     x, dt, B, C = _rows(x), _rows(dt), _rows(B), _rows(C)
     if out is None:
-        out = torch.empty((batch, dim), device=dev, dtype=io)
+        out = x.new_empty((batch, dim))
     else:
         _check_out("out", out, (batch, dim), io, dev)
-    sizes = (dim,) if heads is None else (heads, dim // heads if heads else 0)
+    sizes = (dim,) if heads is None else (heads, dim // heads)
     _run(fn, dev, x.data_ptr(), x.stride(0), dt.data_ptr(), dt.stride(0), A.data_ptr(),
-         B.data_ptr(), B.stride(0), C.data_ptr(), C.stride(0), _ptr(D), _ptr(z),
-         0 if z is None else z.stride(0), _ptr(dt_bias), _ptr(slots),
-         flags | (SSM_DELTA_SOFTPLUS if softplus else 0), state.data_ptr(), out.data_ptr(),
-         batch, nslots, *sizes, dstate)
+         B.data_ptr(), B.stride(0), C.data_ptr(), C.stride(0), _ptr(D), z_ptr, z_stride,
+         _ptr(dt_bias), _ptr(slots), flags | (SSM_DELTA_SOFTPLUS if softplus else 0),
+         state.data_ptr(), out.data_ptr(), batch, nslots, *sizes, dstate)
     return out
 
 
@@ -386,40 +387,35 @@ def ssd_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: b
 # ------------------------------------------------------------------ the gated norm
 
 def _norm_inputs(y, weight, z, groups):
-    import torch
-
-    _check_device("y", y)
+    dev = _device("y", y)
     if y.dim() != 3:
         raise ValueError("y must be [batch, dim, seqlen]")
-    flags, dev = _io_flag("y", y), y.device
+    flags = _io_flag("y", y)
     batch, dim, seqlen = y.shape
     if groups < 1 or dim % groups:
         raise ValueError("the channel count must be a multiple of groups")
-    _check("weight", weight, (dim,), torch.float32, dev)
+    weight = _param("weight", weight, (dim,), _torch().float32, dev)
     if z is not None:
         _check("z", z, y.shape, y.dtype, dev)
         z = _in_place(z)
-    return flags, _in_place(y), z, _dense(weight)[0]
+    return flags, dev, _in_place(y), z, weight, batch, dim, seqlen
 
 
 def _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out, save):
-    import torch
-
-    flags, y, z, weight = _norm_inputs(y, weight, z, groups)
-    batch, dim, seqlen = y.shape
-    dev = y.device
+    flags, dev, y, z, weight, batch, dim, seqlen = _norm_inputs(y, weight, z, groups)
     shape = (batch, seqlen, dim) if token_major else (batch, dim, seqlen)
     if out is None:
-        out = torch.empty(shape, device=dev, dtype=y.dtype)
+        out = y.new_empty(shape)
     else:
         _check_out("out", out, shape, y.dtype, dev)
-    rstd = (torch.empty((batch, groups, seqlen), device=dev, dtype=torch.float32) if save
-            else None)
-    _run(_lib().ssm_norm_fwd, dev, y.data_ptr(), _strides(y), _ptr(z),
-         None if z is None else _strides(z), weight.data_ptr(), eps,
-         flags | (SSM_NORM_BEFORE_GATE if norm_before_gate else 0), out.data_ptr(),
-         _strides(out.transpose(1, 2)) if token_major else None, _ptr(rstd), batch, dim, groups,
-         seqlen)
+    rstd = y.new_empty((batch, groups, seqlen), dtype=_torch().float32) if save else None
+    z_ptr = z_strides = None
+    if z is not None:
+        z_ptr, z_strides = z.data_ptr(), _strides(z)
+    _run(_lib().ssm_norm_fwd, dev, y.data_ptr(), _strides(y), z_ptr, z_strides,
+         weight.data_ptr(), eps, flags | (SSM_NORM_BEFORE_GATE if norm_before_gate else 0),
+         out.data_ptr(), _Strides(seqlen * dim, 1, dim) if token_major else None, _ptr(rstd),
+         batch, dim, groups, seqlen)
     return out, rstd
 
 
@@ -450,20 +446,17 @@ def norm_backward(y, weight, rstd, dout, z=None, groups: int = 1, norm_before_ga
     ``norm_train``'s; dout: of out's shape, steps or channels contiguous. Bitwise
     reproducible. workspace: a uint8 device tensor of at least
     ssm_norm_bwd_workspace_bytes(...) bytes, allocated here when None."""
-    import torch
-
-    flags, y, z, weight = _norm_inputs(y, weight, z, groups)
-    batch, dim, seqlen = y.shape
-    dev = y.device
-    _check_out("rstd", rstd, (batch, groups, seqlen), torch.float32, dev)
+    f32 = _torch().float32
+    flags, dev, y, z, weight, batch, dim, seqlen = _norm_inputs(y, weight, z, groups)
+    _check_out("rstd", rstd, (batch, groups, seqlen), f32, dev)
     _check("dout", dout, (batch, seqlen, dim) if token_major else (batch, dim, seqlen), y.dtype,
            dev)
     dout = _in_place(dout.transpose(1, 2) if token_major else dout)
     flags |= SSM_NORM_BEFORE_GATE if norm_before_gate else 0
-    need = _lib().ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags)
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace(
+        workspace, _lib().ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags), y)
     g = {"dy": _empty_like_order(y), "dz": None if z is None else _empty_like_order(z),
-         "dweight": torch.empty((dim,), device=dev, dtype=torch.float32)}
+         "dweight": y.new_empty((dim,), dtype=f32)}
     _run(_lib().ssm_norm_bwd, dev, y.data_ptr(), _strides(y), _ptr(z),
          None if z is None else _strides(z), weight.data_ptr(), rstd.data_ptr(), dout.data_ptr(),
          _strides(dout), flags, g["dy"].data_ptr(), _strides(g["dy"]), _ptr(g["dz"]),

@@ -150,36 +150,103 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
+// ---------------------------------------------------------------- partial rows
+
+// The sum over rows of part[row][col] for one column per thread of a workgroup of kCols columns by
+// kSlices slices of the rows, in a fixed order: a slice's rows in order, eight loads at once,
+// then the slices. The result is in the threads of slice 0.
+template <int kCols, int kSlices>
+__device__ __forceinline__ float sum_rows(const float* part, int64_t rows, int64_t cols, int64_t col,
+                                          float (&buf)[kSlices][kCols + 1]) {
+  const int col_in = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+  float a = 0.0f;
+  if (col < cols) {
+    int64_t r = slice;
+    for (; r + 7 * kSlices < rows; r += 8 * kSlices) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[(r + i * kSlices) * cols + col];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a += v[i];
+    }
+    for (; r < rows; r += kSlices) a += part[r * cols + col];
+  }
+  buf[slice][col_in] = a;
+  __syncthreads();
+  if (slice == 0)
+    for (int s = 1; s < kSlices; ++s) a += buf[s][col_in];
+  return a;
+}
+
 // ---------------------------------------------------------------- cache slots
 
 // Rows of a single-token call name cache slots; rows naming the same slot are successive
 // tokens of it, in row order. Of such rows the first takes all (a workgroup each, so the state
 // stays in registers between them): `first` says whether row r is it, `next` is the following
-// row of the slot (INT32_MAX: none). Every lane of the wave takes part.
+// row of the slot (INT32_MAX: none).
 struct SlotOrder {
   bool first;
   int next;
 };
 
-__device__ __forceinline__ SlotOrder slot_order(const int32_t* slots, int batch, int r, int slot) {
-  bool before = false;
-  int next = INT32_MAX;
-#pragma unroll 4
-  for (int i = threadIdx.x & 63; i < batch; i += 64) {
-    const bool same = slots[i] == slot;
-    before |= same && i < r;
-    next = same && i > r && i < next ? i : next;
+// The search over all rows' slots for the R rows from r on (their slots in `slot`, < 0: none),
+// shared by the kWaves waves of a workgroup (its threads read each slot once), every one of
+// whose threads takes part. buf: LDS; a call may follow another with the other `turn` (0 or
+// 1) and no barrier between.
+template <int kWaves, int R>
+__device__ __forceinline__ void slot_order(const int32_t* slots, int batch, int r, const int (&slot)[R],
+                                           int (&buf)[2][kWaves][2], int turn, SlotOrder (&order)[R]) {
+  bool before[R];
+  int next[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    before[k] = false;
+    next[k] = INT32_MAX;
   }
-  SlotOrder o;
-  o.first = __ballot(before) == 0;
-  if (__ballot(next != INT32_MAX) != 0) {
-    for (int m = 32; m > 0; m >>= 1) {
-      const int other = __shfl_xor(next, m, 64);
-      next = other < next ? other : next;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < batch; i += 64 * kWaves) {
+    const int s = slots[i];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      before[k] |= s == slot[k] && i < r + k;
+      next[k] = s == slot[k] && i > r + k && i < next[k] ? i : next[k];
     }
   }
-  o.next = __builtin_amdgcn_readfirstlane(next);
-  return o;
+  // Almost every search finds nothing, so a wave says in one word whether it found any row of
+  // the R slots, and the rows themselves are looked for only then.
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < R; ++k) any |= (__ballot(before[k]) != 0 ? 1u : 0u) << k;
+  bool later = false;
+#pragma unroll
+  for (int k = 0; k < R; ++k) later |= next[k] != INT32_MAX;
+  if (__ballot(later) != 0) any |= 1u << 31;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) buf[turn][wave][0] = int(any);
+  __syncthreads();
+  any = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) any |= uint32_t(buf[turn][w][0]);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    order[k].first = ((any >> k) & 1u) == 0;
+    order[k].next = INT32_MAX;
+  }
+  if (any >> 31) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      for (int m = 32; m > 0; m >>= 1) {
+        const int other = __shfl_xor(next[k], m, 64);
+        next[k] = other < next[k] ? other : next[k];
+      }
+      if ((threadIdx.x & 63) == 0) buf[turn][wave][1] = next[k];
+      __syncthreads();
+      for (int w = 0; w < kWaves; ++w)
+        order[k].next = buf[turn][w][1] < order[k].next ? buf[turn][w][1] : order[k].next;
+      order[k].next = __builtin_amdgcn_readfirstlane(order[k].next);
+      __syncthreads();
+    }
+  }
 }
 
 }  // namespace ssm

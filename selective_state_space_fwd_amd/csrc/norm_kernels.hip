@@ -430,22 +430,14 @@ __global__ __launch_bounds__(64 * kNormBwdWaves) void norm_bwd_kernel(NormParams
   }
 }
 
-// The partial rows summed in a fixed order: 32 columns by 8 slices of the rows per workgroup.
-__global__ __launch_bounds__(256) void norm_bwd_reduce(const float* part, float* dweight, int64_t rows,
-                                                       int64_t cols) {
-  __shared__ float sums[8][33];
-  const int col_in = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t col = int64_t(blockIdx.x) * 32 + col_in;
-  float a = 0.0f;
-  if (col < cols)
-    for (int64_t r = slice; r < rows; r += 8) a += part[r * cols + col];
-  sums[slice][col_in] = a;
-  __syncthreads();
-  if (slice == 0 && col < cols) {
-#pragma unroll
-    for (int s = 1; s < 8; ++s) a += sums[s][col_in];
-    dweight[col] = a;
-  }
+constexpr int kReduceCols = 32, kReduceSlices = 32;
+
+__global__ __launch_bounds__(kReduceCols* kReduceSlices) void norm_bwd_reduce(const float* part, float* dweight,
+                                                                              int64_t rows, int64_t cols) {
+  __shared__ float buf[kReduceSlices][kReduceCols + 1];
+  const int64_t col = int64_t(blockIdx.x) * kReduceCols + threadIdx.x % kReduceCols;
+  const float a = sum_rows<kReduceCols, kReduceSlices>(part, rows, cols, col, buf);
+  if (threadIdx.x < kReduceCols && col < cols) dweight[col] = a;
 }
 
 Tensor tensor_of(const View& v) {
@@ -541,8 +533,8 @@ int launch_norm_bwd(const NormArgs& a, void* stream) {
     if (err) return err;
     rows = norm_partials(a.batch, s);
   }
-  hipLaunchKernelGGL(norm_bwd_reduce, dim3(unsigned((a.dim + 31) / 32)), dim3(256), 0, st, a.workspace,
-                     a.dweight, rows, a.dim);
+  hipLaunchKernelGGL(norm_bwd_reduce, dim3(unsigned((a.dim + kReduceCols - 1) / kReduceCols)),
+                     dim3(kReduceCols * kReduceSlices), 0, st, a.workspace, a.dweight, rows, a.dim);
   return int(hipGetLastError());
 }
 

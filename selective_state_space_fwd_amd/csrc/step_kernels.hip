@@ -5,9 +5,12 @@
 //   dt = softplus(dt + bias);  h = exp(dt A) h + dt x B;  y = sum_n C h + D x;  out = y silu(z)
 //
 // The state, fp32, is all of the traffic (8 bytes a state against 2 or 4 per channel), so the
-// layout is the state's: a lane holds four consecutive states (16 bytes) of kCh channels, a
-// channel's lanes are consecutive and a power of two in number, and every load of a wave is
-// issued before the first use. y is the sum over a channel's lanes.
+// layout is the state's: a lane holds four consecutive states (16 bytes) of CH channels, a
+// channel's lanes are consecutive and a power of two in number. What there is one of per
+// channel (x, the step size, D, z) is loaded by one lane per channel of the wave, in one
+// access each, and dealt to the channel's lanes through the LDS crossbar; y, the sum over a
+// channel's lanes, goes back the same way, so that out is one access too. No load waits for
+// another but the state's for its slot.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,7 +21,6 @@ namespace ssm {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kCh = 4;  // channels per lane
 
 struct StepParams {
   const void* x;
@@ -49,97 +51,133 @@ __device__ __forceinline__ void load4_row(const void* base, int64_t off, int n, 
   for (int i = 0; i < 4; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
 }
 
-// LG: log2 of the lanes per channel.
-template <typename Elem, int LG, bool kHeads>
+// What a lane holds for its one channel of the wave's (lanes past the wave's channels: zeros).
+struct Channel {
+  float x, dt, z;
+};
+
+// LG: log2 of the lanes per channel. CH: channels per lane, at most 2^LG (a lane per channel).
+template <typename Elem, int LG, int CH, bool kHeads>
 __global__ __launch_bounds__(64 * kWaves) void state_step_kernel(StepParams p) {
   constexpr int CPW = 64 >> LG;  // channels per wave and access
+  static_assert(CH * CPW <= 64, "a lane per channel");
   const int lane = threadIdx.x & 63;
   const int wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
   const int n0 = (lane & ((1 << LG) - 1)) * 4;
   const int nn = p.dstate - n0 < 4 ? p.dstate - n0 : 4;  // states of this lane (<= 0: none)
-  const int64_t first_ch = int64_t(wave) * kCh * CPW + (lane >> LG);
+  const int64_t ch0 = int64_t(wave) * (CH * CPW);        // the wave's first channel
+  const int64_t mine = ch0 + lane;                       // this lane's one channel
+  const bool own = lane < CH * CPW && mine < p.dim;
+  const int64_t first_ch = ch0 + (lane >> LG);           // of its states, the first
   int r = blockIdx.y;
   const int slot = p.slots ? p.slots[r] : r;
-  if (slot < 0 || slot >= p.nslots) {  // a row of no slot: zeros
-#pragma unroll
-    for (int k = 0; k < kCh; ++k) {
-      const int64_t ch = first_ch + k * CPW;
-      if (n0 == 0 && ch < p.dim) static_cast<Elem*>(p.out)[int64_t(r) * p.dim + ch] = Elem(0);
+
+  const int64_t step = kHeads ? int64_t(uint32_t(own ? mine : 0) / uint32_t(p.headdim)) : mine;
+  auto load_channel = [&](int row) {
+    Channel c{0.0f, 0.0f, 0.0f};
+    if (own) {
+      c.x = widen<Elem>(static_cast<const Elem*>(p.x)[row * p.xs + mine]);
+      c.dt = widen<Elem>(static_cast<const Elem*>(p.dt)[row * p.dts + step]);
+      if (p.z) c.z = widen<Elem>(static_cast<const Elem*>(p.z)[row * p.zs + mine]);
     }
+    return c;
+  };
+  Channel c = load_channel(r);
+  const float bias = own && p.bias ? p.bias[step] : 0.0f;
+  const float skip = own && p.D ? p.D[mine] : 0.0f;
+  const float head_a = kHeads && own ? p.A[step] * kLog2e : 0.0f;
+  float bv[4], cv[4], a[kHeads ? 1 : CH][4], h[CH][4];
+  load4_row<Elem>(p.B, r * p.bs + n0, nn, bv);
+  load4_row<Elem>(p.C, r * p.cs + n0, nn, cv);
+  if (slot < 0 || slot >= p.nslots) {  // a row of no slot: zeros
+    if (own) static_cast<Elem*>(p.out)[int64_t(r) * p.dim + mine] = Elem(0);
     return;
   }
-  float h[kCh][4], a[kCh][4];
 #pragma unroll
-  for (int k = 0; k < kCh; ++k) {
+  for (int k = 0; k < CH; ++k) {
     const int64_t ch = first_ch + k * CPW;
     const int n = ch < p.dim ? nn : 0;
     load4(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, n, h[k]);
-    if constexpr (kHeads) {
-      a[k][0] = ch < p.dim ? p.A[uint32_t(ch) / uint32_t(p.headdim)] * kLog2e : 0.0f;
-    } else {
+    if constexpr (!kHeads) {
       load4(p.A + ch * p.dstate + n0, n, a[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[k][i] *= kLog2e;
     }
   }
-  SlotOrder order{true, INT32_MAX};
-  if (p.slots) order = slot_order(p.slots, p.batch, r, slot);
-  if (!order.first) return;
+  __shared__ int found[2][kWaves][2];
+  int turn = 0;
+  SlotOrder order[1] = {{true, INT32_MAX}};
+  const int slots[1] = {slot};
+  if (p.slots) slot_order<kWaves, 1>(p.slots, p.batch, r, slots, found, turn, order);
+  if (!order[0].first) return;  // the first row of this slot takes this one
   for (;;) {
-    float bv[4], cv[4], x[kCh], y[kCh];
-    load4_row<Elem>(p.B, r * p.bs + n0, nn, bv);
-    load4_row<Elem>(p.C, r * p.cs + n0, nn, cv);
+    float dt = c.dt + bias;
+    if (p.softplus) dt = softplus_f(dt);
+    const float dx = dt * c.x;
+    const float deal = kHeads ? exp2_hw(dt * head_a) : dt;  // Mamba-2: the decay itself
+    float y[CH];
 #pragma unroll
-    for (int k = 0; k < kCh; ++k) {
-      const int64_t ch = first_ch + k * CPW;
-      const bool ok = ch < p.dim;
-      const int64_t step = kHeads ? int64_t(uint32_t(ok ? ch : 0) / uint32_t(p.headdim)) : ch;
-      x[k] = ok ? widen<Elem>(static_cast<const Elem*>(p.x)[r * p.xs + ch]) : 0.0f;
-      float dt = ok ? widen<Elem>(static_cast<const Elem*>(p.dt)[r * p.dts + step]) : 0.0f;
-      if (ok && p.bias) dt += p.bias[step];
-      if (p.softplus) dt = softplus_f(dt);
-      const float dx = dt * x[k];
-      const float one = kHeads ? exp2_hw(dt * a[k][0]) : 0.0f;
+    for (int k = 0; k < CH; ++k) {
+      const int from = k * CPW + (lane >> LG);
+      const float dk = __shfl(deal, from, 64), dxk = __shfl(dx, from, 64);
       y[k] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float keep = kHeads ? one : exp2_hw(dt * a[k][i]);
-        h[k][i] = __builtin_fmaf(keep, h[k][i], dx * bv[i]);
+        const float keep = kHeads ? dk : exp2_hw(dk * a[kHeads ? 0 : k][i]);
+        h[k][i] = __builtin_fmaf(keep, h[k][i], dxk * bv[i]);
         // (a lane's states past dstate add nothing, whatever dt x is)
         y[k] = i < nn ? __builtin_fmaf(cv[i], h[k][i], y[k]) : y[k];
       }
     }
+    float yc = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kCh; ++k) y[k] = sum_lanes<LG>(y[k]);
-#pragma unroll
-    for (int k = 0; k < kCh; ++k) {
-      const int64_t ch = first_ch + k * CPW;
-      if (n0 == 0 && ch < p.dim) {
-        float v = p.D ? __builtin_fmaf(p.D[ch], x[k], y[k]) : y[k];
-        if (p.z) v = gate_f(v, widen<Elem>(static_cast<const Elem*>(p.z)[r * p.zs + ch]));
-        static_cast<Elem*>(p.out)[int64_t(r) * p.dim + ch] = narrow<Elem>(v);
-      }
+    for (int k = 0; k < CH; ++k) {
+      const float v = __shfl(sum_lanes<LG>(y[k]), (lane & (CPW - 1)) << LG, 64);
+      yc = (lane / CPW) == k ? v : yc;
     }
-    if (order.next == INT32_MAX) break;
-    r = order.next;
-    order = slot_order(p.slots, p.batch, r, slot);
+    if (own) {
+      float v = p.D ? __builtin_fmaf(skip, c.x, yc) : yc;
+      if (p.z) v = gate_f(v, c.z);
+      static_cast<Elem*>(p.out)[int64_t(r) * p.dim + mine] = narrow<Elem>(v);
+    }
+    if (order[0].next == INT32_MAX) break;
+    r = order[0].next;
+    slot_order<kWaves, 1>(p.slots, p.batch, r, slots, found, turn ^= 1, order);
+    c = load_channel(r);
+    load4_row<Elem>(p.B, r * p.bs + n0, nn, bv);
+    load4_row<Elem>(p.C, r * p.cs + n0, nn, cv);
   }
 #pragma unroll
-  for (int k = 0; k < kCh; ++k) {
+  for (int k = 0; k < CH; ++k) {
     const int64_t ch = first_ch + k * CPW;
     const int n = ch < p.dim ? nn : 0;
     store_run<float, 4>(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, n, h[k]);
   }
 }
 
-template <typename Elem, int LG>
-void run_lg(const StepArgs& a, const StepParams& p, hipStream_t s) {
-  constexpr int per = kWaves * kCh * (64 >> LG);
+template <typename Elem, int LG, int CH>
+void run_ch(const StepArgs& a, const StepParams& p, hipStream_t s) {
+  constexpr int per = kWaves * CH * (64 >> LG);
   const dim3 grid(unsigned((a.dim + per - 1) / per), unsigned(a.batch));
   if (a.headdim)
-    hipLaunchKernelGGL((state_step_kernel<Elem, LG, true>), grid, dim3(64 * kWaves), 0, s, p);
+    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, true>), grid, dim3(64 * kWaves), 0, s, p);
   else
-    hipLaunchKernelGGL((state_step_kernel<Elem, LG, false>), grid, dim3(64 * kWaves), 0, s, p);
+    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, false>), grid, dim3(64 * kWaves), 0, s, p);
+}
+
+// Eight channels per lane (fewer where a wave has no lane per channel) while that leaves a wave
+// for every slot of the device, 8192; two below, for more waves. Mamba-2, 64 heads x 64, 128
+// states: 256 rows take 197 us with eight channels (205 with four, 284 with two, 200 with
+// sixteen), 5.5 TB/s, as a large copy; 32 heads, 8 rows take 5.9 us with two (5.9 with four,
+// 7.9 with one).
+template <typename Elem, int LG>
+void run_lg(const StepArgs& a, const StepParams& p, hipStream_t s) {
+  constexpr int most = (1 << LG) < 8 ? (1 << LG) : 8;
+  constexpr int few = most < 2 ? most : 2;
+  if (a.dim * a.batch / (most * (64 >> LG)) < 8192)
+    run_ch<Elem, LG, few>(a, p, s);
+  else
+    run_ch<Elem, LG, most>(a, p, s);
 }
 
 template <typename Elem>
