@@ -52,8 +52,8 @@ extern "C" {
  * final_state to the initial state. out and final_state must overlap no other argument (a
  * strided array counts with its whole extent).
  * Returns SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (width, a storage type other than
- * fp32/bf16, neither stride 1, batch*dim or seqlen above 2^31 - 1, or a launch of more than
- * 2^31 - 1 waves or workgroups), SSM_ERR_MISALIGNED (a pointer not aligned to its element
+ * fp32/bf16, neither stride 1, batch above 65535, batch*dim or seqlen above 2^31 - 1, or a
+ * launch of more than 2^31 - 1 waves along a batch row), SSM_ERR_MISALIGNED (a pointer not aligned to its element
  * size) or SSM_ERR_HIP.
  */
 SSM_API int ssm_conv_fwd(const void* x, const int64_t* x_strides, const float* weight,
@@ -97,7 +97,7 @@ SSM_API int64_t ssm_conv_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t
  * A row whose slot lies outside [0, nslots) (-1, say: the padding of a captured batch) has no
  * state: its out is 0 and nothing else is written. Rows naming the same slot are successive
  * tokens of it, in row order. out and state must overlap no other argument. Errors as
- * ssm_conv_fwd; batch at most 65535 (SSM_ERR_UNSUPPORTED above).
+ * ssm_conv_fwd.
  */
 SSM_API int ssm_conv_step(const void* x, int64_t x_stride, void* state, const float* weight,
                           const float* bias, const int32_t* slots, uint32_t flags, void* out,

@@ -59,18 +59,23 @@ inline int conv_row_lanes_log2(int64_t seqlen) {
   return lg;
 }
 
+// Channels a wave of the channel-ordered kernels covers.
+constexpr int kConvWaveChannels = 64;
+
+// Channels per lane of the channel-ordered kernels.
+constexpr int kConvLaneChannels = 4;
+
 // Steps one workgroup of the channel-ordered kernels covers (its waves lie along time).
-inline int64_t conv_channel_tile_steps(Io io) {
-  return int64_t(kConvSteps) * (io == Io::BF16 ? 8 : 4) * kConvWaves;
-}
+constexpr int64_t kConvChannelTileSteps =
+    int64_t(kConvSteps) * (64 * kConvLaneChannels / kConvWaveChannels) * kConvWaves;
 
 // Tiles of one row that one wave of the time-ordered backward walks.
 constexpr int kConvBwdTiles = 4;
 
 // Partial sums of dweight and dbias per channel: one per batch row and run of steps.
-inline int64_t conv_partials(int64_t batch, int64_t seqlen, Io io, Order order) {
+inline int64_t conv_partials(int64_t batch, int64_t seqlen, Order order) {
   const int64_t run = order == Order::Channel
-                          ? conv_channel_tile_steps(io)
+                          ? kConvChannelTileSteps
                           : int64_t(kConvBwdTiles) * (int64_t(kConvSteps) << conv_row_lanes_log2(seqlen));
   return batch * (seqlen > 0 ? seqlen / run + (seqlen % run != 0) : 1);
 }

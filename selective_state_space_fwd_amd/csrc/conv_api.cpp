@@ -29,7 +29,7 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t dim, int64_t width, int64
   if (width < ssm::kConvMinWidth || width > ssm::kConvMaxWidth) return SSM_ERR_UNSUPPORTED;
   z->esz = io == SSM_IO_BF16 ? 2 : 4;
   int64_t rows, bytes;
-  if (!mul_ok(batch, dim, &rows) || rows > kInt32Max || dim > kInt32Max || batch > kInt32Max ||
+  if (!mul_ok(batch, dim, &rows) || rows > kInt32Max || dim > kInt32Max || batch > 65535 ||
       seqlen > kInt32Max || !mul_ok(rows, seqlen, &z->elems) || !mul_ok(z->elems, z->esz, &bytes) ||
       dim > kInt32Max / (width + 1))
     return SSM_ERR_UNSUPPORTED;
@@ -37,15 +37,17 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t dim, int64_t width, int64
   return SSM_OK;
 }
 
-// The most waves or workgroups of any launch (one run of steps per lane at least).
+// The most waves along the grid's first axis, and workgroups in all, of any launch (one run of
+// steps per lane at least; the second axis is the batch row).
 bool launch_fits(int64_t batch, int64_t dim, int64_t seqlen) {
   const int lg = ssm::conv_row_lanes_log2(seqlen);
   const int64_t run = int64_t(ssm::kConvSteps) << lg, per = int64_t(1) << (6 - lg);
   const int64_t tiles = seqlen > 0 ? (seqlen + run - 1) / run : 1;
-  int64_t waves, wgs;
-  if (!mul_ok((batch * dim + per - 1) / per, tiles, &waves) || waves > kInt32Max) return false;
-  const int64_t crun = ssm::conv_channel_tile_steps(ssm::Io::F32);
-  return mul_ok((dim + 63) / 64 * ((seqlen + crun - 1) / crun), batch, &wgs) && wgs <= kInt32Max;
+  int64_t waves;
+  if (!mul_ok((dim + per - 1) / per, tiles, &waves) || waves > kInt32Max) return false;
+  const int64_t crun = ssm::kConvChannelTileSteps, cw = ssm::kConvWaveChannels;
+  int64_t wgs;
+  return mul_ok((dim + cw - 1) / cw * ((seqlen + crun - 1) / crun), batch, &wgs) && wgs <= kInt32Max;
 }
 
 // A single step has runs of no length either way: the time-ordered kernels' lanes then lie
@@ -114,10 +116,9 @@ int64_t ssm_conv_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t width, 
   if (batch < 0 || dim < 0 || seqlen < 0 || width < ssm::kConvMinWidth || width > ssm::kConvMaxWidth ||
       (io != SSM_IO_F32 && io != SSM_IO_BF16))
     return -1;
-  const ssm::Io s = io == SSM_IO_BF16 ? ssm::Io::BF16 : ssm::Io::F32;
-  if (seqlen > kInt32Max || batch > kInt32Max) return -1;
-  const int64_t t = ssm::conv_partials(batch, seqlen, s, ssm::Order::Time);
-  const int64_t c = ssm::conv_partials(batch, seqlen, s, ssm::Order::Channel);
+  if (seqlen > kInt32Max || batch > 65535) return -1;
+  const int64_t t = ssm::conv_partials(batch, seqlen, ssm::Order::Time);
+  const int64_t c = ssm::conv_partials(batch, seqlen, ssm::Order::Channel);
   int64_t row, total;
   if (!mul_ok(dim, (width + 1) * 4, &row) || !mul_ok(t > c ? t : c, row, &total)) return -1;
   return total;
@@ -178,7 +179,7 @@ int ssm_conv_step(const void* x, int64_t x_stride, void* state, const float* wei
   if (int st = check_sizes(flags, batch, dim, width, 1, &z)) return st;
   if (nslots < 0 || (!slots && nslots < batch)) return SSM_ERR_INVALID_ARG;
   int64_t cache, bytes, reach;
-  if (batch > 65535 || nslots > kInt32Max || !mul_ok(nslots, dim, &cache) ||
+  if (nslots > kInt32Max || !mul_ok(nslots, dim, &cache) ||
       !mul_ok(cache, (width - 1) * z.esz, &bytes))
     return SSM_ERR_UNSUPPORTED;
   if (batch > 1 && x_stride < 0) return SSM_ERR_INVALID_ARG;

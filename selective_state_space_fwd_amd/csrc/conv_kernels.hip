@@ -8,13 +8,21 @@
 // registers and only the W - 1 inputs at a block's edge are fetched twice (or taken from the
 // neighbouring lane). Two orders of x in memory:
 //   time     runs of steps: a lane holds one channel's 8 steps, lanes lie along time;
-//   channel  runs of channels (a slice of a projection's output): a lane holds 16 bytes of
-//            channels by 8 steps, loads one 16-byte word per step and stores one run of
-//            steps per channel, which turns the order through registers alone. A wave
-//            covers 64 channels by 64 (bf16) or 32 (fp32) steps: 128-byte or longer
-//            segments on both sides.
+//   channel  runs of channels (a slice of a projection's output): a lane holds 4 channels by 8
+//            steps, loads one word of channels per step and stores one run of steps per
+//            channel, which turns the order through registers alone. A wave covers 64
+//            channels by 32 steps, a workgroup 128 steps.
 // Sums are fp32; a result is rounded once, at its store. A row's steps at and behind its
-// length are never read; its outputs there are zeros.
+// length do not count; its outputs there are zeros.
+//
+// b4, 2304 channels, 2048 steps, bf16 (75 MB in and out, 12 us by a library copy of that size):
+// 15.5 us channel order, 16 us time order, by the kernel trace. What that took: no branch
+// around a load (23 -> 16 us, with the weights of a workgroup in LDS instead of a load per
+// channel that is waited for), index arithmetic of 32 bits (time order 20 -> 16: it was VALU
+// bound), stores past L2 (1 us). Eight channels a lane 17.7 us, sixteen-channel waves 28 us.
+// The gradient (113 MB): 34 us channel order, 28.5 us time order, of which the VALU needs 21
+// (a sigmoid for 11 steps of each 8); 43 us with workgroups in plain order, where an XCD's
+// tiles all lie at one offset of the 4096-byte rows and so in two of its L2's channels.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,6 +34,7 @@ namespace {
 
 constexpr int S = kConvSteps;
 constexpr int kThreads = 64 * kConvWaves;
+constexpr int CW = kConvWaveChannels;
 
 struct ConvParams {
   const void* x;
@@ -42,52 +51,61 @@ struct ConvParams {
   int64_t dxb, dxc, dxt;
   void* dinitial;
   float* part;       // [batch * runs][dim][W + 1]
-  int batch, dim, seqlen;
+  uint32_t dim, seqlen;
   int silu;
-  uint32_t waves;    // time order: waves with work
+  uint32_t waves;    // time order: waves with work, per batch row
   uint32_t tiles;    // runs of steps per row
   int lanes_log2;    // time order: lanes along a row
-  uint32_t cblocks;  // channel order: blocks of 64 channels
 };
 
-__device__ __forceinline__ int row_length(const ConvParams& p, int b) {
+// The grid's second axis is the batch row.
+__device__ __forceinline__ uint32_t row_length(const ConvParams& p, int b) {
   if (!p.lengths) return p.seqlen;
   const int n = p.lengths[b];
-  return n < 0 ? 0 : n > p.seqlen ? p.seqlen : n;
+  return n < 0 ? 0 : uint32_t(n) > p.seqlen ? p.seqlen : uint32_t(n);
 }
 
+// Steps of a row from t0 on, before `end`.
+__device__ __forceinline__ int steps_left(uint32_t end, uint32_t t0) { return t0 < end ? int(end - t0) : 0; }
+
 template <int W>
-__device__ __forceinline__ void load_weights(const ConvParams& p, int d, float (&w)[W], float& bias) {
+__device__ __forceinline__ void load_weights(const ConvParams& p, uint32_t d, float (&w)[W], float& bias) {
 #pragma unroll
   for (int k = 0; k < W; ++k) w[k] = p.weight[int64_t(d) * W + k];
   bias = p.bias ? p.bias[d] : 0.0f;
 }
 
-// Place m of e: the initial state for m < W - 1 (zero without one), x at step m - (W - 1).
+// Place m of e, in fp32: the initial state for m < W - 1 (zero without one), x at step m - (W - 1).
 template <typename Elem, int W>
-__device__ __forceinline__ Elem place(const ConvParams& p, const Elem* xrow, int b, int d, int64_t m) {
+__device__ __forceinline__ Elem place(const ConvParams& p, const Elem* xrow, int64_t row, int64_t m) {
   if (m >= W - 1) return xrow[(m - (W - 1)) * p.xt];
   if (!p.initial) return Elem(0);
-  return static_cast<const Elem*>(p.initial)[(int64_t(b) * p.dim + d) * (W - 1) + m];
+  return static_cast<const Elem*>(p.initial)[row * (W - 1) + m];
 }
 
 // The last W - 1 inputs before the row's end (one lane per row).
 template <typename Elem, int W>
-__device__ __forceinline__ void store_final(const ConvParams& p, const Elem* xrow, int b, int d, int len) {
-  Elem* f = static_cast<Elem*>(p.final_state) + (int64_t(b) * p.dim + d) * (W - 1);
+__device__ __forceinline__ void store_final(const ConvParams& p, const Elem* xrow, int64_t row, uint32_t len) {
+  Elem* f = static_cast<Elem*>(p.final_state) + row * (W - 1);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) f[k] = place<Elem, W>(p, xrow, b, d, int64_t(len) + k);
+  for (int k = 0; k < W - 1; ++k) f[k] = place<Elem, W>(p, xrow, row, int64_t(len) + k);
 }
 
-// e[i] = the input of step t0 - (W - 1) + i, i < W - 1, from memory (a block's left edge).
+// e[0 .. W - 2] of a row's first steps.
 template <typename Elem, int W, int E>
-__device__ __forceinline__ void load_left(const ConvParams& p, const Elem* xrow, int b, int d, int t0,
-                                          int len, float (&e)[E]) {
+__device__ __forceinline__ void load_initial(const ConvParams& p, int64_t row, float (&e)[E]) {
 #pragma unroll
-  for (int i = 0; i < W - 1; ++i) {
-    const int64_t m = int64_t(t0) + i;
-    e[i] = m < int64_t(len) + W - 1 ? widen<Elem>(place<Elem, W>(p, xrow, b, d, m)) : 0.0f;
-  }
+  for (int i = 0; i < W - 1; ++i)
+    e[i] = p.initial ? widen<Elem>(static_cast<const Elem*>(p.initial)[row * (W - 1) + i]) : 0.0f;
+}
+
+// e[0 .. W - 2] of a block that starts at step t0 > 0 of a row of contiguous steps (t0 >= 4).
+template <typename Elem, int W, int E>
+__device__ __forceinline__ void load_left(const Elem* xrow, uint32_t t0, uint32_t len, float (&e)[E]) {
+  float v[4];
+  load_few<Elem, 4>(xrow + t0 - 4, steps_left(len, t0 - 4), v);
+#pragma unroll
+  for (int i = 0; i < W - 1; ++i) e[i] = v[4 - (W - 1) + i];
 }
 
 template <int W, int E>
@@ -98,86 +116,218 @@ __device__ __forceinline__ float window(const float (&w)[W], float bias, const f
   return acc;
 }
 
-// ---------------------------------------------------------------- forward, time order
-
-template <typename Elem, int W>
-__global__ __launch_bounds__(kThreads) void conv_fwd_time(ConvParams p) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t wave = blockIdx.x * kConvWaves + (threadIdx.x >> 6);
-  if (wave >= p.waves) return;
-  const uint32_t group = wave / p.tiles, tile = wave - group * p.tiles;
-  const int lanes = 1 << p.lanes_log2;
-  const int j = lane & (lanes - 1);
-  const int64_t row = (int64_t(group) << (6 - p.lanes_log2)) + (lane >> p.lanes_log2);
-  if (row >= int64_t(p.batch) * p.dim) return;
-  const int b = int(uint32_t(row) / uint32_t(p.dim)), d = int(row - int64_t(b) * p.dim);
-  const int len = row_length(p, b);
-  const Elem* xrow = static_cast<const Elem*>(p.x) + b * p.xb + d * p.xc;
-  const int64_t t0 = (int64_t(tile) * lanes + j) * S;
-  float w[W], bias, e[S + W - 1], own[S];
-  load_weights<W>(p, d, w, bias);
-  load_run<Elem, S>(xrow + t0, t0 < len ? int(len - t0) : 0, own);
+// The S outputs of a block, zeros from the n-th on.
+template <int W>
+__device__ __forceinline__ void conv_block(const float (&w)[W], float bias, bool silu,
+                                           const float (&e)[S + W - 1], int n, float (&o)[S]) {
 #pragma unroll
-  for (int i = 0; i < S; ++i) e[W - 1 + i] = own[i];
-  // The left edge is the last steps of the lane before (of the same row, so active too).
+  for (int i = 0; i < S; ++i) o[i] = window<W>(w, bias, e, i);
+  if (silu) {
 #pragma unroll
-  for (int i = 0; i < W - 1; ++i) e[i] = shift_up_one(own[S - (W - 1) + i], 0.0f);
-  if (j == 0 && t0 < p.seqlen) load_left<Elem, W>(p, xrow, b, d, int(t0), len, e);
-  if (t0 < p.seqlen) {
-    float o[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      float v = window<W>(w, bias, e, i);
-      if (p.silu) v = silu_f(v);
-      o[i] = t0 + i < len ? v : 0.0f;
-    }
-    Elem* orow = static_cast<Elem*>(p.out) + row * p.seqlen;
-    store_run<Elem, S>(orow + t0, int(p.seqlen - t0 < S ? p.seqlen - t0 : S), o);
+    for (int i = 0; i < S; ++i) o[i] = silu_f(o[i]);
   }
-  if (p.final_state && tile == 0 && j == 0) store_final<Elem, W>(p, xrow, b, d, len);
+  if (n < S) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) o[i] = i < n ? o[i] : 0.0f;
+  }
 }
 
-// ---------------------------------------------------------------- forward, channel order
+// Where a lane of the time-ordered kernels is: 2^lanes_log2 lanes along a row.
+struct TimeLane {
+  uint32_t d, run, j;
+  bool live;
+};
+
+__device__ __forceinline__ TimeLane time_lane(const ConvParams& p) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * kConvWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t group = wave / p.tiles;
+  TimeLane a;
+  a.run = wave - group * p.tiles;
+  a.j = lane & ((1u << p.lanes_log2) - 1);
+  a.d = (group << (6 - p.lanes_log2)) + (lane >> p.lanes_log2);
+  a.live = wave < p.waves && a.d < p.dim;
+  return a;
+}
+
+// ---------------------------------------------------------------- forward, time order
+
+// A wave takes T consecutive tiles of its rows, their loads in flight together.
+template <typename Elem, int W, int T>
+__global__ __launch_bounds__(kThreads) void conv_fwd_time(ConvParams p) {
+  const TimeLane a = time_lane(p);
+  if (!a.live) return;
+  const int b = blockIdx.y;
+  const int64_t row = int64_t(b) * p.dim + a.d;
+  const uint32_t len = row_length(p, b);
+  const Elem* xrow = static_cast<const Elem*>(p.x) + b * p.xb + a.d * p.xc;
+  Elem* orow = static_cast<Elem*>(p.out) + row * p.seqlen;
+  const uint32_t step = uint32_t(S) << p.lanes_log2, start = a.run * T * step + a.j * S;
+  float w[W], bias, e[T][S + W - 1];
+#pragma unroll
+  for (int q = 0; q < T; ++q) {
+    const uint32_t t0 = start + q * step;
+    float own[S];
+    load_run<Elem, S>(xrow + t0, steps_left(len, t0), own);
+#pragma unroll
+    for (int i = 0; i < S; ++i) e[q][W - 1 + i] = own[i];
+  }
+  load_weights<W>(p, a.d, w, bias);
+#pragma unroll
+  for (int q = 0; q < T; ++q) {
+    const uint32_t t0 = start + q * step;
+    // The left edge is the last steps of the lane before (of the same row, so active too).
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) e[q][i] = shift_up_one(e[q][S + i], 0.0f);
+    if (a.j == 0) {
+      if (t0 == 0)
+        load_initial<Elem, W>(p, row, e[q]);
+      else
+        load_left<Elem, W>(xrow, t0, len, e[q]);
+    }
+    float o[S];
+    conv_block<W>(w, bias, p.silu, e[q], steps_left(len, t0), o);
+    store_run_stream<Elem, S>(orow + t0, steps_left(p.seqlen, t0), o);
+  }
+  if (p.final_state && a.run == 0 && a.j == 0) store_final<Elem, W>(p, xrow, row, len);
+}
+
+// ---------------------------------------------------------------- channel order
+
+// Words of the steps t .. t + N - 1, of nc channels from p's on. A step outside the sequence
+// takes the nearest one's word, so that the loads need no branch: the callers replace what lies
+// before the first step by the initial state and let nothing at or behind a row's end count.
+template <typename Elem, int CV>
+using Word = Dwords<CV * int(sizeof(Elem)) / 4>;
+
+template <typename Elem, int CV, int N>
+__device__ __forceinline__ void load_rows(const Elem* p, int64_t pitch, int64_t t, uint32_t seqlen, int nc,
+                                          Word<Elem, CV> (&raw)[N]) {
+  const Elem* at[N];
+  if (t >= 0 && t + N <= seqlen) {
+    at[0] = p + t * pitch;
+#pragma unroll
+    for (int i = 1; i < N; ++i) at[i] = at[i - 1] + pitch;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      at[i] = p + (t + i < 0 ? 0 : t + i >= seqlen ? int64_t(seqlen) - 1 : t + i) * pitch;
+  }
+  if (nc >= CV) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const Word<Elem, CV>*>(at[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[CV];
+      load_few<Elem, CV>(at[i], nc, v);
+      pack_few<Elem, CV>(v, raw[i]);
+    }
+  }
+}
+
+// Where a lane of the channel-ordered kernels is: CG lanes along channels, TB along time; a
+// workgroup's waves along time.
+template <int kCV>
+struct ChanLane {
+  static constexpr int CV = kCV;  // channels per lane
+  static constexpr int CG = CW / CV;
+  static constexpr int TB = 64 / CG;
+  uint32_t tile, cb, cl, c0, t0;
+  int b, wv, tb, nc;
+};
+
+template <int CV, bool kXcdOrder>
+__device__ __forceinline__ ChanLane<CV> chan_lane(const ConvParams& p) {
+  using L = ChanLane<CV>;
+  const int lane = threadIdx.x & 63;
+  L a;
+  a.wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  a.tb = lane / L::CG;
+  uint32_t in_row = blockIdx.x;
+  a.b = blockIdx.y;
+  if constexpr (kXcdOrder) {
+    const uint32_t id = xcd_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+    a.b = int(id / gridDim.x);
+    in_row = id - a.b * gridDim.x;
+  }
+  a.cb = in_row / p.tiles;
+  a.tile = in_row - a.cb * p.tiles;
+  a.cl = (lane % L::CG) * L::CV;
+  a.c0 = a.cb * CW + a.cl;
+  a.t0 = ((a.tile * kConvWaves + a.wv) * L::TB + a.tb) * S;
+  a.nc = a.c0 < p.dim ? int(p.dim - a.c0) : 0;  // channels from c0 on
+  return a;
+}
+
+// The weights and biases of the workgroup's channels, through LDS: every lane needs its
+// channels' in turn, and a load from memory for each would be waited for each time. They are
+// loaded ahead of the block's inputs (loads complete in order), so the barrier does not wait
+// for those.
+template <int W>
+struct Weights {
+  static constexpr int kPer = (CW * (W + 1) + kThreads - 1) / kThreads;
+  float v[kPer];
+  __device__ __forceinline__ void load(const ConvParams& p, uint32_t cb) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int i = threadIdx.x + q * kThreads;  // the weights, then the biases
+      const int64_t at = i < CW * W ? int64_t(cb) * CW * W + i : int64_t(cb) * CW + (i - CW * W);
+      v[q] = 0.0f;
+      if (i < CW * W) {
+        if (at < int64_t(p.dim) * W) v[q] = p.weight[at];
+      } else if (i < CW * (W + 1) && p.bias && at < p.dim) {
+        v[q] = p.bias[at];
+      }
+    }
+  }
+  __device__ __forceinline__ void stage(float (&s)[CW * (W + 1)]) const {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (threadIdx.x + q * kThreads < CW * (W + 1)) s[threadIdx.x + q * kThreads] = v[q];
+    __syncthreads();
+  }
+  // Channel c of the workgroup's.
+  static __device__ __forceinline__ void of(const float (&s)[CW * (W + 1)], int c, float (&w)[W], float& bias) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = s[c * W + k];
+    bias = s[CW * W + c];
+  }
+};
 
 template <typename Elem, int W>
 __global__ __launch_bounds__(kThreads) void conv_fwd_chan(ConvParams p) {
-  constexpr int CV = Vec<Elem>::kN;        // channels per lane
-  constexpr int CG = 64 / CV;              // lanes along channels: 64 channels
-  constexpr int TB = 64 / CG;              // lanes along time
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles;
-  const uint32_t cb = rest % p.cblocks;
-  const int b = int(rest / p.cblocks);
-  const int c0 = int(cb) * 64 + (lane % CG) * CV;
-  const int64_t t0 = ((int64_t(tile) * kConvWaves + wv) * TB + lane / CG) * S;
-  const int nc = p.dim - c0;  // channels from c0 on
-  if (nc <= 0 || t0 >= p.seqlen) return;
-  const int len = row_length(p, b);
-  const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + c0;
-  uint4 raw[S + W - 1];
-#pragma unroll
-  for (int i = 0; i < S + W - 1; ++i) {
-    const int64_t t = t0 - (W - 1) + i;
-    raw[i] = t >= 0 && t < len ? load_word_n<Elem>(xb + t * p.xt, nc) : make_uint4(0, 0, 0, 0);
-  }
+  constexpr int CV = kConvLaneChannels;
+  __shared__ float sw[CW * (W + 1)];
+  const ChanLane<CV> a = chan_lane<CV, false>(p);
+  Weights<W> weights;
+  weights.load(p, a.cb);
+  const int b = a.b;
+  const bool live = a.nc > 0 && a.t0 < p.seqlen;
+  const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + a.c0;
+  const uint32_t len = row_length(p, b);
+  Word<Elem, CV> raw[S + W - 1];
+  if (live) load_rows<Elem, CV, S + W - 1>(xb, p.xt, int64_t(a.t0) - (W - 1), p.seqlen, a.nc, raw);
+  weights.stage(sw);
+  if (!live) return;
+  const int n = steps_left(len, a.t0), all = steps_left(p.seqlen, a.t0);
+  const int64_t row0 = int64_t(b) * p.dim + a.c0;
+  Elem* orow = static_cast<Elem*>(p.out) + row0 * p.seqlen + a.t0;
+  const bool first = a.tile == 0 && a.wv == 0;  // of the wave; its lanes of tb 0 start the row
 #pragma unroll
   for (int c = 0; c < CV; ++c) {
-    if (c >= nc) break;
-    const int d = c0 + c;
     float w[W], bias, e[S + W - 1], o[S];
-    load_weights<W>(p, d, w, bias);
+    Weights<W>::of(sw, a.cl + c, w, bias);
 #pragma unroll
-    for (int i = 0; i < S + W - 1; ++i) e[i] = word_elem<Elem>(raw[i], c);
-    if (t0 == 0) load_left<Elem, W>(p, xb + c, b, d, 0, len, e);
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      float v = window<W>(w, bias, e, i);
-      if (p.silu) v = silu_f(v);
-      o[i] = t0 + i < len ? v : 0.0f;
-    }
-    Elem* orow = static_cast<Elem*>(p.out) + (int64_t(b) * p.dim + d) * p.seqlen;
-    store_run<Elem, S>(orow + t0, int(p.seqlen - t0 < S ? p.seqlen - t0 : S), o);
-    if (p.final_state && t0 == 0) store_final<Elem, W>(p, xb + c, b, d, len);
+    for (int i = 0; i < S + W - 1; ++i) e[i] = few_elem<Elem>(raw[i], c);
+    if (first && a.tb == 0 && c < a.nc) load_initial<Elem, W>(p, row0 + c, e);
+    conv_block<W>(w, bias, p.silu, e, n, o);
+    if (c < a.nc) store_run_stream<Elem, S>(orow, all, o);
+    orow += p.seqlen;
+  }
+  if (p.final_state && first && a.tb == 0) {
+    for (int c = 0; c < CV; ++c)
+      if (c < a.nc) store_final<Elem, W>(p, xb + c, row0 + c, len);
   }
 }
 
@@ -198,8 +348,11 @@ __device__ __forceinline__ void conv_grad_block(const float (&w)[W], float bias,
                                                 float (&dw)[W + 1]) {
   float dp[S + W - 1];
 #pragma unroll
-  for (int i = 0; i < S + W - 1; ++i)
-    dp[i] = silu ? g[i] * silu_grad_f(window<W>(w, bias, e, i)) : g[i];
+  for (int i = 0; i < S + W - 1; ++i) dp[i] = g[i];
+  if (silu) {
+#pragma unroll
+    for (int i = 0; i < S + W - 1; ++i) dp[i] *= silu_grad_f(window<W>(w, bias, e, i));
+  }
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     float a = 0.0f;
@@ -214,14 +367,34 @@ __device__ __forceinline__ void conv_grad_block(const float (&w)[W], float bias,
 
 // dfinal's share of the gradient of place m of e (final_state[k] is place len + k).
 template <typename Elem, int W>
-__device__ __forceinline__ float dfinal_at(const ConvParams& p, int64_t row, int len, int64_t m) {
+__device__ __forceinline__ float dfinal_at(const ConvParams& p, int64_t row, uint32_t len, int64_t m) {
   if (!p.dfinal || m < len || m >= int64_t(len) + W - 1) return 0.0f;
   return widen<Elem>(static_cast<const Elem*>(p.dfinal)[row * (W - 1) + (m - len)]);
 }
 
+// dfinal's share of dx of the S steps from t0 on.
 template <typename Elem, int W>
-__device__ __forceinline__ void store_dinitial(const ConvParams& p, int64_t row, int len, const float (&w)[W],
-                                               const float (&dp)[W - 1]) {
+__device__ __forceinline__ void add_dfinal(const ConvParams& p, int64_t row, uint32_t len, uint32_t t0,
+                                           float (&dx)[S]) {
+  if (t0 >= len || int64_t(t0) + S + W - 1 <= len) return;
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (t0 + i < len) dx[i] += dfinal_at<Elem, W>(p, row, len, int64_t(t0) + i + W - 1);
+}
+
+// The gradient of a row's initial state, from the row's first steps (one lane per row).
+template <typename Elem, int W>
+__device__ __forceinline__ void store_dinitial(const ConvParams& p, const Elem* xrow, const Elem* grow,
+                                               int64_t row, uint32_t len, const float (&w)[W], float bias) {
+  float e[2 * (W - 1)], dp[W - 1];
+#pragma unroll
+  for (int m = 0; m < 2 * (W - 1); ++m)
+    e[m] = m < int64_t(len) + W - 1 ? widen<Elem>(place<Elem, W>(p, xrow, row, m)) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < W - 1; ++i) {
+    dp[i] = uint32_t(i) < len ? widen<Elem>(grow[i]) : 0.0f;
+    if (p.silu) dp[i] *= silu_grad_f(window<W>(w, bias, e, i));
+  }
 #pragma unroll
   for (int m = 0; m < W - 1; ++m) {
     float a = dfinal_at<Elem, W>(p, row, len, m);
@@ -231,162 +404,182 @@ __device__ __forceinline__ void store_dinitial(const ConvParams& p, int64_t row,
   }
 }
 
-// dp of the first W - 1 steps, for dinitial.
-template <int W>
-__device__ __forceinline__ void first_dp(const float (&w)[W], float bias, bool silu,
-                                         const float (&e)[S + 2 * (W - 1)],
-                                         const float (&g)[S + W - 1], float (&dp)[W - 1]) {
-#pragma unroll
-  for (int i = 0; i < W - 1; ++i)
-    dp[i] = silu ? g[i] * silu_grad_f(window<W>(w, bias, e, i)) : g[i];
-}
-
 // Time order: a wave walks kConvBwdTiles tiles of its rows (lanes along time, as the forward).
 template <typename Elem, int W>
 __global__ __launch_bounds__(kThreads) void conv_bwd_time(ConvParams p) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t wave = blockIdx.x * kConvWaves + (threadIdx.x >> 6);
-  if (wave >= p.waves) return;
-  const uint32_t group = wave / p.tiles, run = wave - group * p.tiles;
-  const int lanes = 1 << p.lanes_log2;
-  const int j = lane & (lanes - 1);
-  const int64_t row = (int64_t(group) << (6 - p.lanes_log2)) + (lane >> p.lanes_log2);
-  const bool live = row < int64_t(p.batch) * p.dim;
-  const int b = live ? int(uint32_t(row) / uint32_t(p.dim)) : 0;
-  const int d = live ? int(row - int64_t(b) * p.dim) : 0;
-  const int len = live ? row_length(p, b) : 0;
+  const TimeLane a = time_lane(p);
+  const int b = blockIdx.y;
+  const int64_t row = int64_t(b) * p.dim + (a.live ? a.d : 0);
+  const uint32_t d = a.live ? a.d : 0;
+  const uint32_t len = row_length(p, b);
   const Elem* xrow = static_cast<const Elem*>(p.x) + b * p.xb + d * p.xc;
-  const Elem* grow = static_cast<const Elem*>(p.dout) + (live ? row : 0) * p.seqlen;
+  const Elem* grow = static_cast<const Elem*>(p.dout) + row * p.seqlen;
   Elem* dxrow = static_cast<Elem*>(p.dx) + b * p.dxb + d * p.dxc;
+  const uint32_t step = uint32_t(S) << p.lanes_log2, start = a.run * kConvBwdTiles * step + a.j * S;
   float w[W], bias, dw[W + 1];
   load_weights<W>(p, d, w, bias);
 #pragma unroll
   for (int k = 0; k <= W; ++k) dw[k] = 0.0f;
-  for (int q = 0; q < kConvBwdTiles; ++q) {
-    const int64_t t0 = ((int64_t(run) * kConvBwdTiles + q) * lanes + j) * S;
-    if (!live || (t0 >= p.seqlen && t0 > 0)) break;  // (an empty row still has its states)
-    float e[S + 2 * (W - 1)], g[S + W - 1], own[S], dx[S];
-    const int n = t0 < len ? int(len - t0 < 2 * S ? len - t0 : 2 * S) : 0;  // steps from t0 on
-    load_run<Elem, S>(xrow + t0, n, own);
+  if (a.live) {
+    for (int q = 0; q < kConvBwdTiles; ++q) {
+      const uint32_t t0 = start + q * step;
+      if (t0 >= p.seqlen) break;
+      float e[S + 2 * (W - 1)], g[S + W - 1], own[S], next[4], dx[S];
+      const int n = steps_left(len, t0);
+      load_run<Elem, S>(xrow + t0, n, own);
 #pragma unroll
-    for (int i = 0; i < S; ++i) e[W - 1 + i] = own[i];
-    load_left<Elem, W>(p, xrow, b, d, int(t0), len, e);
-    load_run<Elem, S>(grow + t0, n, own);
+      for (int i = 0; i < S; ++i) e[W - 1 + i] = own[i];
+      load_run<Elem, S>(grow + t0, n, own);
 #pragma unroll
-    for (int i = 0; i < S; ++i) g[i] = own[i];
+      for (int i = 0; i < S; ++i) g[i] = own[i];
+      load_few<Elem, 4>(xrow + t0 + S, n - S, next);
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) {
-      e[W - 1 + S + i] = S + i < n ? widen<Elem>(xrow[t0 + S + i]) : 0.0f;
-      g[S + i] = S + i < n ? widen<Elem>(grow[t0 + S + i]) : 0.0f;
+      for (int i = 0; i < W - 1; ++i) e[W - 1 + S + i] = next[i];
+      load_few<Elem, 4>(grow + t0 + S, n - S, next);
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) g[S + i] = next[i];
+      if (t0 == 0)
+        load_initial<Elem, W>(p, row, e);
+      else
+        load_left<Elem, W>(xrow, t0, len, e);
+      conv_grad_block<W>(w, bias, p.silu, e, g, dx, dw);
+      if (p.dfinal) add_dfinal<Elem, W>(p, row, len, t0, dx);
+      store_run_stream<Elem, S>(dxrow + t0, steps_left(p.seqlen, t0), dx);
     }
-    conv_grad_block<W>(w, bias, p.silu, e, g, dx, dw);
-    if (t0 == 0 && p.dinitial) {
-      float dp[W - 1];
-      first_dp<W>(w, bias, p.silu, e, g, dp);
-      store_dinitial<Elem, W>(p, row, len, w, dp);
-    }
-    if (p.dfinal && t0 + S + W - 1 > len && t0 < len) {
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-        if (t0 + i < len) dx[i] += dfinal_at<Elem, W>(p, row, len, t0 + i + W - 1);
-    }
-    store_run<Elem, S>(dxrow + t0, int(p.seqlen - t0 < S ? p.seqlen - t0 : S), dx);
+    if (p.dinitial && a.run == 0 && a.j == 0) store_dinitial<Elem, W>(p, xrow, grow, row, len, w, bias);
   }
   // Sum over the row's lanes, then one store per row.
-  for (int m = lanes >> 1; m > 0; m >>= 1)
+  for (int m = 1 << p.lanes_log2 >> 1; m > 0; m >>= 1)
 #pragma unroll
     for (int k = 0; k <= W; ++k) dw[k] += __shfl_xor(dw[k], m, 64);
-  if (live && j == 0) {
-    float* part = p.part + ((int64_t(b) * p.tiles + run) * p.dim + d) * (W + 1);
+  if (a.live && a.j == 0) {
+    float* part = p.part + ((int64_t(b) * p.tiles + a.run) * p.dim + d) * (W + 1);
 #pragma unroll
     for (int k = 0; k <= W; ++k) part[k] = dw[k];
   }
 }
 
-// Channel order: as the forward; the lanes' sums meet in LDS.
-template <typename Elem, int W>
-__global__ __launch_bounds__(kThreads) void conv_bwd_chan(ConvParams p) {
-  constexpr int CV = Vec<Elem>::kN;
-  constexpr int CG = 64 / CV;
-  constexpr int TB = 64 / CG;
-  constexpr int K = W + 1;
-  __shared__ float sums[kConvWaves * TB][64 * K + 1];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const uint32_t tile = blockIdx.x % p.tiles, rest = blockIdx.x / p.tiles;
-  const uint32_t cb = rest % p.cblocks;
-  const int b = int(rest / p.cblocks);
-  const int cl = (lane % CG) * CV;
-  const int c0 = int(cb) * 64 + cl;
-  const int64_t t0 = ((int64_t(tile) * kConvWaves + wv) * TB + lane / CG) * S;
-  const int nc = p.dim - c0;
-  const int len = row_length(p, b);
-  float* mine = sums[wv * TB + lane / CG] + cl * K;
-  if (nc > 0 && t0 < p.seqlen) {
-    const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + c0;
-    uint4 raw[S + 2 * (W - 1)];
-    float dxw[S][CV];
+// dx of a lane's channels by S steps, gathered channel by channel into the words of its steps
+// (bf16: two channels a dword, when the second has come).
+template <typename Elem, int CV>
+struct StepWords {
+  Word<Elem, CV> w[S];
+  float even[S];
+  __device__ __forceinline__ void put(int c, const float (&dx)[S]) {
 #pragma unroll
-    for (int i = 0; i < S + 2 * (W - 1); ++i) {
-      const int64_t t = t0 - (W - 1) + i;
-      raw[i] = t >= 0 && t < len ? load_word_n<Elem>(xb + t * p.xt, nc) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < S; ++i) {
+      if constexpr (sizeof(Elem) == 4) {
+        w[i].w[c] = __float_as_uint(dx[i]);
+      } else if (c & 1) {
+        uint32_t d = pack_bf16x2(even[i], dx[i]);
+        asm volatile("" : "+v"(d));  // now, not with the store: half the registers
+        w[i].w[c / 2] = d;
+      } else {
+        even[i] = dx[i];
+      }
     }
-    const int n = t0 < len ? int(len - t0 < 2 * S ? len - t0 : 2 * S) : 0;
+  }
+};
+
+// Channel order: as the forward, dout's words of all channels in flight with x's; the lanes'
+// sums meet in LDS.
+template <typename Elem, int W>
+__global__ __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 4 : 3) void conv_bwd_chan(ConvParams p) {
+  constexpr int CV = kConvLaneChannels, K = W + 1;
+  using L = ChanLane<CV>;
+  constexpr int kRows = kConvWaves * L::TB;  // of sums: a lane along time each
+  __shared__ float sw[CW * (W + 1)], sums[kRows][CW * K + 1];
+  const L a = chan_lane<CV, true>(p);
+  Weights<W> weights;
+  weights.load(p, a.cb);
+  const int b = a.b;
+  const bool live = a.nc > 0 && a.t0 < p.seqlen;
+  const uint32_t len = row_length(p, b);
+  const int n = live ? steps_left(len, a.t0) : 0;
+  const int64_t row0 = int64_t(b) * p.dim + a.c0;
+  const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + a.c0;
+  const Elem* gb = static_cast<const Elem*>(p.dout) + row0 * p.seqlen + a.t0;
+  Word<Elem, CV> raw[S + 2 * (W - 1)];
+  Word<Elem, S> graw[CV];
+  Word<Elem, 4> gnext[CV];
+  if (live) load_rows<Elem, CV, S + 2 * (W - 1)>(xb, p.xt, int64_t(a.t0) - (W - 1), p.seqlen, a.nc, raw);
+  const bool whole = a.nc >= CV && n >= S + 4;
+  if (whole) {
 #pragma unroll
     for (int c = 0; c < CV; ++c) {
-      float dw[K];
+      const Elem* g = gb + int64_t(c) * p.seqlen;
+      graw[c] = *reinterpret_cast<const Word<Elem, S>*>(g);
+      gnext[c] = *reinterpret_cast<const Word<Elem, 4>*>(g + S);
+    }
+  }
+  weights.stage(sw);
+  const bool first = a.tile == 0 && a.wv == 0;
+  if (live && int64_t(a.t0) + S + W - 1 > len) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) dw[k] = 0.0f;
-      if (c < nc) {
-        const int d = c0 + c;
-        const int64_t row = int64_t(b) * p.dim + d;
-        const Elem* grow = static_cast<const Elem*>(p.dout) + row * p.seqlen;
-        float w[W], bias, e[S + 2 * (W - 1)], g[S + W - 1], own[S], dx[S];
-        load_weights<W>(p, d, w, bias);
-        load_run<Elem, S>(grow + t0, n, own);
+    for (int i = 0; i < S + 2 * (W - 1); ++i)
+      if (int64_t(a.t0) - (W - 1) + i >= len) raw[i] = Word<Elem, CV>{};
+  }
+  StepWords<Elem, CV> words;
+  float* mine = sums[a.wv * L::TB + a.tb] + a.cl * K;
 #pragma unroll
-        for (int i = 0; i < S; ++i) g[i] = own[i];
+  for (int c = 0; c < CV; ++c) {
+    float dw[K];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) g[S + i] = S + i < n ? widen<Elem>(grow[t0 + S + i]) : 0.0f;
+    for (int k = 0; k < K; ++k) dw[k] = 0.0f;
+    if (live) {
+      float w[W], bias, e[S + 2 * (W - 1)], g[S + W - 1], dx[S];
+      Weights<W>::of(sw, a.cl + c, w, bias);
+      if (whole) {
 #pragma unroll
-        for (int i = 0; i < S + 2 * (W - 1); ++i) e[i] = word_elem<Elem>(raw[i], c);
-        if (t0 == 0) load_left<Elem, W>(p, xb + c, b, d, 0, len, e);
-        conv_grad_block<W>(w, bias, p.silu, e, g, dx, dw);
-        if (t0 == 0 && p.dinitial) {
-          float dp[W - 1];
-          first_dp<W>(w, bias, p.silu, e, g, dp);
-          store_dinitial<Elem, W>(p, row, len, w, dp);
-        }
-        if (p.dfinal && t0 + S + W - 1 > len && t0 < len) {
+        for (int i = 0; i < S; ++i) g[i] = few_elem<Elem>(graw[c], i);
 #pragma unroll
-          for (int i = 0; i < S; ++i)
-            if (t0 + i < len) dx[i] += dfinal_at<Elem, W>(p, row, len, t0 + i + W - 1);
-        }
-#pragma unroll
-        for (int i = 0; i < S; ++i) dxw[i][c] = dx[i];
+        for (int i = 0; i < W - 1; ++i) g[S + i] = few_elem<Elem>(gnext[c], i);
       } else {
 #pragma unroll
-        for (int i = 0; i < S; ++i) dxw[i][c] = 0.0f;
+        for (int i = 0; i < S + W - 1; ++i)
+          g[i] = c < a.nc && i < n ? widen<Elem>(gb[int64_t(c) * p.seqlen + i]) : 0.0f;
       }
 #pragma unroll
-      for (int k = 0; k < K; ++k) mine[c * K + k] = dw[k];
+      for (int i = 0; i < S + 2 * (W - 1); ++i) e[i] = few_elem<Elem>(raw[i], c);
+      if (first && a.tb == 0 && c < a.nc) load_initial<Elem, W>(p, row0 + c, e);
+      conv_grad_block<W>(w, bias, p.silu, e, g, dx, dw);
+      if (p.dfinal && c < a.nc) add_dfinal<Elem, W>(p, row0 + c, len, a.t0, dx);
+      words.put(c, dx);
     }
-    Elem* dxb = static_cast<Elem*>(p.dx) + b * p.dxb + c0;
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (t0 + i < p.seqlen) store_run<Elem, CV>(dxb + (t0 + i) * p.dxt, nc < CV ? nc : CV, dxw[i]);
-  } else {
+    for (int k = 0; k < K; ++k) mine[c * K + k] = dw[k];
+  }
+  if (live) {
+    Elem* dxb = static_cast<Elem*>(p.dx) + b * p.dxb + a.c0 + a.t0 * p.dxt;
+    if (a.nc >= CV && a.t0 + S <= p.seqlen) {
 #pragma unroll
-    for (int i = 0; i < CV * K; ++i) mine[i] = 0.0f;
+      for (int i = 0; i < S; ++i) *reinterpret_cast<Word<Elem, CV>*>(dxb + i * p.dxt) = words.w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        float v[CV];
+#pragma unroll
+        for (int c = 0; c < CV; ++c) v[c] = few_elem<Elem>(words.w[i], c);
+        if (a.t0 + i < p.seqlen) store_few<Elem, CV>(dxb + i * p.dxt, a.nc, v);
+      }
+    }
+    if (p.dinitial && first && a.tb == 0) {
+      for (int c = 0; c < CV; ++c) {
+        if (c >= a.nc) break;
+        float w[W], bias;
+        load_weights<W>(p, a.c0 + c, w, bias);
+        store_dinitial<Elem, W>(p, xb + c, gb + int64_t(c) * p.seqlen, row0 + c, len, w, bias);
+      }
+    }
   }
   __syncthreads();
-  const int cols = 64 * K;
+  constexpr int cols = CW * K;
   for (int i = threadIdx.x; i < cols; i += kThreads) {
-    float a = 0.0f;
+    float v = 0.0f;
 #pragma unroll
-    for (int r = 0; r < kConvWaves * TB; ++r) a += sums[r][i];
-    const int64_t col = int64_t(cb) * cols + i;  // (channel, k)
-    if (col < int64_t(p.dim) * K)
-      p.part[(int64_t(b) * p.tiles + tile) * p.dim * K + col] = a;
+    for (int r = 0; r < kRows; ++r) v += sums[r][i];
+    const int64_t col = int64_t(a.cb) * cols + i;  // (channel, k)
+    if (col < int64_t(p.dim) * K) p.part[(int64_t(b) * p.tiles + a.tile) * p.dim * K + col] = v;
   }
 }
 
@@ -433,48 +626,60 @@ ConvParams params_of(const ConvArgs& a) {
   p.dxt = a.dxs.step;
   p.dinitial = a.dinitial;
   p.part = a.workspace;
-  p.batch = int(a.batch);
-  p.dim = int(a.dim);
-  p.seqlen = int(a.seqlen);
+  p.dim = uint32_t(a.dim);
+  p.seqlen = uint32_t(a.seqlen);
   p.silu = a.silu ? 1 : 0;
   p.lanes_log2 = conv_row_lanes_log2(a.seqlen);
-  p.cblocks = uint32_t((a.dim + 63) / 64);
   return p;
 }
 
 // Workgroups of the time-ordered kernels, `run` steps of a row per wave.
-unsigned time_grid(const ConvArgs& a, ConvParams* p, int64_t run) {
-  const int64_t rows = a.batch * a.dim, per = int64_t(1) << (6 - p->lanes_log2);
+dim3 time_grid(const ConvArgs& a, ConvParams* p, int64_t run) {
+  const int64_t per = int64_t(1) << (6 - p->lanes_log2);
   p->tiles = a.seqlen > 0 ? uint32_t((a.seqlen + run - 1) / run) : 1;
-  p->waves = uint32_t((rows + per - 1) / per * p->tiles);
-  return (p->waves + kConvWaves - 1) / kConvWaves;
+  p->waves = uint32_t((a.dim + per - 1) / per * p->tiles);
+  return dim3((p->waves + kConvWaves - 1) / kConvWaves, unsigned(a.batch));
 }
 
-unsigned chan_grid(const ConvArgs& a, ConvParams* p) {
-  const int64_t run = conv_channel_tile_steps(a.io);
+dim3 chan_grid(const ConvArgs& a, ConvParams* p) {
+  const int64_t run = kConvChannelTileSteps;
   p->tiles = uint32_t((a.seqlen + run - 1) / run);
-  return unsigned(p->tiles) * p->cblocks * unsigned(a.batch);
+  return dim3(unsigned(p->tiles * ((a.dim + CW - 1) / CW)), unsigned(a.batch));
 }
 
+template <typename Elem, int W, int T>
+void run_fwd_time(const ConvArgs& a, ConvParams& p, hipStream_t s) {
+  const dim3 grid = time_grid(a, &p, (int64_t(S) << p.lanes_log2) * T);
+  hipLaunchKernelGGL((conv_fwd_time<Elem, W, T>), grid, dim3(kThreads), 0, s, p);
+}
+
+// Two tiles a wave in bf16 once one a wave gives twice the waves the device holds at a time:
+// half the index arithmetic, by which bf16 is bound (b4, 2304 channels, 2048 steps: 15.5 us
+// against 17.7; four tiles 17.9). One otherwise (b5, 523 channels, 777 steps: 5.2 us against
+// 5.8), and in fp32, which memory binds (1536 channels, 65536 steps: 147 us against 152).
 template <typename Elem, int W>
 void run_fwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
   if (a.order == Order::Time || a.seqlen == 0) {
-    const unsigned grid = time_grid(a, &p, int64_t(S) << p.lanes_log2);
-    hipLaunchKernelGGL((conv_fwd_time<Elem, W>), dim3(grid), dim3(kThreads), 0, s, p);
+    const int64_t tile = int64_t(S) << p.lanes_log2;
+    const int64_t waves = a.batch * a.dim * ((a.seqlen + tile - 1) / tile) >> (6 - p.lanes_log2);
+    if (sizeof(Elem) == 2 && waves >= 16384)
+      run_fwd_time<Elem, W, 2>(a, p, s);
+    else
+      run_fwd_time<Elem, W, 1>(a, p, s);
   } else {
-    const unsigned grid = chan_grid(a, &p);
-    hipLaunchKernelGGL((conv_fwd_chan<Elem, W>), dim3(grid), dim3(kThreads), 0, s, p);
+    const dim3 grid = chan_grid(a, &p);
+    hipLaunchKernelGGL((conv_fwd_chan<Elem, W>), grid, dim3(kThreads), 0, s, p);
   }
 }
 
 template <typename Elem, int W>
 void run_bwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
   if (a.order == Order::Time || a.seqlen == 0) {
-    const unsigned grid = time_grid(a, &p, (int64_t(S) << p.lanes_log2) * kConvBwdTiles);
-    hipLaunchKernelGGL((conv_bwd_time<Elem, W>), dim3(grid), dim3(kThreads), 0, s, p);
+    const dim3 grid = time_grid(a, &p, (int64_t(S) << p.lanes_log2) * kConvBwdTiles);
+    hipLaunchKernelGGL((conv_bwd_time<Elem, W>), grid, dim3(kThreads), 0, s, p);
   } else {
-    const unsigned grid = chan_grid(a, &p);
-    hipLaunchKernelGGL((conv_bwd_chan<Elem, W>), dim3(grid), dim3(kThreads), 0, s, p);
+    const dim3 grid = chan_grid(a, &p);
+    hipLaunchKernelGGL((conv_bwd_chan<Elem, W>), grid, dim3(kThreads), 0, s, p);
   }
 }
 
@@ -531,53 +736,6 @@ struct ConvStepParams {
   int64_t nslots;
   int batch, dim, silu;
 };
-
-// N dwords at element alignment.
-template <int N>
-struct __attribute__((packed, aligned(2))) Dwords {
-  uint32_t w[N];
-};
-
-// The n (of C) values from p on, the rest zero.
-template <typename Elem, int C>
-__device__ __forceinline__ void load_few(const Elem* p, int n, float (&v)[C]) {
-  constexpr int N = C * int(sizeof(Elem)) / 4;
-  if (n >= C) {
-    const Dwords<N> d = *reinterpret_cast<const Dwords<N>*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (sizeof(Elem) == 4) {
-        v[i] = __uint_as_float(d.w[i]);
-      } else {
-        v[2 * i] = bf16_lo(d.w[i]);
-        v[2 * i + 1] = bf16_hi(d.w[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
-  }
-}
-
-template <typename Elem, int C>
-__device__ __forceinline__ void store_few(Elem* p, int n, const float (&v)[C]) {
-  constexpr int N = C * int(sizeof(Elem)) / 4;
-  if (n >= C) {
-    Dwords<N> d;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (sizeof(Elem) == 4)
-        d.w[i] = __float_as_uint(v[i]);
-      else
-        d.w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    }
-    *reinterpret_cast<Dwords<N>*>(p) = d;
-  } else {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (i < n) p[i] = narrow<Elem>(v[i]);
-  }
-}
 
 template <typename Elem, int W, int R>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepParams p) {

@@ -31,6 +31,14 @@ __device__ __forceinline__ void store16_any(void* p, uint4 v) {
   *static_cast<Any16*>(p) = r;
 }
 
+// The same past L2 (non-temporal): for output that its kernel does not read again, so that the
+// inputs' lines stay and the writes drain evenly.
+__device__ __forceinline__ void store16_stream(void* p, uint4 v) {
+  typedef uint32_t word4 __attribute__((ext_vector_type(4), aligned(2)));
+  const word4 q = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(q, static_cast<word4*>(p));
+}
+
 template <typename Elem>
 __device__ __forceinline__ float widen(Elem v);
 template <>
@@ -95,6 +103,69 @@ __device__ __forceinline__ void store_run(Elem* p, int n, const float (&v)[S]) {
   }
 }
 
+template <typename Elem, int S>
+__device__ __forceinline__ void store_run_stream(Elem* p, int n, const float (&v)[S]) {
+  constexpr int N = Vec<Elem>::kN;
+  if (n >= S) {
+#pragma unroll
+    for (int q = 0; q < S / N; ++q) store16_stream(p + q * N, narrow_raw16<Elem>(v + q * N));
+  } else {
+    store_run<Elem, S>(p, n, v);
+  }
+}
+
+// N dwords at element alignment.
+template <int N>
+struct __attribute__((packed, aligned(2))) Dwords {
+  uint32_t w[N];
+};
+
+// Value c (a constant after unrolling) of storage dwords, and all of them rounded.
+template <typename Elem, int N>
+__device__ __forceinline__ float few_elem(const Dwords<N>& d, int c) {
+  if constexpr (sizeof(Elem) == 4) return __uint_as_float(d.w[c]);
+  return (c & 1) ? bf16_hi(d.w[c / 2]) : bf16_lo(d.w[c / 2]);
+}
+
+template <typename Elem, int C>
+__device__ __forceinline__ void pack_few(const float (&v)[C], Dwords<C * int(sizeof(Elem)) / 4>& d) {
+#pragma unroll
+  for (int i = 0; i < C * int(sizeof(Elem)) / 4; ++i) {
+    if constexpr (sizeof(Elem) == 4)
+      d.w[i] = __float_as_uint(v[i]);
+    else
+      d.w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  }
+}
+
+// The n (of C) values from p on, the rest zero.
+template <typename Elem, int C>
+__device__ __forceinline__ void load_few(const Elem* p, int n, float (&v)[C]) {
+  constexpr int N = C * int(sizeof(Elem)) / 4;
+  if (n >= C) {
+    const Dwords<N> d = *reinterpret_cast<const Dwords<N>*>(p);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = few_elem<Elem>(d, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
+  }
+}
+
+template <typename Elem, int C>
+__device__ __forceinline__ void store_few(Elem* p, int n, const float (&v)[C]) {
+  constexpr int N = C * int(sizeof(Elem)) / 4;
+  if (n >= C) {
+    Dwords<N> d;
+    pack_few<Elem, C>(v, d);
+    *reinterpret_cast<Dwords<N>*>(p) = d;
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < n) p[i] = narrow<Elem>(v[i]);
+  }
+}
+
 // The storage word of n <= kN elements, zeros past them.
 template <typename Elem>
 __device__ __forceinline__ uint4 load_word_n(const Elem* p, int n) {
@@ -117,6 +188,19 @@ template <>
 __device__ __forceinline__ float word_elem<uint16_t>(const uint4& w, int c) {
   const uint32_t d = c < 2 ? w.x : c < 4 ? w.y : c < 6 ? w.z : w.w;
   return (c & 1) ? bf16_hi(d) : bf16_lo(d);
+}
+
+// The first n elements of a storage word.
+template <typename Elem>
+__device__ __forceinline__ void store_word_n(Elem* p, int n, const uint4& w) {
+  constexpr int N = Vec<Elem>::kN;
+  if (n >= N) {
+    store16_any(p, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = narrow<Elem>(word_elem<Elem>(w, i));
+  }
 }
 
 // silu(p) = p sigmoid(p), and its derivative sigmoid(p) (1 + p (1 - sigmoid(p))).
@@ -148,6 +232,17 @@ __device__ __forceinline__ float sum_lanes(float v) {
   if constexpr (LG >= 5) v += __shfl_xor(v, 16, 64);
   if constexpr (LG >= 6) v += __shfl_xor(v, 32, 64);
   return v;
+}
+
+// ---------------------------------------------------------------- workgroup order
+
+// The place of this workgroup in an order that gives each of the eight XCDs, to which workgroups
+// are dealt in turn, one contiguous run: neighbours then share an L2, and an XCD whose tiles
+// would all lie at one offset of rows a power of two long (all in the same few channels of
+// its L2) gets tiles of every offset.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t total) {
+  const uint32_t per = total / 8;
+  return id < per * 8 ? (id % 8) * per + id / 8 : id;
 }
 
 // ---------------------------------------------------------------- partial rows

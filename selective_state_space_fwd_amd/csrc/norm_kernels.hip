@@ -118,18 +118,6 @@ __device__ __forceinline__ void load_square(const Tensor& x, int b, int64_t c0, 
   }
 }
 
-template <typename Elem>
-__device__ __forceinline__ void store_word_n(Elem* p, int n, const uint4& w) {
-  constexpr int N = Vec<Elem>::kN;
-  if (n >= N) {
-    store16_any(p, w);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = narrow<Elem>(word_elem<Elem>(w, i));
-  }
-}
-
 template <typename Elem, int kSteps>
 __device__ __forceinline__ void store_square(const Tensor& x, int b, int64_t c0, int64_t t0, int nc, int nt,
                                              Square<Elem, kSteps>& s) {
@@ -204,8 +192,8 @@ __device__ __forceinline__ void sum_group(float (&v)[N], int lg, float* buf) {
     for (int i = 0; i < N; ++i) v[i] += buf[(w * times + tb) * N + i];
 }
 
-// Where a workgroup's lanes are: workgroups are dealt to the eight XCDs in turn, so a run of
-// consecutive tiles, which share cache lines of the time-ordered tensors, goes to one XCD.
+// Where a workgroup's lanes are; consecutive tiles, which share cache lines of the time-ordered
+// tensors, go to one XCD.
 struct Place {
   int b, grp, tile, nt;
   int64_t t0, c0;  // first step; first channel within the group, of round 0
@@ -214,9 +202,7 @@ struct Place {
 template <typename Elem, int kSteps>
 __device__ __forceinline__ Place place_of(const NormParams& p) {
   constexpr int CV = Vec<Elem>::kN;
-  uint32_t id = blockIdx.x;
-  const uint32_t per = p.total / 8;
-  if (id < per * 8) id = (id % 8) * per + id / 8;
+  const uint32_t id = xcd_order(blockIdx.x, p.total);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Place a;
   a.tile = int(id % p.tiles);

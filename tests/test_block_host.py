@@ -86,8 +86,8 @@ def test_conv_bwd_refusals():
 
 def test_conv_workspace():
     ws = ssm.ssm_conv_bwd_workspace_bytes
-    # a row of 2048 bf16 steps: runs of 256 steps with channels contiguous (of 2048 else)
-    assert ws(4, 2304, 4, 2048, BF) == 4 * 8 * 2304 * 5 * 4
+    # a row of 2048 bf16 steps: runs of 128 steps with channels contiguous (of 2048 else)
+    assert ws(4, 2304, 4, 2048, BF) == 4 * 16 * 2304 * 5 * 4
     assert ws(3, 10, 2, 1, F32) == 3 * 10 * 3 * 4
     assert ws(3, 10, 2, 0, F32) == 3 * 10 * 3 * 4 and ws(0, 10, 2, 5, F32) == 0
     for bad in ((-1, 1, 4, 1, BF), (1, -1, 4, 1, BF), (1, 1, 4, -1, BF), (1, 1, 1, 1, BF),
