@@ -146,50 +146,61 @@ struct NormArgs {
   bool norm_first;
 };
 
-// How a launch covers the tensors: a lane holds 16 bytes of channels by `steps` steps (1 when
-// every tensor has channels contiguous, else as many steps as channels); 2^lanes_log2 lanes
-// of a wave lie along the channels of one group, the others along time; `waves` waves of a
-// workgroup along the channels, which cover the group in `blocks` rounds.
+// How a launch covers the tensors: a lane holds 16 bytes of channels by `steps` steps;
+// 2^lanes_log2 lanes of a wave lie along the channels of one group, the others along time;
+// `waves` waves of a workgroup along the channels, which cover the group in `blocks` rounds.
 struct NormShape {
   int steps, lanes_log2, waves;
   int64_t blocks, tiles;    // tiles: workgroups along time
 };
 
-// Most waves of a workgroup, forward and backward (the backward holds one tensor more).
-constexpr int kNormFwdWaves = 16;
-constexpr int kNormBwdWaves = 8;
+// Steps of a lane by storage type (Io), where some tensor has its steps contiguous.
+constexpr int kNormFwdSteps[2] = {4, 8};
+constexpr int kNormBwdSteps[2] = {4, 4};
+// Most waves of a workgroup.
+constexpr int kNormMostWaves = 16;
 
-inline NormShape norm_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel,
-                            int most_waves) {
+// Lanes along channels: all that the group has work for, then fewer, down to eight, while
+// `good` waves still cover the group and the sequence has steps for the lanes freed.
+inline NormShape norm_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, int steps, int good,
+                            int most) {
   const int64_t cv = io == Io::BF16 ? 8 : 4;
   const int64_t g = dim / groups;
   NormShape s;
-  s.steps = all_channel ? 1 : int(cv);
-  // Lanes along channels: all that the group has work for, then fewer, down to eight, while
-  // half the most waves still cover the group and the sequence has steps for the lanes freed.
+  s.steps = steps;
   int lg = 0;
   while (lg < 6 && (cv << lg) < g) ++lg;
-  while (!all_channel && lg > 3 &&
-         (g + (cv << (lg - 1)) - 1) / (cv << (lg - 1)) <= most_waves / 2 &&
-         int64_t(s.steps) * (64 >> lg) < seqlen)
+  while (steps > 1 && lg > 3 && (g + (cv << (lg - 1)) - 1) / (cv << (lg - 1)) <= good &&
+         int64_t(steps) * (64 >> lg) < seqlen)
     --lg;
   s.lanes_log2 = lg;
   const int64_t w = (g + (cv << lg) - 1) / (cv << lg);
-  s.waves = int(w < most_waves ? w : most_waves);
+  s.waves = int(w < most ? w : most);
   s.blocks = (w + s.waves - 1) / s.waves;
   const int64_t run = int64_t(s.steps) * (64 >> lg);
   s.tiles = seqlen / run + (seqlen % run != 0);
   return s;
 }
 
+// all_channel: every tensor has its channels contiguous, and a lane holds one step. Else eight
+// steps (bf16): b4, 2048 channels, 2048 steps take 19.5 us with eight waves a workgroup (100 MB:
+// 5.2 TB/s), 21.8 with four, 20.1 with sixteen, and 21.4 with four steps a lane.
+inline NormShape norm_fwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel) {
+  return norm_shape(dim, groups, seqlen, io, all_channel ? 1 : kNormFwdSteps[int(io)], 8, kNormMostWaves);
+}
+
+// The backward takes squares of channels by steps whatever the orders (a lane of one step would
+// leave a partial sum of dweight per token). With the channels contiguous throughout eight
+// waves a workgroup are best (two workgroups a CU); a tensor with steps contiguous wants more
+// steps in a workgroup, which reads 2 bytes of each of its channels per step: b4, 2048
+// channels, 2048 steps, bf16, y so ordered 51 us with eight waves, 46 with sixteen; none so
+// ordered 33 and 39.
+inline NormShape norm_bwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel) {
+  return norm_shape(dim, groups, seqlen, io, kNormBwdSteps[int(io)], all_channel ? 8 : 16, kNormMostWaves);
+}
+
 // Partial sums of dweight per channel: one per batch row and tile of steps.
 inline int64_t norm_partials(int64_t batch, const NormShape& s) { return batch * s.tiles; }
-
-// The backward takes squares of channels by steps whatever the orders (a lane of one step
-// would leave a partial sum of dweight per token).
-inline NormShape norm_bwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io) {
-  return norm_shape(dim, groups, seqlen, io, false, kNormBwdWaves);
-}
 
 int launch_norm_fwd(const NormArgs& a, void* stream);
 int launch_norm_bwd(const NormArgs& a, void* stream);

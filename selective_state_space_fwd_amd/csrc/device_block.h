@@ -120,6 +120,11 @@ struct __attribute__((packed, aligned(2))) Dwords {
   uint32_t w[N];
 };
 
+// Past L2, as store16_stream.
+__device__ __forceinline__ void store_stream(void* p, const Dwords<4>& d) {
+  store16_stream(p, make_uint4(d.w[0], d.w[1], d.w[2], d.w[3]));
+}
+
 // Value c (a constant after unrolling) of storage dwords, and all of them rounded.
 template <typename Elem, int N>
 __device__ __forceinline__ float few_elem(const Dwords<N>& d, int c) {

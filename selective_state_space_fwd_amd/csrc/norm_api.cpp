@@ -102,8 +102,9 @@ int64_t ssm_norm_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t groups,
   if (elems == 0) return 0;
   const ssm::Io io = esz == 2 ? ssm::Io::BF16 : ssm::Io::F32;
   // (one token per row: as many partial sums as rows where their strides keep them apart)
-  const int64_t n = ssm::norm_partials(batch, ssm::norm_bwd_shape(dim, groups, seqlen, io));
-  if (!mul_ok(n, dim * 4, &total)) return -1;
+  const int64_t c = ssm::norm_partials(batch, ssm::norm_bwd_shape(dim, groups, seqlen, io, true));
+  const int64_t t = ssm::norm_partials(batch, ssm::norm_bwd_shape(dim, groups, seqlen, io, false));
+  if (!mul_ok(c > t ? c : t, dim * 4, &total)) return -1;
   return total;
 }
 

@@ -39,23 +39,31 @@ struct NormParams {
   uint32_t tiles, total;
 };
 
-// The words of a lane's square, one per channel (steps within) when kSteps > 1; one word of
-// channels when kSteps is 1.
+// The words of a lane's square of CV = 16 bytes of channels by kSteps steps: one per channel, of
+// its steps, when kSteps > 1; one word of channels when kSteps is 1.
 template <typename Elem, int kSteps>
 struct Square {
   static constexpr int CV = Vec<Elem>::kN;
   static constexpr int kWords = kSteps > 1 ? CV : 1;
-  uint4 w[kWords];
+  static constexpr int kSize = kSteps > 1 ? kSteps : CV;  // elements of a word
+  using Word = Dwords<kSize * int(sizeof(Elem)) / 4>;
+  Word w[kWords];
   __device__ __forceinline__ float at(int c, int t) const {
-    return kSteps > 1 ? word_elem<Elem>(w[kSteps > 1 ? c : 0], t) : word_elem<Elem>(w[0], c);
+    return kSteps > 1 ? few_elem<Elem>(w[kSteps > 1 ? c : 0], t) : few_elem<Elem>(w[0], c);
   }
 };
 
-// Makes the compiler take the words as new: what was computed from them before (the gate's
-// exponentials, 64 values a lane) is then formed again after the reduction instead of held
-// across it, where it does not fit the registers.
-__device__ __forceinline__ void forget_word(uint4& w) {
-  asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+// Makes the compiler take the words as new, so that what was computed from them before is not
+// held across a reduction (what is to be held, the gate's sigmoids, is held by name).
+template <int N>
+__device__ __forceinline__ void forget_word(Dwords<N>& w) {
+  uint32_t v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = w.w[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) w.w[i] = v[i];
 }
 template <typename Elem, int kSteps>
 __device__ __forceinline__ void forget(Square<Elem, kSteps>& s) {
@@ -63,80 +71,108 @@ __device__ __forceinline__ void forget(Square<Elem, kSteps>& s) {
   for (int i = 0; i < Square<Elem, kSteps>::kWords; ++i) forget_word(s.w[i]);
 }
 
-// Rows and columns of the words exchanged.
-template <typename Elem>
-__device__ __forceinline__ void turn(uint4 (&w)[Vec<Elem>::kN]);
-template <>
-__device__ __forceinline__ void turn<float>(uint4 (&w)[4]) {
-  const uint4 a = w[0], b = w[1], c = w[2], d = w[3];
-  w[0] = make_uint4(a.x, b.x, c.x, d.x);
-  w[1] = make_uint4(a.y, b.y, c.y, d.y);
-  w[2] = make_uint4(a.z, b.z, c.z, d.z);
-  w[3] = make_uint4(a.w, b.w, c.w, d.w);
-}
-template <>
-__device__ __forceinline__ void turn<uint16_t>(uint4 (&w)[8]) {
-  uint32_t in[8][4], out[8][4];
+// kSteps words of CV channels turned into CV words of kSteps steps, and back.
+template <typename Elem, int kSteps>
+__device__ __forceinline__ void turn(const Dwords<4> (&rows)[kSteps], Square<Elem, kSteps>& s) {
+  constexpr int CV = Vec<Elem>::kN;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    in[i][0] = w[i].x;
-    in[i][1] = w[i].y;
-    in[i][2] = w[i].z;
-    in[i][3] = w[i].w;
+  for (int c = 0; c < CV; ++c) {
+    if constexpr (sizeof(Elem) == 4) {
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t) s.w[c].w[t] = rows[t].w[c];
+    } else {
+#pragma unroll
+      for (int q = 0; q < kSteps / 2; ++q)  // halves c of rows 2q and 2q + 1
+        s.w[c].w[q] = __builtin_amdgcn_perm(rows[2 * q + 1].w[c / 2], rows[2 * q].w[c / 2],
+                                            (c & 1) ? 0x07060302u : 0x05040100u);
+    }
   }
+}
+
+template <typename Elem, int kSteps>
+__device__ __forceinline__ void turn_back(const Square<Elem, kSteps>& s, Dwords<4> (&rows)[kSteps]) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int t = 0; t < kSteps; ++t) {
+    if constexpr (sizeof(Elem) == 4) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)  // halves c of words 2q and 2q + 1
-      out[c][q] = __builtin_amdgcn_perm(in[2 * q + 1][c / 2], in[2 * q][c / 2],
-                                        (c & 1) ? 0x07060302u : 0x05040100u);
+      for (int c = 0; c < 4; ++c) rows[t].w[c] = s.w[c].w[t];
+    } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+      for (int q = 0; q < 4; ++q)  // halves t of channels 2q and 2q + 1
+        rows[t].w[q] = __builtin_amdgcn_perm(s.w[2 * q + 1].w[t / 2], s.w[2 * q].w[t / 2],
+                                             (t & 1) ? 0x07060302u : 0x05040100u);
+    }
+  }
+}
+
+// n (of C) elements from p on as dwords, zeros past them; and back.
+template <typename Elem, int C>
+__device__ __forceinline__ void load_part(const Elem* p, int n, Dwords<C * int(sizeof(Elem)) / 4>& d) {
+  float v[C];
+  load_few<Elem, C>(p, n, v);
+  pack_few<Elem, C>(v, d);
+}
+template <typename Elem, int C>
+__device__ __forceinline__ void store_part(Elem* p, int n, const Dwords<C * int(sizeof(Elem)) / 4>& d) {
+  float v[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] = few_elem<Elem>(d, i);
+  store_few<Elem, C>(p, n, v);
 }
 
 // The square at (b, channel c0, step t0): nc channels and nt steps of it exist (<= 0: none).
-// Whole squares take straight-line 16-byte loads; the others go word by word.
+// Whole squares take straight-line loads of whole words; the others go word by word.
 template <typename Elem, int kSteps>
 __device__ __forceinline__ void load_square(const Tensor& x, int b, int64_t c0, int64_t t0, int nc, int nt,
                                             Square<Elem, kSteps>& s) {
-  constexpr int CV = Vec<Elem>::kN;
+  using Sq = Square<Elem, kSteps>;
+  constexpr int CV = Sq::CV;
   const Elem* p = static_cast<const Elem*>(x.p) + b * x.b + c0 * x.c + t0 * x.t;
   if constexpr (kSteps == 1) {
-    s.w[0] = nt > 0 ? load_word_n<Elem>(p, nc) : make_uint4(0, 0, 0, 0);
-  } else {
-    const int64_t pitch = x.chan ? x.t : x.c;  // from word to word
+    load_part<Elem, CV>(p, nt > 0 ? nc : 0, s.w[0]);
+  } else if (x.chan) {
+    Dwords<4> rows[kSteps];
     if (nc == CV && nt == kSteps) {
 #pragma unroll
-      for (int i = 0; i < CV; ++i) s.w[i] = load16_any(p + i * pitch);
+      for (int t = 0; t < kSteps; ++t) rows[t] = *reinterpret_cast<const Dwords<4>*>(p + t * x.t);
     } else {
-      const int words = x.chan ? nt : nc, n = x.chan ? nc : nt;
 #pragma unroll
-      for (int i = 0; i < CV; ++i)
-        s.w[i] = i < words ? load_word_n<Elem>(p + i * pitch, n) : make_uint4(0, 0, 0, 0);
+      for (int t = 0; t < kSteps; ++t) load_part<Elem, CV>(p + t * x.t, t < nt ? nc : 0, rows[t]);
     }
-    if (x.chan) turn<Elem>(s.w);
+    turn<Elem, kSteps>(rows, s);
+  } else if (nc == CV && nt == kSteps) {
+#pragma unroll
+    for (int c = 0; c < CV; ++c) s.w[c] = *reinterpret_cast<const typename Sq::Word*>(p + c * x.c);
+  } else {
+#pragma unroll
+    for (int c = 0; c < CV; ++c) load_part<Elem, kSteps>(p + c * x.c, c < nc ? nt : 0, s.w[c]);
   }
 }
 
 template <typename Elem, int kSteps>
 __device__ __forceinline__ void store_square(const Tensor& x, int b, int64_t c0, int64_t t0, int nc, int nt,
-                                             Square<Elem, kSteps>& s) {
-  constexpr int CV = Vec<Elem>::kN;
+                                             const Square<Elem, kSteps>& s) {
+  using Sq = Square<Elem, kSteps>;
+  constexpr int CV = Sq::CV;
   Elem* p = static_cast<Elem*>(const_cast<void*>(x.p)) + b * x.b + c0 * x.c + t0 * x.t;
   if constexpr (kSteps == 1) {
-    if (nt > 0) store_word_n<Elem>(p, nc, s.w[0]);
-  } else {
-    if (x.chan) turn<Elem>(s.w);
-    const int64_t pitch = x.chan ? x.t : x.c;
+    store_part<Elem, CV>(p, nt > 0 ? nc : 0, s.w[0]);
+  } else if (x.chan) {
+    Dwords<4> rows[kSteps];
+    turn_back<Elem, kSteps>(s, rows);
     if (nc == CV && nt == kSteps) {
 #pragma unroll
-      for (int i = 0; i < CV; ++i) store16_any(p + i * pitch, s.w[i]);
+      for (int t = 0; t < kSteps; ++t) store_stream(p + t * x.t, rows[t]);
     } else {
-      const int words = x.chan ? nt : nc, n = x.chan ? nc : nt;
 #pragma unroll
-      for (int i = 0; i < CV; ++i)
-        if (i < words) store_word_n<Elem>(p + i * pitch, n, s.w[i]);
+      for (int t = 0; t < kSteps; ++t) store_part<Elem, CV>(p + t * x.t, t < nt ? nc : 0, rows[t]);
     }
+  } else if (nc == CV && nt == kSteps) {
+#pragma unroll
+    for (int c = 0; c < CV; ++c) *reinterpret_cast<typename Sq::Word*>(p + c * x.c) = s.w[c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < CV; ++c) store_part<Elem, kSteps>(p + c * x.c, c < nc ? nt : 0, s.w[c]);
   }
 }
 
@@ -148,10 +184,10 @@ __device__ __forceinline__ void put(Square<Elem, kSteps>& s, int c, const float 
                                     float (&row)[Vec<Elem>::kN]) {
   constexpr int CV = Vec<Elem>::kN;
   if constexpr (kSteps > 1) {
-    s.w[c] = narrow_raw16<Elem>(v);
+    pack_few<Elem, kSteps>(v, s.w[c]);
   } else {
     row[c] = v[0];
-    if (c == CV - 1) s.w[0] = narrow_raw16<Elem>(row);
+    if (c == CV - 1) pack_few<Elem, CV>(row, s.w[0]);
   }
 }
 
@@ -225,39 +261,38 @@ __device__ __forceinline__ int channels_left(const NormParams& p, int64_t c0) {
 // kHeld: the group is covered in one round and stays in registers; else the rounds are read a
 // second time (groups of more than 16 waves of channels).
 template <typename Elem, int kSteps, bool kHeld, int kMode>
-__global__ __launch_bounds__(64 * kNormFwdWaves) void norm_fwd_kernel(NormParams p) {
+__global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParams p) {
   constexpr int CV = Vec<Elem>::kN;
   extern __shared__ float buf[];
   const Place a = place_of<Elem, kSteps>(p);
   const int64_t round = int64_t(blockDim.x >> 6) * (int64_t(CV) << p.lanes_log2);
   const int64_t base = int64_t(a.grp) * p.g;
   Square<Elem, kSteps> y, z;
-  float sum[kSteps];
+  float q[CV][kSteps], sum[kSteps];  // q: y s, the result but for w r
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) sum[t] = 0.0f;
-  auto read = [&](int64_t c0) {
+  auto read = [&](int64_t c0, bool add) {
     const int nc = channels_left<CV>(p, c0);
     load_square<Elem, kSteps>(p.y, a.b, base + c0, a.t0, nc, a.nt, y);
     if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p.z, a.b, base + c0, a.t0, nc, a.nt, z);
-  };
-  auto add = [&]() {
 #pragma unroll
-    for (int c = 0; c < CV; ++c)
+    for (int c = 0; c < CV; ++c) {
 #pragma unroll
       for (int t = 0; t < kSteps; ++t) {
-        float v = y.at(c, t);
-        if constexpr (kMode == kGateFirst) v *= silu_f(z.at(c, t));
-        sum[t] = __builtin_fmaf(v, v, sum[t]);
+        const float v = y.at(c, t);
+        q[c][t] = kMode == kNoGate ? v : v * silu_f(z.at(c, t));
+        const float n = kMode == kNormFirst ? v : q[c][t];
+        if (add) sum[t] = __builtin_fmaf(n, n, sum[t]);
       }
+      // A channel's words go out of use as its values come into it, if the channels are not
+      // interleaved.
+      if constexpr (kSteps > 1) __builtin_amdgcn_sched_barrier(0);
+    }
   };
   if constexpr (kHeld) {
-    read(a.c0);
-    add();
+    read(a.c0, true);
   } else {
-    for (int k = 0; k < p.blocks; ++k) {
-      read(a.c0 + k * round);
-      add();
-    }
+    for (int k = 0; k < p.blocks; ++k) read(a.c0 + k * round, true);
   }
   sum_group<kSteps>(sum, p.lanes_log2, buf);
   float r[kSteps];
@@ -277,23 +312,16 @@ __global__ __launch_bounds__(64 * kNormFwdWaves) void norm_fwd_kernel(NormParams
     for (int c = 0; c < CV; ++c) {
       float v[kSteps];
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        v[t] = y.at(c, t) * (r[t] * w[c]);
-        if constexpr (kMode != kNoGate) v[t] *= silu_f(z.at(c, t));
-      }
+      for (int t = 0; t < kSteps; ++t) v[t] = q[c][t] * (r[t] * w[c]);
       put<Elem, kSteps>(o, c, v, row);
     }
     store_square<Elem, kSteps>(p.out, a.b, base + c0, a.t0, nc, a.nt, o);
   };
   if constexpr (kHeld) {
-    if constexpr (kSteps > 1) {
-      forget<Elem, kSteps>(y);
-      if constexpr (kMode != kNoGate) forget<Elem, kSteps>(z);
-    }
     write(a.c0);
   } else {
     for (int k = 0; k < p.blocks; ++k) {
-      read(a.c0 + k * round);
+      read(a.c0 + k * round, false);
       write(a.c0 + k * round);
     }
   }
@@ -306,14 +334,14 @@ __global__ __launch_bounds__(64 * kNormFwdWaves) void norm_fwd_kernel(NormParams
 // dweight = sum over tokens of dout (s) times the normed value; per workgroup and channel
 // here, over workgroups by a second launch in a fixed order.
 template <typename Elem, int kSteps, bool kHeld, int kMode>
-__global__ __launch_bounds__(64 * kNormBwdWaves) void norm_bwd_kernel(NormParams p) {
+__global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParams p) {
   constexpr int CV = Vec<Elem>::kN;
   extern __shared__ float buf[];
   const Place a = place_of<Elem, kSteps>(p);
   const int64_t round = int64_t(blockDim.x >> 6) * (int64_t(CV) << p.lanes_log2);
   const int64_t base = int64_t(a.grp) * p.g;
   Square<Elem, kSteps> y, z, g;
-  float w[CV], sum[kSteps], r[kSteps];
+  float w[CV], sum[kSteps], r[kSteps], sigma[CV][kSteps];
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
     sum[t] = 0.0f;
@@ -333,7 +361,11 @@ __global__ __launch_bounds__(64 * kNormBwdWaves) void norm_bwd_kernel(NormParams
 #pragma unroll
       for (int t = 0; t < kSteps; ++t) {
         float v = y.at(c, t);
-        if constexpr (kMode != kNoGate) v *= silu_f(z.at(c, t));
+        if constexpr (kMode != kNoGate) {
+          const float zv = z.at(c, t), sg = sigmoid_f(zv);
+          if (kHeld) sigma[c][t] = sg;
+          v *= zv * sg;
+        }
         sum[t] = __builtin_fmaf(w[c] * g.at(c, t), v, sum[t]);
         if (kSteps > 1 && t == kSteps - 1) __builtin_amdgcn_sched_barrier(0);
       }
@@ -365,19 +397,20 @@ __global__ __launch_bounds__(64 * kNormBwdWaves) void norm_bwd_kernel(NormParams
         const float yv = y.at(c, t), gv = g.at(c, t);
         float s = 1.0f, ds = 0.0f;
         if constexpr (kMode != kNoGate) {
-          const float zv = z.at(c, t), sg = sigmoid_f(zv);
+          const float zv = z.at(c, t), sg = kHeld ? sigma[c][t] : sigmoid_f(zv);
           s = zv * sg;
-          ds = sg * __builtin_fmaf(zv, 1.0f - sg, 1.0f);
+          ds = __builtin_fmaf(s, 1.0f - sg, sg);
         }
-        dw[c] = __builtin_fmaf(gv * s, yv * r[t], dw[c]);
-        const float a1 = r[t] * (w[c] * gv);
+        const float gr = gv * r[t], v = kMode == kNoGate ? yv : yv * s;
+        dw[c] = __builtin_fmaf(gr, v, dw[c]);
         if constexpr (kMode == kNormFirst) {
+          const float a1 = w[c] * gr;
           dy[t] = __builtin_fmaf(-yv, m[t], a1 * s);
-          dz[t] = a1 * yv * ds;
+          dz[t] = a1 * (yv * ds);
         } else {
-          const float dv = __builtin_fmaf(-(yv * s), m[t], a1);
+          const float dv = __builtin_fmaf(-v, m[t], w[c] * gr);
           dy[t] = dv * s;
-          dz[t] = dv * yv * ds;
+          dz[t] = dv * (yv * ds);
         }
       }
       put<Elem, kSteps>(dys, c, dy, row_y);
@@ -460,15 +493,15 @@ NormParams params_of(const NormArgs& a, const NormShape& s) {
 
 template <typename Elem, int kSteps, bool kHeld, int kMode>
 void launch(const NormParams& p, const NormShape& s, bool backward, hipStream_t st) {
+  constexpr int io = sizeof(Elem) == 2 ? int(Io::BF16) : int(Io::F32);
   const dim3 grid(p.total), block(64 * s.waves);
   const size_t lds = size_t(s.waves) * (64 >> s.lanes_log2) * kSteps * 4;
-  if constexpr (kSteps > 1) {  // (the backward has no form of one step)
-    if (backward) {
-      hipLaunchKernelGGL((norm_bwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
-      return;
-    }
+  if constexpr (kSteps == kNormBwdSteps[io]) {
+    if (backward) hipLaunchKernelGGL((norm_bwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
   }
-  hipLaunchKernelGGL((norm_fwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
+  if constexpr (kSteps == 1 || kSteps == kNormFwdSteps[io]) {
+    if (!backward) hipLaunchKernelGGL((norm_fwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
+  }
 }
 
 template <typename Elem, int kSteps, bool kHeld>
@@ -481,13 +514,21 @@ void run_mode(const NormParams& p, const NormShape& s, bool backward, hipStream_
     launch<Elem, kSteps, kHeld, kGateFirst>(p, s, backward, st);
 }
 
+template <typename Elem, int kSteps>
+void run_steps(const NormParams& p, const NormShape& s, bool backward, hipStream_t st) {
+  s.blocks == 1 ? run_mode<Elem, kSteps, true>(p, s, backward, st)
+                : run_mode<Elem, kSteps, false>(p, s, backward, st);
+}
+
 template <typename Elem>
 void run(const NormParams& p, const NormShape& s, bool backward, hipStream_t st) {
-  constexpr int CV = Vec<Elem>::kN;
+  constexpr int io = sizeof(Elem) == 2 ? int(Io::BF16) : int(Io::F32);
   if (s.steps == 1)
-    s.blocks == 1 ? run_mode<Elem, 1, true>(p, s, backward, st) : run_mode<Elem, 1, false>(p, s, backward, st);
+    run_steps<Elem, 1>(p, s, false, st);
+  else if (backward)
+    run_steps<Elem, kNormBwdSteps[io]>(p, s, true, st);
   else
-    s.blocks == 1 ? run_mode<Elem, CV, true>(p, s, backward, st) : run_mode<Elem, CV, false>(p, s, backward, st);
+    run_steps<Elem, kNormFwdSteps[io]>(p, s, false, st);
 }
 
 }  // namespace
@@ -495,7 +536,7 @@ void run(const NormParams& p, const NormShape& s, bool backward, hipStream_t st)
 int launch_norm_fwd(const NormArgs& a, void* stream) {
   const bool chan = a.y.order == Order::Channel && (!a.z.p || a.z.order == Order::Channel) &&
                     a.out.order == Order::Channel;
-  const NormShape s = norm_shape(a.dim, a.groups, a.seqlen, a.io, chan, kNormFwdWaves);
+  const NormShape s = norm_fwd_shape(a.dim, a.groups, a.seqlen, a.io, chan);
   const NormParams p = params_of(a, s);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.io == Io::BF16)
@@ -509,7 +550,10 @@ int launch_norm_bwd(const NormArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   int64_t rows = 0;
   if (a.batch > 0 && a.seqlen > 0) {
-    const NormShape s = norm_bwd_shape(a.dim, a.groups, a.seqlen, a.io);
+    const bool chan = a.y.order == Order::Channel && a.dout.order == Order::Channel &&
+                      a.dy.order == Order::Channel &&
+                      (!a.z.p || (a.z.order == Order::Channel && a.dz.order == Order::Channel));
+    const NormShape s = norm_bwd_shape(a.dim, a.groups, a.seqlen, a.io, chan);
     const NormParams p = params_of(a, s);
     if (a.io == Io::BF16)
       run<uint16_t>(p, s, true, st);
