@@ -28,21 +28,24 @@ on the current stream of the tensors' device, whichever device is current.
 from __future__ import annotations
 
 import ctypes
+import os
 from typing import Dict, Optional, Tuple
 
 from . import (SSM_DELTA_SOFTPLUS, SSM_ERR_UNSUPPORTED, SSM_IO_BF16, SSM_IO_F32, SSM_OK,
                SsmScanError, _ptr, lib)
+from .build import BINDING_PATH
 
 SSM_CONV_SILU = 1 << 11
 SSM_NORM_BEFORE_GATE = 1 << 12
 
 _Strides = ctypes.c_int64 * 3
-_bound = None
+_bound = _binding = None
 
 
 def _lib() -> ctypes.CDLL:
-    """libssmscan.so with the argument types of the entry points below."""
-    global _bound
+    """libssmscan.so with the argument types of the entry points below, and the extension module
+    (csrc/binding.cpp) given their addresses."""
+    global _bound, _binding
     if _bound is not None:
         return _bound
     L = lib()
@@ -66,8 +69,24 @@ def _lib() -> ctypes.CDLL:
         getattr(L, name).restype = ctypes.c_int
     L.ssm_conv_bwd_workspace_bytes.restype = i64
     L.ssm_norm_bwd_workspace_bytes.restype = i64
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: build it first "
+                           "(python -m selective_state_space_fwd_amd.build)")
+    from . import _binding as module
+
+    address = lambda name: ctypes.cast(getattr(L, name), vp).value
+    module.bind(address("ssm_conv_fwd"), address("ssm_conv_step"), address("ssm_scan_step"),
+                address("ssm_ssd_step"), address("ssm_norm_fwd"), SsmScanError)
+    _binding = module
     _bound = L
     return L
+
+
+def _load():
+    """The extension module, on first use."""
+    _torch()
+    _lib()
+    return _binding
 
 
 # ------------------------------------------------------------------ raw C entry points
@@ -110,8 +129,11 @@ def ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
 
 # ------------------------------------------------------------------ checks and the call
 #
-# A decode loop makes these calls once per layer and token, so the checks are written for their
-# cost: one look at each tensor, the message formed only for one that fails, devices as ints.
+# A decode loop makes these calls once per layer and token. Where every argument is what the C ABI
+# takes as it stands, conv, conv_step, scan_step, ssd_step and norm go through csrc/binding.cpp,
+# which looks at them in C++ and returns None, having done nothing, when one is not; the checks
+# here then copy what needs copying and name what is wrong. (conv_step of 8 rows: 4.5 us a call
+# there, 8.4 here, of which the launch is 3; ssd_step 5.0 and 11.6.)
 
 def _io_flag(name, t) -> int:
     dtype = t.dtype
@@ -244,6 +266,10 @@ def conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=N
     read). Returns (out [batch, dim, seqlen] contiguous, final_state [batch, dim, width-1]: the
     last inputs of each row, the initial_state of a next call), in x's dtype.
     """
+    r = (_binding or _load()).conv(x, weight, bias, silu, initial_state, lengths, out, final_state,
+                                   return_final_state)
+    if r is not None:
+        return r
     (flags, dev, x, weight, bias, initial_state, lengths, batch, dim, width,
      seqlen) = _conv_inputs(x, weight, bias, initial_state, lengths)
     if out is None:
@@ -296,6 +322,9 @@ def conv_step(x, state, weight, bias=None, silu: bool = False, slots=None, out=N
     contiguous, x's dtype, updated in place; slots: [batch] int32, the slot of each row (None:
     row i is slot i). A row whose slot lies outside [0, nslots) gives 0 and changes nothing;
     rows naming one slot are successive tokens of it. Returns out [batch, dim]."""
+    r = (_binding or _load()).conv_step(x, state, weight, bias, silu, slots, out)
+    if r is not None:
+        return r
     torch = _torch()
     dev = _device("x", x)
     if x.dim() != 2 or state.dim() != 3:
@@ -365,6 +394,10 @@ def scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None,
     contiguous, updated in place (dstate at most 256); slots: [batch] int32, the slot of each
     row (None: row i is slot i). A row whose slot lies outside [0, nslots) gives 0 and changes
     nothing; rows naming one slot are successive tokens of it. Returns out [batch, dim]."""
+    r = (_binding or _load()).state_step(False, u, delta, A, B, C, state, D, z, delta_bias,
+                                         delta_softplus, slots, out)
+    if r is not None:
+        return r
     if A.dim() != 2:
         raise ValueError("A must be [dim, dstate]")
     return _step(_lib().ssm_scan_step, None, u, delta, A, B, C, state, D, z, delta_bias,
@@ -375,6 +408,10 @@ def ssd_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: b
              slots=None, out=None):
     """One token of the Mamba-2 recurrence (``ssd``), as ``scan_step``: x, z: [batch,
     nheads*headdim]; dt: [batch, nheads]; A, dt_bias: [nheads]; D: [nheads*headdim]."""
+    r = (_binding or _load()).state_step(True, x, dt, A, B, C, state, D, z, dt_bias, dt_softplus,
+                                         slots, out)
+    if r is not None:
+        return r
     if A.dim() != 1:
         raise ValueError("A must be [nheads]")
     heads = A.shape[0]
@@ -402,6 +439,10 @@ def _norm_inputs(y, weight, z, groups):
 
 
 def _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out, save):
+    r = (_binding or _load()).norm(y, weight, z, eps, groups, norm_before_gate, token_major, out,
+                                   save)
+    if r is not None:
+        return r
     flags, dev, y, z, weight, batch, dim, seqlen = _norm_inputs(y, weight, z, groups)
     shape = (batch, seqlen, dim) if token_major else (batch, dim, seqlen)
     if out is None:

@@ -30,6 +30,10 @@ SOURCES = ["scan_kernels.hip", "scan_short.hip", "scan_bwd.hip", "ssd_kernels.hi
 SHAPE2_LIB_PATH = os.path.join(PKG, "libssmscan_shape2.so")
 SHAPE2_SOURCES = ["scan_kernels.hip", "scan_short.hip", "scan_bwd.hip", "scan_api.cpp"]
 SHAPE2_DEFINES = ["-DSSM_BF16_K=4", "-DSSM_BF16_G=4", "-DSSM_F32_K=2", "-DSSM_F32_G=1"]
+# The short way from Python into the single-token entry points, an extension module built against
+# the installed torch (host code only).
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 
@@ -43,23 +47,45 @@ def compile_flags() -> list:
             "-fvisibility=hidden", "-Wall", "-I", INCLUDE, "-I", CSRC]
 
 
-def _link(sources, target, verbose, extra=()):
+def _compile(cmd, sources, target, verbose):
     fd, tmp = tempfile.mkstemp(prefix=os.path.basename(target) + ".", suffix=".tmp", dir=PKG)
     os.close(fd)
-    cmd = [hipcc(), *compile_flags(), *extra, "-shared", "-o", tmp, *sources]
+    cmd = [*cmd, "-shared", "-o", tmp, *sources]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, cwd=PKG, capture_output=True, text=True)
     if r.returncode != 0:
         os.unlink(tmp)
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({r.returncode}):\n{r.stderr}")
     os.replace(tmp, target)
     return target
 
 
+def _link(sources, target, verbose, extra=()):
+    return _compile([hipcc(), *compile_flags(), *extra], sources, target, verbose)
+
+
+def _build_binding(verbose: bool) -> str:
+    """_binding.so: g++ against torch's and Python's headers and torch's libraries (found in the
+    process by then: the module is imported after torch)."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"]]
+    for path in include_paths(device_type="cuda"):
+        cmd += ["-isystem", path]
+    libs = ["-L" + library_paths(device_type="cuda")[0], "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10_hip", "-lc10"]
+    return _compile(cmd, [BINDING_SOURCE, *libs], BINDING_PATH, verbose)
+
+
 def build(verbose: bool = False) -> str:
-    """Build libssmscan.so (the scan library), libssmprobe.so (the VALU probes) and
-    libssmscan_shape2.so (the test-only second launch shape)."""
+    """Build libssmscan.so (the scan library), libssmprobe.so (the VALU probes),
+    libssmscan_shape2.so (the test-only second launch shape) and _binding.so (the binding's
+    extension module)."""
+    _build_binding(verbose)
     _link([PROBE_SOURCE], PROBE_LIB_PATH, verbose)
     _link([os.path.join(CSRC, s) for s in SHAPE2_SOURCES], SHAPE2_LIB_PATH, verbose,
           SHAPE2_DEFINES)
