@@ -193,7 +193,7 @@ inline NormShape norm_fwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io 
 // leave a partial sum of dweight per token). With the channels contiguous throughout eight
 // waves a workgroup are best (two workgroups a CU); a tensor with steps contiguous wants more
 // steps in a workgroup, which reads 2 bytes of each of its channels per step: b4, 2048
-// channels, 2048 steps, bf16, y so ordered 51 us with eight waves, 46 with sixteen; none so
+// channels, 2048 steps, bf16, y so ordered 51 us with eight waves, 44 with sixteen; none so
 // ordered 33 and 39.
 inline NormShape norm_bwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel) {
   return norm_shape(dim, groups, seqlen, io, kNormBwdSteps[int(io)], all_channel ? 8 : 16, kNormMostWaves);

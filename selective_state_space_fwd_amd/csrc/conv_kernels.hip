@@ -20,7 +20,7 @@
 // around a load (23 -> 16 us, with the weights of a workgroup in LDS instead of a load per
 // channel that is waited for), index arithmetic of 32 bits (time order 20 -> 16: it was VALU
 // bound), stores past L2 (1 us). Eight channels a lane 17.7 us, sixteen-channel waves 28 us.
-// The gradient (113 MB): 34 us channel order, 28.5 us time order, of which the VALU needs 21
+// The gradient (113 MB): 32.5 us channel order, 28.5 us time order, of which the VALU needs 21
 // (a sigmoid for 11 steps of each 8); 43 us with workgroups in plain order, where an XCD's
 // tiles all lie at one offset of the 4096-byte rows and so in two of its L2's channels.
 #include <hip/hip_runtime.h>
@@ -504,12 +504,14 @@ __global__ __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 4 : 3) void conv_bwd_
   Word<Elem, 4> gnext[CV];
   if (live) load_rows<Elem, CV, S + 2 * (W - 1)>(xb, p.xt, int64_t(a.t0) - (W - 1), p.seqlen, a.nc, raw);
   const bool whole = a.nc >= CV && n >= S + 4;
+  // The steps behind a block are the next lane's first where that lies in the wave and is whole.
+  const bool last = a.tb == L::TB - 1 || n < 2 * S + 4;
   if (whole) {
 #pragma unroll
     for (int c = 0; c < CV; ++c) {
       const Elem* g = gb + int64_t(c) * p.seqlen;
       graw[c] = *reinterpret_cast<const Word<Elem, S>*>(g);
-      gnext[c] = *reinterpret_cast<const Word<Elem, 4>*>(g + S);
+      if (last) gnext[c] = *reinterpret_cast<const Word<Elem, 4>*>(g + S);
     }
   }
   weights.stage(sw);
@@ -519,6 +521,13 @@ __global__ __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 4 : 3) void conv_bwd_
     for (int i = 0; i < S + 2 * (W - 1); ++i)
       if (int64_t(a.t0) - (W - 1) + i >= len) raw[i] = Word<Elem, CV>{};
   }
+#pragma unroll
+  for (int c = 0; c < CV; ++c)
+#pragma unroll
+    for (int q = 0; q < int(sizeof(Elem)); ++q) {
+      const uint32_t v = __shfl_down(graw[c].w[q], L::CG, 64);
+      gnext[c].w[q] = last ? gnext[c].w[q] : v;
+    }
   StepWords<Elem, CV> words;
   float* mine = sums[a.wv * L::TB + a.tb] + a.cl * K;
 #pragma unroll
