@@ -75,8 +75,9 @@ def _lib() -> ctypes.CDLL:
     from . import _binding as module
 
     address = lambda name: ctypes.cast(getattr(L, name), vp).value
-    module.bind(address("ssm_conv_fwd"), address("ssm_conv_step"), address("ssm_scan_step"),
-                address("ssm_ssd_step"), address("ssm_norm_fwd"), SsmScanError)
+    module.bind(*map(address, ("ssm_conv_fwd", "ssm_conv_step", "ssm_scan_step", "ssm_ssd_step",
+                               "ssm_norm_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes",
+                               "ssm_norm_bwd", "ssm_norm_bwd_workspace_bytes")), SsmScanError)
     _binding = module
     _bound = L
     return L
@@ -130,8 +131,7 @@ def ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
 # ------------------------------------------------------------------ checks and the call
 #
 # A decode loop makes these calls once per layer and token. Where every argument is what the C ABI
-# takes as it stands, conv, conv_step, scan_step, ssd_step and norm go through csrc/binding.cpp,
-# which looks at them in C++ and returns None, having done nothing, when one is not; the checks
+# takes as it stands, the functions below go through csrc/binding.cpp, which looks at them in C++ and returns None, having done nothing, when one is not; the checks
 # here then copy what needs copying and name what is wrong. (conv_step of 8 rows: 4.5 us a call
 # there, 8.4 here, of which the launch is 3; ssd_step 5.0 and 11.6.)
 
@@ -294,6 +294,10 @@ def conv_backward(x, weight, dout, bias=None, silu: bool = False, initial_state=
     a bias), dinitial (x's dtype; by default where an initial_state is given, None else).
     Bitwise reproducible. workspace: a uint8 device tensor of at least
     ssm_conv_bwd_workspace_bytes(...) bytes, allocated here when None."""
+    r = (_binding or _load()).conv_backward(x, weight, dout, bias, silu, initial_state, lengths,
+                                            dfinal, want_dinitial, workspace)
+    if r is not None:
+        return dict(zip(("dx", "dweight", "dbias", "dinitial"), r))
     f32 = _torch().float32
     (flags, dev, x, weight, bias, initial_state, lengths, batch, dim, width,
      seqlen) = _conv_inputs(x, weight, bias, initial_state, lengths)
@@ -487,6 +491,10 @@ def norm_backward(y, weight, rstd, dout, z=None, groups: int = 1, norm_before_ga
     ``norm_train``'s; dout: of out's shape, steps or channels contiguous. Bitwise
     reproducible. workspace: a uint8 device tensor of at least
     ssm_norm_bwd_workspace_bytes(...) bytes, allocated here when None."""
+    r = (_binding or _load()).norm_backward(y, weight, rstd, dout, z, groups, norm_before_gate,
+                                            token_major, workspace)
+    if r is not None:
+        return dict(zip(("dy", "dz", "dweight"), r))
     f32 = _torch().float32
     flags, dev, y, z, weight, batch, dim, seqlen = _norm_inputs(y, weight, z, groups)
     _check_out("rstd", rstd, (batch, groups, seqlen), f32, dev)

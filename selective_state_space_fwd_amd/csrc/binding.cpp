@@ -1,6 +1,6 @@
-// The short way from Python into the entry points that a decode loop makes once per layer and
-// token (block.py: conv, conv_step, scan_step, ssd_step, norm), where marshalling through ctypes
-// takes longer than the kernels. Each function here takes the arguments of its Python
+// The short way from Python into the entry points of block.py (conv, conv_step, scan_step,
+// ssd_step, norm and the gradients), which a decode loop or a training step makes once per layer
+// and where marshalling through ctypes can take longer than the kernels. Each function here takes the arguments of its Python
 // namesake in order, and either
 //   * makes the call, when every argument is what the C ABI takes as it stands (a device tensor
 //     of the right dtype and shape, on the current device, contiguous or strided where the ABI
@@ -30,6 +30,10 @@ decltype(&ssm_conv_step) g_conv_step;
 decltype(&ssm_scan_step) g_scan_step;
 decltype(&ssm_ssd_step) g_ssd_step;
 decltype(&ssm_norm_fwd) g_norm_fwd;
+decltype(&ssm_conv_bwd) g_conv_bwd;
+decltype(&ssm_conv_bwd_workspace_bytes) g_conv_ws;
+decltype(&ssm_norm_bwd) g_norm_bwd;
+decltype(&ssm_norm_bwd_workspace_bytes) g_norm_ws;
 PyObject* g_error;  // SsmScanError
 
 // An argument as a tensor: a plain torch.Tensor, or None (`t` undefined). `ok` turns false for
@@ -118,12 +122,13 @@ PyObject* give(PyObject* own, const at::Tensor& t) {
   if (!(cond)) Py_RETURN_NONE
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses and the error class");
+  constexpr int kFunctions = 9;
+  if (n != kFunctions + 1) {
+    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses and the error class");
     return nullptr;
   }
-  void* f[5];
-  for (int i = 0; i < 5; ++i) {
+  void* f[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -132,10 +137,48 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_scan_step = reinterpret_cast<decltype(g_scan_step)>(f[2]);
   g_ssd_step = reinterpret_cast<decltype(g_ssd_step)>(f[3]);
   g_norm_fwd = reinterpret_cast<decltype(g_norm_fwd)>(f[4]);
-  Py_INCREF(a[5]);
+  g_conv_bwd = reinterpret_cast<decltype(g_conv_bwd)>(f[5]);
+  g_conv_ws = reinterpret_cast<decltype(g_conv_ws)>(f[6]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(f[7]);
+  g_norm_ws = reinterpret_cast<decltype(g_norm_ws)>(f[8]);
+  Py_INCREF(a[kFunctions]);
   Py_XDECREF(g_error);
-  g_error = a[5];
+  g_error = a[kFunctions];
   Py_RETURN_NONE;
+}
+
+// An uninitialised tensor of t's shape and contiguous axis.
+at::Tensor empty_in_order(const Arg& t) {
+  const int64_t b = t->size(0), d = t->size(1), L = t->size(2);
+  if (L <= 1 || t->stride(2) == 1) return at::empty({b, d, L}, t->options());
+  return at::empty({b, L, d}, t->options()).transpose(1, 2);
+}
+
+// A workspace of `need` bytes: the caller's, or one made here (`made_ws`). Null if neither will do.
+void* workspace_of(const Arg& ws, int64_t need, int dev, const at::Tensor& like, at::Tensor* made_ws, int64_t* bytes) {
+  if (need < 0) return nullptr;
+  if (ws) {
+    if (ws->scalar_type() != at::kByte || !ws->is_cuda() || ws->get_device() != dev || !ws->is_contiguous() ||
+        ws->numel() < need)
+      return nullptr;
+    *bytes = ws->numel();
+    return ws.mut();
+  }
+  *bytes = need > 0 ? need : 1;
+  *made_ws = at::empty({*bytes}, like.options().dtype(at::kByte));
+  return made_ws->data_ptr();
+}
+
+// A new tuple of results; an undefined tensor is None.
+PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
+  PyObject* out = PyTuple_New(Py_ssize_t(ts.size()));
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : ts) {
+    PyObject* o = t.defined() ? THPVariable_Wrap(t) : (Py_INCREF(Py_None), Py_None);
+    PyTuple_SET_ITEM(out, i++, o);
+  }
+  return out;
 }
 
 // conv(x, weight, bias, silu, initial_state, lengths, out, final_state, return_final_state)
@@ -287,6 +330,91 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// conv_backward(x, weight, dout, bias, silu, initial_state, lengths, dfinal, want_dinitial, workspace):
+// (dx, dweight, dbias or None, dinitial or None)
+PyObject* conv_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  bool ok = n == 10;
+  SSM_NEED(ok && g_conv_bwd);
+  const Arg x(a[0], &ok), w(a[1], &ok), g(a[2], &ok), bias(a[3], &ok), init(a[5], &ok), lengths(a[6], &ok),
+      dfin(a[7], &ok), ws(a[9], &ok);
+  const bool silu = flag_of(a[4], &ok), want = a[8] == Py_None ? bool(init) : flag_of(a[8], &ok);
+  SSM_NEED(ok && x && w && g && x->dim() == 3 && w->dim() == 2);
+  const int dev = device_of(x), io = io_of(x);
+  const at::ScalarType type = x->scalar_type();
+  const int64_t b = x->size(0), d = x->size(1), L = x->size(2), W = w->size(1);
+  SSM_NEED(dev >= 0 && io >= 0 && W >= 2 && ordered(x, type, dev, {b, d, L}) &&
+           dense(w, at::kFloat, dev, {d, W}) && dense(g, type, dev, {b, d, L}) &&
+           dense_or_none(bias, at::kFloat, dev, {d}) && dense_or_none(init, type, dev, {b, d, W - 1}) &&
+           dense_or_none(lengths, at::kInt, dev, {b}) && dense_or_none(dfin, type, dev, {b, d, W - 1}));
+  const uint32_t flags = uint32_t(io) | (silu ? SSM_CONV_SILU : 0);
+  at::Tensor made_ws;
+  int64_t bytes = 0;
+  void* wp = workspace_of(ws, g_conv_ws(b, d, W, L, flags), dev, *x.t, &made_ws, &bytes);
+  SSM_NEED(wp);
+  const at::Tensor dx = empty_in_order(x), dw = at::empty({d, W}, w->options());
+  const at::Tensor db = bias ? at::empty({d}, w->options()) : at::Tensor();
+  const at::Tensor di = want ? at::empty({b, d, W - 1}, x->options()) : at::Tensor();
+  const int64_t xs[3] = {x->stride(0), x->stride(1), x->stride(2)}, ds[3] = {dx.stride(0), dx.stride(1), dx.stride(2)};
+  if (!made([&] {
+        return g_conv_bwd(x.data(), xs, static_cast<const float*>(w.data()), static_cast<const float*>(bias.data()),
+                          init.data(), static_cast<const int32_t*>(lengths.data()), flags, g.data(), dfin.data(),
+                          dx.data_ptr(), ds, static_cast<float*>(dw.data_ptr()),
+                          bias ? static_cast<float*>(db.data_ptr()) : nullptr, want ? di.data_ptr() : nullptr, wp,
+                          bytes, b, d, W, L, stream_of(dev));
+      }))
+    return nullptr;
+  return tuple_of({dx, dw, db, di});
+  END_HANDLE_TH_ERRORS
+}
+
+// norm_backward(y, weight, rstd, dout, z, groups, norm_before_gate, token_major, workspace):
+// (dy, dz or None, dweight)
+PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  bool ok = n == 9;
+  SSM_NEED(ok && g_norm_bwd && PyLong_CheckExact(a[5]));
+  const Arg y(a[0], &ok), w(a[1], &ok), rstd(a[2], &ok), g(a[3], &ok), z(a[4], &ok), ws(a[8], &ok);
+  const bool first = flag_of(a[6], &ok), token = flag_of(a[7], &ok);
+  const long groups = PyLong_AsLong(a[5]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    ok = false;
+  }
+  SSM_NEED(ok && y && w && rstd && g && y->dim() == 3 && groups >= 1);
+  const int dev = device_of(y), io = io_of(y);
+  const at::ScalarType type = y->scalar_type();
+  const int64_t b = y->size(0), d = y->size(1), L = y->size(2);
+  SSM_NEED(dev >= 0 && io >= 0 && d % groups == 0 && ordered(y, type, dev, {b, d, L}) &&
+           (!z || ordered(z, type, dev, {b, d, L})) && dense(w, at::kFloat, dev, {d}) &&
+           dense(rstd, at::kFloat, dev, {b, groups, L}) &&
+           (token ? dense(g, type, dev, {b, L, d}) : dense(g, type, dev, {b, d, L})));
+  const uint32_t flags = uint32_t(io) | (first ? SSM_NORM_BEFORE_GATE : 0);
+  at::Tensor made_ws;
+  int64_t bytes = 0;
+  void* wp = workspace_of(ws, g_norm_ws(b, d, groups, L, flags), dev, *y.t, &made_ws, &bytes);
+  SSM_NEED(wp);
+  const at::Tensor dy = empty_in_order(y), dz = z ? empty_in_order(z) : at::Tensor();
+  const at::Tensor dw = at::empty({d}, w->options());
+  const int64_t ys[3] = {y->stride(0), y->stride(1), y->stride(2)}, gs[3] = {L * d, 1, d};
+  const int64_t dys[3] = {dy.stride(0), dy.stride(1), dy.stride(2)};
+  int64_t zs[3] = {0, 0, 0}, dzs[3] = {0, 0, 0};
+  if (z)
+    for (int i = 0; i < 3; ++i) {
+      zs[i] = z->stride(i);
+      dzs[i] = dz.stride(i);
+    }
+  if (!made([&] {
+        return g_norm_bwd(y.data(), ys, z.data(), z ? zs : nullptr, static_cast<const float*>(w.data()),
+                          static_cast<const float*>(rstd.data()), g.data(), token ? gs : nullptr, flags,
+                          dy.data_ptr(), dys, z ? dz.data_ptr() : nullptr, z ? dzs : nullptr,
+                          static_cast<float*>(dw.data_ptr()), wp, bytes, b, d, groups, L, stream_of(dev));
+      }))
+    return nullptr;
+  return tuple_of({dy, dz, dw});
+  END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyCFunction fast() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
@@ -297,6 +425,8 @@ PyMethodDef g_methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},
                            {"conv_step", fast<conv_step>(), METH_FASTCALL, nullptr},
                            {"state_step", fast<state_step>(), METH_FASTCALL, nullptr},
                            {"norm", fast<norm>(), METH_FASTCALL, nullptr},
+                           {"conv_backward", fast<conv_backward>(), METH_FASTCALL, nullptr},
+                           {"norm_backward", fast<norm_backward>(), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,

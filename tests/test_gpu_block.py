@@ -280,6 +280,7 @@ def test_both_ways_of_marshalling_agree(monkeypatch):
 
     class Never:
         conv = conv_step = state_step = norm = staticmethod(lambda *a: None)
+        conv_backward = norm_backward = staticmethod(lambda *a: None)
 
     r = Rand(750)
     x, w, bias = r((2, 40, 50), "bf16")[0], r((40, 4))[0], r((40,))[0]
@@ -299,14 +300,22 @@ def test_both_ways_of_marshalling_agree(monkeypatch):
                ssm.ssd_step(row, dt4, A2, B, B, st, D=D_, dt_bias=b4, dt_softplus=True), st,
                ssm.norm(tok, bias, z=x, eps=1e-3, groups=5, token_major=True),
                *ssm.norm_train(x, bias, norm_before_gate=True, z=x)]
+        for g in (ssm.conv_backward(tok, w, x, bias=bias, silu=True, initial_state=init,
+                                    lengths=lengths, dfinal=init),
+                  ssm.conv_backward(x, w, x, want_dinitial=True),
+                  ssm.norm_backward(tok, bias, got[-1], x, z=x),
+                  ssm.norm_backward(x, bias, got[-1], tok.transpose(1, 2), token_major=True)):
+            got += [v for v in g.values() if v is not None]
         return got
 
     native = calls()
     assert all(v is not None for v in (block._binding.conv(x, w, None, False, None, None, None, None, True),
-                                       block._binding.norm(x, bias, None, 1e-5, 1, False, False, None, False)))
+                                       block._binding.norm(x, bias, None, 1e-5, 1, False, False, None, False),
+                                       block._binding.conv_backward(tok, w, x, None, False, None, None, None,
+                                                                    None, None)))
     monkeypatch.setattr(block, "_binding", Never)
     for a, c in zip(native, calls()):
-        assert a.shape == c.shape and same(a.contiguous(), c.contiguous())
+        assert a.shape == c.shape and a.stride() == c.stride() and same(a.contiguous(), c.contiguous())
 
 
 def test_outputs_given_and_arguments_copied():
