@@ -23,8 +23,8 @@
  * `stream`, use no atomics (bitwise reproducible) and allocate nothing; every check happens
  * before any HIP call. Outputs must overlap no other argument (a strided array counts with its
  * whole extent). Returns SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (a storage type other
- * than fp32/bf16, neither stride 1, dim or seqlen above 2^31 - 1, more than 2^31 - 1
- * workgroups), SSM_ERR_MISALIGNED (a pointer not aligned to its element size) or SSM_ERR_HIP.
+ * than fp32/bf16, neither stride 1, dim or seqlen above 2^31 - 1, tokens times groups and
+ * 32-channel blocks above 2^31 - 1), SSM_ERR_MISALIGNED (a pointer not aligned to its element size) or SSM_ERR_HIP.
  */
 #ifndef SSM_NORM_H
 #define SSM_NORM_H
@@ -43,13 +43,21 @@ extern "C" {
 /*
  * ssm_norm_fwd -- required: y, weight, out (NULL only when empty); optional (NULL): z (no
  * gate), rstd (not returned; the backward needs it). batch, dim, seqlen >= 0; groups >= 1 and a
- * divisor of dim; eps >= 0.
+ * divisor of dim; eps >= 0. workspace: ssm_norm_fwd_workspace_bytes(batch, dim, groups, seqlen,
+ * flags) bytes (workspace_bytes, at least that), 256-byte aligned, overwritten; calls that share
+ * it must not overlap in time. Not looked at (NULL) where every tensor has channel stride 1 and
+ * a group at most 4096 channels; SSM_ERR_INVALID_ARG without it elsewhere.
  */
 SSM_API int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z,
                          const int64_t* z_strides, const float* weight, float eps,
                          uint32_t flags, void* out, const int64_t* out_strides, float* rstd,
-                         int64_t batch, int64_t dim, int64_t groups, int64_t seqlen,
-                         void* stream);
+                         void* workspace, int64_t workspace_bytes, int64_t batch, int64_t dim,
+                         int64_t groups, int64_t seqlen, void* stream);
+
+/* Bytes of workspace ssm_norm_fwd needs at most: a sum per token and block of channels. -1 as
+ * ssm_norm_bwd_workspace_bytes. */
+SSM_API int64_t ssm_norm_fwd_workspace_bytes(int64_t batch, int64_t dim, int64_t groups,
+                                             int64_t seqlen, uint32_t flags);
 
 /*
  * ssm_norm_bwd -- gradients of L = sum(dout * out): dy, dz (required when z is given),
@@ -67,7 +75,7 @@ SSM_API int ssm_norm_bwd(const void* y, const int64_t* y_strides, const void* z,
                          int64_t seqlen, void* stream);
 
 /* Bytes of workspace ssm_norm_bwd needs, whatever the strides: a partial sum of dweight per run
- * of tokens. -1 for negative sizes, groups not a divisor of dim, an unknown storage type or a
+ * of tokens and a sum per token and block of channels. -1 for negative sizes, groups not a divisor of dim, an unknown storage type or a
  * size past int64. */
 SSM_API int64_t ssm_norm_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t groups,
                                              int64_t seqlen, uint32_t flags);

@@ -55,7 +55,7 @@ EXPORTED = ("ssm_scan_fwd", "ssm_scan_strerror", "ssm_scan_abi_version",
             "ssm_ssd_workspace_bytes", "ssm_ssd_fwd", "ssm_ssd_fwd_noalloc",
             "ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes", "ssm_conv_step",
             "ssm_scan_step", "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd",
-            "ssm_norm_bwd_workspace_bytes")
+            "ssm_norm_fwd_workspace_bytes", "ssm_norm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -521,4 +521,4 @@ from .block import (SSM_CONV_SILU, SSM_NORM_BEFORE_GATE, causal_conv, conv,  # n
                     conv_backward, conv_step, gated_norm, norm, norm_backward, norm_train,
                     scan_step, ssd_step, ssm_conv_bwd, ssm_conv_bwd_workspace_bytes,
                     ssm_conv_fwd, ssm_conv_step, ssm_norm_bwd, ssm_norm_bwd_workspace_bytes,
-                    ssm_norm_fwd, ssm_scan_step, ssm_ssd_step)
+                    ssm_norm_fwd, ssm_norm_fwd_workspace_bytes, ssm_scan_step, ssm_ssd_step)

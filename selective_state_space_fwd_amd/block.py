@@ -59,8 +59,10 @@ def _lib() -> ctypes.CDLL:
                                 u32, vp, vp, i64, i64, i64, i64, vp]
     L.ssm_ssd_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp,
                                u32, vp, vp, i64, i64, i64, i64, i64, vp]
-    L.ssm_norm_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, u32, vp, vp, vp, i64, i64,
-                               i64, i64, vp]
+    L.ssm_norm_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, u32, vp, vp, vp, vp, i64, i64,
+                               i64, i64, i64, vp]
+    L.ssm_norm_fwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+    L.ssm_norm_fwd_workspace_bytes.restype = i64
     L.ssm_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp, vp,
                                i64, i64, i64, i64, i64, vp]
     L.ssm_norm_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
@@ -77,7 +79,8 @@ def _lib() -> ctypes.CDLL:
     address = lambda name: ctypes.cast(getattr(L, name), vp).value
     module.bind(*map(address, ("ssm_conv_fwd", "ssm_conv_step", "ssm_scan_step", "ssm_ssd_step",
                                "ssm_norm_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes",
-                               "ssm_norm_bwd", "ssm_norm_bwd_workspace_bytes")), SsmScanError)
+                               "ssm_norm_bwd", "ssm_norm_bwd_workspace_bytes",
+                               "ssm_norm_fwd_workspace_bytes")), SsmScanError)
     _binding = module
     _bound = L
     return L
@@ -118,6 +121,10 @@ def ssm_ssd_step(*args) -> int:
 
 def ssm_norm_fwd(*args) -> int:
     return _lib().ssm_norm_fwd(*args)
+
+
+def ssm_norm_fwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
+    return _lib().ssm_norm_fwd_workspace_bytes(batch, dim, groups, seqlen, flags)
 
 
 def ssm_norm_bwd(*args) -> int:
@@ -457,10 +464,12 @@ def _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out,
     z_ptr = z_strides = None
     if z is not None:
         z_ptr, z_strides = z.data_ptr(), _strides(z)
+    workspace = _workspace(
+        None, _lib().ssm_norm_fwd_workspace_bytes(batch, dim, groups, seqlen, flags), y)
     _run(_lib().ssm_norm_fwd, dev, y.data_ptr(), _strides(y), z_ptr, z_strides,
          weight.data_ptr(), eps, flags | (SSM_NORM_BEFORE_GATE if norm_before_gate else 0),
          out.data_ptr(), _Strides(seqlen * dim, 1, dim) if token_major else None, _ptr(rstd),
-         batch, dim, groups, seqlen)
+         workspace.data_ptr(), workspace.numel(), batch, dim, groups, seqlen)
     return out, rstd
 
 

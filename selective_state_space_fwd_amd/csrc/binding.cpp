@@ -34,6 +34,7 @@ decltype(&ssm_conv_bwd) g_conv_bwd;
 decltype(&ssm_conv_bwd_workspace_bytes) g_conv_ws;
 decltype(&ssm_norm_bwd) g_norm_bwd;
 decltype(&ssm_norm_bwd_workspace_bytes) g_norm_ws;
+decltype(&ssm_norm_fwd_workspace_bytes) g_norm_fwd_ws;
 PyObject* g_error;  // SsmScanError
 
 // An argument as a tensor: a plain torch.Tensor, or None (`t` undefined). `ok` turns false for
@@ -122,9 +123,9 @@ PyObject* give(PyObject* own, const at::Tensor& t) {
   if (!(cond)) Py_RETURN_NONE
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kFunctions = 9;
+  constexpr int kFunctions = 10;
   if (n != kFunctions + 1) {
-    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses and the error class");
+    PyErr_SetString(PyExc_TypeError, "bind takes ten addresses and the error class");
     return nullptr;
   }
   void* f[kFunctions];
@@ -141,6 +142,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_conv_ws = reinterpret_cast<decltype(g_conv_ws)>(f[6]);
   g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(f[7]);
   g_norm_ws = reinterpret_cast<decltype(g_norm_ws)>(f[8]);
+  g_norm_fwd_ws = reinterpret_cast<decltype(g_norm_fwd_ws)>(f[9]);
   Py_INCREF(a[kFunctions]);
   Py_XDECREF(g_error);
   g_error = a[kFunctions];
@@ -310,6 +312,14 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor made_out, rstd;
   if (!out) made_out = token ? at::empty({b, L, d}, y->options()) : at::empty({b, d, L}, y->options());
   if (save) rstd = at::empty({b, groups, L}, y->options().dtype(at::kFloat));
+  // (not needed, and not made, for a decode step: channels contiguous throughout)
+  at::Tensor made_ws;
+  int64_t bytes = 0;
+  void* wp = nullptr;
+  if (y->stride(1) != 1 || (z && z->stride(1) != 1) || !(token || L == 1) || d / groups > 4096) {
+    wp = workspace_of(Arg(Py_None, &ok), g_norm_fwd_ws(b, d, groups, L, uint32_t(io)), dev, *y.t, &made_ws, &bytes);
+    SSM_NEED(wp);
+  }
   void* op = out ? out.mut() : made_out.data_ptr();
   const int64_t ys[3] = {y->stride(0), y->stride(1), y->stride(2)}, os[3] = {L * d, 1, d};
   int64_t zs[3] = {0, 0, 0};
@@ -318,7 +328,8 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!made([&] {
         return g_norm_fwd(y.data(), ys, z.data(), z ? zs : nullptr, static_cast<const float*>(w.data()), float(eps),
                           uint32_t(io) | (first ? SSM_NORM_BEFORE_GATE : 0), op, token ? os : nullptr,
-                          save ? static_cast<float*>(rstd.data_ptr()) : nullptr, b, d, groups, L, stream_of(dev));
+                          save ? static_cast<float*>(rstd.data_ptr()) : nullptr, wp, bytes, b, d, groups, L,
+                          stream_of(dev));
       }))
     return nullptr;
   PyObject* o = give(a[7], made_out);

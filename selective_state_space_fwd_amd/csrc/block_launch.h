@@ -140,7 +140,8 @@ struct NormArgs {
   // backward (out unused)
   View dout, dy, dz;        // dz.p required when z is given
   float* dweight;           // [dim]
-  float* workspace;         // norm_partials(...) x dim floats
+  float* workspace;         // backward: norm_partials(...) x dim floats; then, split, the blocks'
+                            // sums: batch x groups x cblocks x seqlen floats
   int64_t batch, dim, groups, seqlen;
   Io io;
   bool norm_first;
@@ -148,55 +149,92 @@ struct NormArgs {
 
 // How a launch covers the tensors: a lane holds 16 bytes of channels by `steps` steps;
 // 2^lanes_log2 lanes of a wave lie along the channels of one group, the others along time;
-// `waves` waves of a workgroup along the channels, which cover the group in `blocks` rounds.
+// `waves` waves of a workgroup along the channels. A workgroup covers a whole group, or, split,
+// one of the group's `cblocks` blocks of channels.
 struct NormShape {
   int steps, lanes_log2, waves;
-  int64_t blocks, tiles;    // tiles: workgroups along time
+  int64_t cblocks, tiles;    // tiles: workgroups along time
+  bool split;
+};
+
+// all_channel: every tensor has its channels contiguous. dword_rows: every row of steps of the
+// others starts at a multiple of four bytes.
+struct NormOrders {
+  bool all_channel, dword_rows;
 };
 
 // Steps of a lane by storage type (Io), where some tensor has its steps contiguous.
 constexpr int kNormFwdSteps[2] = {4, 8};
 constexpr int kNormBwdSteps[2] = {4, 4};
-// Most waves of a workgroup.
+// Most waves of a workgroup; waves of a split one, and its lanes along channels (8, with 8 along
+// time).
 constexpr int kNormMostWaves = 16;
+constexpr int kNormSplitWaves = 4;
+constexpr int kNormSplitLanes = 3;
 
-// Lanes along channels: all that the group has work for, then fewer, down to eight, while
-// `good` waves still cover the group and the sequence has steps for the lanes freed.
-inline NormShape norm_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, int steps, int good,
-                            int most) {
+// A group of g channels whole. Lanes along channels: all that the group has work for, then fewer,
+// down to eight, while `good` waves still cover the group and the sequence has steps for the
+// lanes freed. More than the most waves: not to be launched.
+inline NormShape norm_whole_shape(int64_t g, int64_t seqlen, Io io, int steps, int good) {
   const int64_t cv = io == Io::BF16 ? 8 : 4;
-  const int64_t g = dim / groups;
-  NormShape s;
-  s.steps = steps;
+  NormShape s{steps, 0, 0, 1, 0, false};
   int lg = 0;
   while (lg < 6 && (cv << lg) < g) ++lg;
   while (steps > 1 && lg > 3 && (g + (cv << (lg - 1)) - 1) / (cv << (lg - 1)) <= good &&
          int64_t(steps) * (64 >> lg) < seqlen)
     --lg;
   s.lanes_log2 = lg;
-  const int64_t w = (g + (cv << lg) - 1) / (cv << lg);
-  s.waves = int(w < most ? w : most);
-  s.blocks = (w + s.waves - 1) / s.waves;
-  const int64_t run = int64_t(s.steps) * (64 >> lg);
+  const int64_t w = (g + (cv << lg) - 1) / (cv << lg), run = int64_t(steps) * (64 >> lg);
+  s.waves = int(w <= kNormMostWaves ? w : kNormMostWaves + 1);
   s.tiles = seqlen / run + (seqlen % run != 0);
   return s;
 }
 
-// all_channel: every tensor has its channels contiguous, and a lane holds one step. Else eight
-// steps (bf16): b4, 2048 channels, 2048 steps take 19.5 us with eight waves a workgroup (100 MB:
-// 5.2 TB/s), 21.8 with four, 20.1 with sixteen, and 21.4 with four steps a lane.
-inline NormShape norm_fwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel) {
-  return norm_shape(dim, groups, seqlen, io, all_channel ? 1 : kNormFwdSteps[int(io)], 8, kNormMostWaves);
+inline NormShape norm_split_shape(int64_t g, int64_t seqlen, Io io, int steps) {
+  const int64_t cv = io == Io::BF16 ? 8 : 4, wave = cv << kNormSplitLanes;
+  const int64_t run = int64_t(steps) * (64 >> kNormSplitLanes), w = (g + wave - 1) / wave;
+  NormShape s{steps, kNormSplitLanes, int(w < kNormSplitWaves ? w : kNormSplitWaves), 0, 0, true};
+  s.cblocks = (w + s.waves - 1) / s.waves;
+  s.tiles = seqlen / run + (seqlen % run != 0);
+  return s;
+}
+
+// Bytes that a workgroup reads on end of a channel whose steps are contiguous.
+inline int64_t norm_run_bytes(const NormShape& s, Io io) {
+  return int64_t(s.steps) * (64 >> s.lanes_log2) * (io == Io::BF16 ? 2 : 4);
+}
+
+// all_channel: a lane holds one step. Else eight steps (bf16): b4, 2048 channels, 2048 steps
+// take 19.5 us with eight waves a workgroup (100 MB: 5.2 TB/s), 21.8 with four, 20.1 with
+// sixteen, and 21.4 with four steps a lane. Split where a group does not fit, and where a
+// workgroup would read 16 bytes on end at odd addresses: b1, 5691 channels, 773 steps, all
+// tensors so ordered, take 58 us whole and 32 split (776 steps: 24 and 23; b4, 2048 channels,
+// 2048 steps: 20 and 33).
+inline NormShape norm_fwd_shape(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, Io io,
+                                NormOrders o) {
+  const int steps = kNormFwdSteps[int(io)];
+  const NormShape s = norm_whole_shape(dim / groups, seqlen, io, o.all_channel ? 1 : steps, 8);
+  const bool split = s.waves > kNormMostWaves ||
+                     (!o.all_channel && !o.dword_rows && norm_run_bytes(s, io) < 32 && seqlen > steps);
+  return split ? norm_split_shape(dim / groups, seqlen, io, steps) : s;
 }
 
 // The backward takes squares of channels by steps whatever the orders (a lane of one step would
 // leave a partial sum of dweight per token). With the channels contiguous throughout eight
 // waves a workgroup are best (two workgroups a CU); a tensor with steps contiguous wants more
-// steps in a workgroup, which reads 2 bytes of each of its channels per step: b4, 2048
-// channels, 2048 steps, bf16, y so ordered 51 us with eight waves, 44 with sixteen; none so
-// ordered 33 and 39.
-inline NormShape norm_bwd_shape(int64_t dim, int64_t groups, int64_t seqlen, Io io, bool all_channel) {
-  return norm_shape(dim, groups, seqlen, io, kNormBwdSteps[int(io)], all_channel ? 8 : 16, kNormMostWaves);
+// steps in a workgroup: b4, 2048 channels, 2048 steps, bf16, y so ordered 51 us with eight
+// waves, 44 with sixteen; none so ordered 33 and 39. Split where such a tensor's channels would
+// be read by less than 32 bytes on end (b1, 2722 channels, 2920 steps: 46 us whole, 40 split;
+// b8, 8192 channels, 512 steps: 141 and 105; b4, 2048 channels, 2048 steps: 41 and 53), or the
+// workgroups are a quarter of the CUs (b1, 2048 channels, 512 steps: 16.5 and 14.2).
+inline NormShape norm_bwd_shape(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, Io io,
+                                NormOrders o) {
+  const int steps = kNormBwdSteps[int(io)];
+  const NormShape s = norm_whole_shape(dim / groups, seqlen, io, steps, o.all_channel ? 8 : 16);
+  const bool split = s.waves > kNormMostWaves ||
+                     (!o.all_channel && seqlen > steps &&
+                      (norm_run_bytes(s, io) < 32 || (s.tiles * groups * batch < 64 && s.waves > kNormSplitWaves)));
+  return split ? norm_split_shape(dim / groups, seqlen, io, steps) : s;
 }
 
 // Partial sums of dweight per channel: one per batch row and tile of steps.

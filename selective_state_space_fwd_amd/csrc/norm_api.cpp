@@ -2,6 +2,8 @@
 // happens here, before any HIP call; the launches are in norm_kernels.hip.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "api_util.h"
 #include "block_launch.h"
 #include "ssm_norm.h"
@@ -16,6 +18,10 @@ using ssm_api::StridedArray;
 
 namespace {
 
+// Channels of a group that a workgroup always holds whole, in one step per lane (16 waves of
+// 64 lanes of four fp32 channels).
+constexpr int64_t kWholeChannels = int64_t(ssm::kNormMostWaves) * 64 * 4;
+
 int check_sizes(uint32_t flags, int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, int64_t* esz,
                 int64_t* elems) {
   if (flags & ~uint32_t(SSM_IO_MASK | SSM_NORM_BEFORE_GATE)) return SSM_ERR_INVALID_ARG;
@@ -26,10 +32,17 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t dim, int64_t groups, int6
   int64_t rows, bytes, tokens, groups_all;
   if (batch > kInt32Max || dim > kInt32Max || seqlen > kInt32Max || !mul_ok(batch, dim, &rows) ||
       !mul_ok(rows, seqlen, elems) || !mul_ok(*elems, 4, &bytes) || !mul_ok(batch, seqlen, &tokens) ||
-      // at most one workgroup per token and group, in either shape
-      !mul_ok(tokens, groups, &groups_all) || groups_all > kInt32Max)
+      // at most one workgroup per token and group, or per token and block of 32 channels
+      !mul_ok(tokens, groups + dim / 32, &groups_all) || groups_all > kInt32Max)
     return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
+}
+
+// Bytes of the blocks' sums of a split norm; -1 past int64.
+int64_t split_bytes(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, ssm::Io io, int steps) {
+  const int64_t blocks = ssm::norm_split_shape(dim / groups, seqlen, io, steps).cblocks;
+  int64_t n;
+  return mul_ok(batch * groups * seqlen, blocks * 4, &n) ? n : -1;
 }
 
 ssm::View view(const void* p, const StridedArray& a) { return ssm::View{p, a.s, a.order}; }
@@ -49,9 +62,19 @@ void batch_as_time(ssm::View* v) { v->s = ssm::Strides{0, v->s.channel, v->s.bat
 
 extern "C" {
 
+int64_t ssm_norm_fwd_workspace_bytes(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen,
+                                     uint32_t flags) {
+  int64_t esz, elems;
+  if (check_sizes(flags & SSM_IO_MASK, batch, dim, groups, seqlen, &esz, &elems) != SSM_OK) return -1;
+  if (elems == 0) return 0;
+  const ssm::Io io = esz == 2 ? ssm::Io::BF16 : ssm::Io::F32;
+  return split_bytes(batch, dim, groups, seqlen, io, ssm::kNormFwdSteps[int(io)]);
+}
+
 int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z, const int64_t* z_strides,
                  const float* weight, float eps, uint32_t flags, void* out, const int64_t* out_strides,
-                 float* rstd, int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, void* stream) {
+                 float* rstd, void* workspace, int64_t workspace_bytes, int64_t batch, int64_t dim,
+                 int64_t groups, int64_t seqlen, void* stream) {
   int64_t esz, elems;
   if (int st = check_sizes(flags, batch, dim, groups, seqlen, &esz, &elems)) return st;
   if (!(eps >= 0.0f)) return SSM_ERR_INVALID_ARG;
@@ -60,8 +83,17 @@ int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z, const i
   if (int st = z ? check_strided(z_strides, batch, dim, seqlen, esz, false, &za) : SSM_OK) return st;
   if (int st = check_strided(out_strides, batch, dim, seqlen, esz, true, &oa)) return st;
   if ((elems > 0 && (!y || !out)) || (dim > 0 && !weight)) return SSM_ERR_INVALID_ARG;
+  // Where no split can come about, the workspace is not looked at.
+  int64_t need = 0;
+  const bool chan = ya.order == ssm::Order::Channel && (!z || za.order == ssm::Order::Channel) &&
+                    oa.order == ssm::Order::Channel;
+  if (elems > 0 && (!chan || dim / groups > kWholeChannels))
+    need = ssm_norm_fwd_workspace_bytes(batch, dim, groups, seqlen, flags);
+  if (need < 0) return SSM_ERR_UNSUPPORTED;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
   const uintptr_t e = uintptr_t(esz);
-  if (!aligned(y, e) || !aligned(z, e) || !aligned(out, e) || !aligned(weight, 4) || !aligned(rstd, 4))
+  if (!aligned(y, e) || !aligned(z, e) || !aligned(out, e) || !aligned(weight, 4) || !aligned(rstd, 4) ||
+      (need > 0 && !aligned(workspace, 256)))
     return SSM_ERR_MISALIGNED;
   Ranges r;
   r.add(y, ya.bytes, false);
@@ -69,6 +101,7 @@ int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z, const i
   r.add(weight, dim * 4, false);
   r.add(out, oa.bytes, true);
   r.add(rstd, elems > 0 ? batch * groups * seqlen * 4 : 0, true);
+  r.add(workspace, need, true);
   if (r.clash()) return SSM_ERR_INVALID_ARG;
   if (elems == 0) return SSM_OK;
   ssm::NormArgs a{};
@@ -80,6 +113,7 @@ int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z, const i
   a.rstd = rstd;
   a.rs = ssm::Strides{groups * seqlen, seqlen, 1};
   a.eps = eps;
+  a.workspace = static_cast<float*>(workspace);
   a.io = esz == 2 ? ssm::Io::BF16 : ssm::Io::F32;
   a.norm_first = (flags & SSM_NORM_BEFORE_GATE) != 0;
   ssm::View v[3] = {view(y, ya), view(z, za), view(out, oa)};
@@ -101,11 +135,16 @@ int64_t ssm_norm_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t groups,
   if (check_sizes(flags & SSM_IO_MASK, batch, dim, groups, seqlen, &esz, &elems) != SSM_OK) return -1;
   if (elems == 0) return 0;
   const ssm::Io io = esz == 2 ? ssm::Io::BF16 : ssm::Io::F32;
-  // (one token per row: as many partial sums as rows where their strides keep them apart)
-  const int64_t c = ssm::norm_partials(batch, ssm::norm_bwd_shape(dim, groups, seqlen, io, true));
-  const int64_t t = ssm::norm_partials(batch, ssm::norm_bwd_shape(dim, groups, seqlen, io, false));
-  if (!mul_ok(c > t ? c : t, dim * 4, &total)) return -1;
-  return total;
+  // The most of any orders, and of a batch of single tokens taken as one sequence.
+  const int64_t g = dim / groups, sums = split_bytes(batch, dim, groups, seqlen, io, ssm::kNormBwdSteps[int(io)]);
+  const int steps = ssm::kNormBwdSteps[int(io)];
+  int64_t n = 0;
+  for (const ssm::NormShape& s : {ssm::norm_whole_shape(g, seqlen, io, steps, 8),
+                                  ssm::norm_whole_shape(g, seqlen, io, steps, 16),
+                                  ssm::norm_split_shape(g, seqlen, io, steps)})
+    n = ssm::norm_partials(batch, s) > n ? ssm::norm_partials(batch, s) : n;
+  if (sums < 0 || !mul_ok(n, dim * 4, &total) || total > INT64_MAX - sums) return -1;
+  return total + sums;
 }
 
 int ssm_norm_bwd(const void* y, const int64_t* y_strides, const void* z, const int64_t* z_strides,

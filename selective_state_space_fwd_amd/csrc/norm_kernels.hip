@@ -9,11 +9,18 @@
 // written in 16-byte words and turned, where it has to be, by byte permutes within the lane.
 // A workgroup holds whole groups of its steps in registers: each tensor is read once, the
 // mean meets in LDS, and the result is rounded once at its store. Where every tensor has
-// channels contiguous (single tokens) a lane holds one step.
+// channels contiguous (single tokens) a lane holds one step. Groups too large for a workgroup,
+// and some whose steps it would read in too small pieces, take two launches instead (Phase).
 //
-// All of it is bound by memory: 3 reads and writes per element forward, 5 backward.
+// Bound by memory: 3 reads and writes per element forward, 5 backward. b4, 2048 channels, 2048
+// steps, bf16, y in the scan's order, z and the result in a projection's: forward 19.5 us (100
+// MB, 5.2 TB/s, the rate of a large copy), gradient 44 us (168 MB, 3.8 TB/s) and 4 for the sums
+// of dweight. The gradient's loads and its arithmetic (20 us, with four transcendentals per
+// element) overlap in part only: a CU holds one workgroup of sixteen waves.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <initializer_list>
 
 #include "block_launch.h"
 #include "device_block.h"
@@ -33,10 +40,11 @@ struct NormParams {
   float* rstd;
   int64_t rb, rg, rt;  // strides of rstd: batch row, group, step
   float* part;  // [batch * tiles][dim]
+  float* split;  // [batch][groups][cblocks][seqlen]: sums over each block of channels
   float eps, inv_g;
   int batch, groups, g, seqlen;
-  int lanes_log2, blocks;
-  uint32_t tiles, total;
+  int lanes_log2;
+  uint32_t tiles, cblocks, total;
 };
 
 // The words of a lane's square of CV = 16 bytes of channels by kSteps steps: one per channel, of
@@ -254,8 +262,8 @@ __device__ __forceinline__ void sum_group(float (&v)[N], const LaneMap& m, float
 // Where a workgroup's lanes are; consecutive tiles, which share cache lines of the time-ordered
 // tensors, go to one XCD.
 struct Place {
-  int b, grp, tile, nt;
-  int64_t t0, c0;  // first step; first channel within the group, of round 0
+  int b, grp, cb, tile, nt;
+  int64_t t0, c0;  // first step; first channel within the group
   LaneMap map;
 };
 
@@ -263,17 +271,54 @@ template <typename Elem, int kSteps>
 __device__ __forceinline__ Place place_of(const NormParams& p) {
   constexpr int CV = Vec<Elem>::kN;
   const uint32_t id = xcd_order(blockIdx.x, p.total);
-  const int wave = threadIdx.x >> 6;
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
   Place a;
   a.map = LaneMap{p.lanes_log2};
   a.tile = int(id % p.tiles);
-  const uint32_t rest = id / p.tiles;
+  uint32_t rest = id / p.tiles;
+  a.cb = int(rest % p.cblocks);
+  rest /= p.cblocks;
   a.grp = int(rest % uint32_t(p.groups));
   a.b = int(rest / uint32_t(p.groups));
   a.t0 = (int64_t(a.tile) * (64 >> p.lanes_log2) + a.map.time()) * kSteps;
   a.nt = a.t0 >= p.seqlen ? 0 : p.seqlen - a.t0 < kSteps ? int(p.seqlen - a.t0) : kSteps;
-  a.c0 = ((int64_t(wave) << p.lanes_log2) + a.map.channel()) * CV;
+  a.c0 = ((int64_t(a.cb * waves + wave) << p.lanes_log2) + a.map.channel()) * CV;
   return a;
+}
+
+// What a launch does of a norm whose sums run over a group: all of it, a workgroup holding whole
+// groups; or, in two launches, a workgroup holding a block of a group's channels, first the sums
+// over its block, then the rest from all blocks' sums.
+enum Phase { kWhole = 0, kSums = 1, kApply = 2 };
+
+// A workgroup's sums over its block of channels to memory, one per step.
+template <int N>
+__device__ __forceinline__ void store_sums(const NormParams& p, const Place& a, const float (&v)[N]) {
+  if ((threadIdx.x >> 6) != 0 || a.map.channel() != 0) return;
+  float* row = p.split + ((int64_t(a.b) * p.groups + a.grp) * p.cblocks + a.cb) * p.seqlen + a.t0;
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    if (t < a.nt) row[t] = v[t];
+}
+
+// The sums of all blocks of a group, for this lane's steps, in block order within each slice of
+// the workgroup and then over the slices. buf: blockDim floats.
+template <int N>
+__device__ __forceinline__ void load_sums(const NormParams& p, const Place& a, float (&v)[N], float* buf) {
+  const int span = (64 >> p.lanes_log2) * N;  // the workgroup's steps: at most 64, a power of two
+  const int at = threadIdx.x & (span - 1), slice = threadIdx.x / span, slices = blockDim.x / span;
+  const int64_t t = int64_t(a.tile) * span + at;
+  const float* col = p.split + (int64_t(a.b) * p.groups + a.grp) * p.cblocks * p.seqlen + t;
+  float sum = 0.0f;
+  if (t < p.seqlen)
+    for (uint32_t k = slice; k < p.cblocks; k += slices) sum += col[int64_t(k) * p.seqlen];
+  buf[threadIdx.x] = sum;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int k = 0; k < slices; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += buf[k * span + a.map.time() * N + i];
 }
 
 template <int CV>
@@ -283,44 +328,45 @@ __device__ __forceinline__ int channels_left(const NormParams& p, int64_t c0) {
 
 // ---------------------------------------------------------------- forward
 //
-// kHeld: the group is covered in one round and stays in registers; else the rounds are read a
-// second time (groups of more than 16 waves of channels).
-template <typename Elem, int kSteps, bool kHeld, int kMode>
+template <typename Elem, int kSteps, int kPhase, int kMode>
 __global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParams p) {
   constexpr int CV = Vec<Elem>::kN;
   extern __shared__ float buf[];
   const Place a = place_of<Elem, kSteps>(p);
-  const int64_t round = int64_t(blockDim.x >> 6) * (int64_t(CV) << p.lanes_log2);
-  const int64_t base = int64_t(a.grp) * p.g;
+  const int64_t base = int64_t(a.grp) * p.g + a.c0;
+  const int nc = channels_left<CV>(p, a.c0);
   Square<Elem, kSteps> y, z;
   float q[CV][kSteps], sum[kSteps];  // q: y s, the result but for w r
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) sum[t] = 0.0f;
-  auto read = [&](int64_t c0, bool add) {
-    const int nc = channels_left<CV>(p, c0);
-    load_square<Elem, kSteps>(p.y, a.b, base + c0, a.t0, nc, a.nt, y);
-    if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p.z, a.b, base + c0, a.t0, nc, a.nt, z);
+  load_square<Elem, kSteps>(p.y, a.b, base, a.t0, nc, a.nt, y);
+  if constexpr (kMode == kGateFirst || (kMode == kNormFirst && kPhase != kSums))
+    load_square<Elem, kSteps>(p.z, a.b, base, a.t0, nc, a.nt, z);
 #pragma unroll
-    for (int c = 0; c < CV; ++c) {
+  for (int c = 0; c < CV; ++c) {
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        const float v = y.at(c, t);
-        q[c][t] = kMode == kNoGate ? v : v * silu_f(z.at(c, t));
-        const float n = kMode == kNormFirst ? v : q[c][t];
-        if (add) sum[t] = __builtin_fmaf(n, n, sum[t]);
-      }
-      // A channel's words go out of use as its values come into it, if the channels are not
-      // interleaved.
-      if constexpr (kSteps > 1) __builtin_amdgcn_sched_barrier(0);
+    for (int t = 0; t < kSteps; ++t) {
+      const float v = y.at(c, t);
+      if constexpr (kMode == kGateFirst || (kMode == kNormFirst && kPhase != kSums))
+        q[c][t] = v * silu_f(z.at(c, t));
+      else
+        q[c][t] = v;
+      const float n = kMode == kNormFirst ? v : q[c][t];
+      if constexpr (kPhase != kApply) sum[t] = __builtin_fmaf(n, n, sum[t]);
     }
-  };
-  if constexpr (kHeld) {
-    read(a.c0, true);
-  } else {
-    for (int k = 0; k < p.blocks; ++k) read(a.c0 + k * round, true);
+    // A channel's words go out of use as its values come into it, if the channels are not
+    // interleaved.
+    if constexpr (kSteps > 1) __builtin_amdgcn_sched_barrier(0);
   }
-  sum_group<kSteps>(sum, a.map, buf);
-  float r[kSteps];
+  if constexpr (kPhase == kApply)
+    load_sums<kSteps>(p, a, sum, buf);
+  else
+    sum_group<kSteps>(sum, a.map, buf);
+  if constexpr (kPhase == kSums) {
+    store_sums<kSteps>(p, a, sum);
+    return;
+  }
+  float r[kSteps], w[CV], row[CV];
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) r[t] = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[t], p.inv_g, p.eps));
   if (p.rstd && a.c0 == 0) {
@@ -328,28 +374,16 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParam
     for (int t = 0; t < kSteps; ++t)
       if (t < a.nt) p.rstd[a.b * p.rb + a.grp * p.rg + (a.t0 + t) * p.rt] = r[t];
   }
-  auto write = [&](int64_t c0) {
-    const int nc = channels_left<CV>(p, c0);
-    float w[CV], row[CV];
-    load_run<float, CV>(p.weight + base + c0, nc, w);
-    Square<Elem, kSteps> o;
+  load_run<float, CV>(p.weight + base, nc, w);
+  Square<Elem, kSteps> o;
 #pragma unroll
-    for (int c = 0; c < CV; ++c) {
-      float v[kSteps];
+  for (int c = 0; c < CV; ++c) {
+    float v[kSteps];
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) v[t] = q[c][t] * (r[t] * w[c]);
-      put<Elem, kSteps>(o, c, v, row);
-    }
-    store_square<Elem, kSteps>(p.out, a.b, base + c0, a.t0, nc, a.nt, o);
-  };
-  if constexpr (kHeld) {
-    write(a.c0);
-  } else {
-    for (int k = 0; k < p.blocks; ++k) {
-      read(a.c0 + k * round, false);
-      write(a.c0 + k * round);
-    }
+    for (int t = 0; t < kSteps; ++t) v[t] = q[c][t] * (r[t] * w[c]);
+    put<Elem, kSteps>(o, c, v, row);
   }
+  store_square<Elem, kSteps>(p.out, a.b, base, a.t0, nc, a.nt, o);
 }
 
 // ---------------------------------------------------------------- backward
@@ -358,118 +392,97 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParam
 // norm first: A = w dout s;  S = sum_G A y; dy = r (A - y r^2 S / G); dz = w dout y r s'
 // dweight = sum over tokens of dout (s) times the normed value; per workgroup and channel
 // here, over workgroups by a second launch in a fixed order.
-template <typename Elem, int kSteps, bool kHeld, int kMode>
+template <typename Elem, int kSteps, int kPhase, int kMode>
 __global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParams p) {
   constexpr int CV = Vec<Elem>::kN;
   extern __shared__ float buf[];
   const Place a = place_of<Elem, kSteps>(p);
-  const int64_t round = int64_t(blockDim.x >> 6) * (int64_t(CV) << p.lanes_log2);
-  const int64_t base = int64_t(a.grp) * p.g;
+  const int64_t base = int64_t(a.grp) * p.g + a.c0;
+  const int nc = channels_left<CV>(p, a.c0);
   Square<Elem, kSteps> y, z, g;
   float w[CV], sum[kSteps], r[kSteps], sigma[CV][kSteps];
+  load_square<Elem, kSteps>(p.y, a.b, base, a.t0, nc, a.nt, y);
+  if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p.z, a.b, base, a.t0, nc, a.nt, z);
+  load_square<Elem, kSteps>(p.dout, a.b, base, a.t0, nc, a.nt, g);
+  load_run<float, CV>(p.weight + base, nc, w);
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
     sum[t] = 0.0f;
     r[t] = t < a.nt ? p.rstd[a.b * p.rb + a.grp * p.rg + (a.t0 + t) * p.rt] : 0.0f;
   }
-  auto read = [&](int64_t c0) {
-    const int nc = channels_left<CV>(p, c0);
-    load_square<Elem, kSteps>(p.y, a.b, base + c0, a.t0, nc, a.nt, y);
-    if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p.z, a.b, base + c0, a.t0, nc, a.nt, z);
-    load_square<Elem, kSteps>(p.dout, a.b, base + c0, a.t0, nc, a.nt, g);
-    load_run<float, CV>(p.weight + base + c0, nc, w);
-  };
-  // sum_G A v: w dout y s either way
-  auto add = [&]() {
+  if constexpr (kPhase == kApply) {
+    load_sums<kSteps>(p, a, sum, buf);
+  } else {
+    // sum_G A v: w dout y s either way
 #pragma unroll
-    for (int c = 0; c < CV; ++c)
+    for (int c = 0; c < CV; ++c) {
 #pragma unroll
       for (int t = 0; t < kSteps; ++t) {
         float v = y.at(c, t);
         if constexpr (kMode != kNoGate) {
           const float zv = z.at(c, t), sg = sigmoid_f(zv);
-          if (kHeld) sigma[c][t] = sg;
+          sigma[c][t] = sg;
           v *= zv * sg;
         }
         sum[t] = __builtin_fmaf(w[c] * g.at(c, t), v, sum[t]);
-        if (kSteps > 1 && t == kSteps - 1) __builtin_amdgcn_sched_barrier(0);
       }
-  };
-  if constexpr (kHeld) {
-    read(a.c0);
-    add();
-  } else {
-    for (int k = 0; k < p.blocks; ++k) {
-      read(a.c0 + k * round);
-      add();
+      __builtin_amdgcn_sched_barrier(0);
     }
+    sum_group<kSteps>(sum, a.map, buf);
   }
-  sum_group<kSteps>(sum, a.map, buf);
+  if constexpr (kPhase == kSums) {
+    store_sums<kSteps>(p, a, sum);
+    return;
+  }
   float m[kSteps];  // r^3 S / G
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) m[t] = r[t] * r[t] * r[t] * (sum[t] * p.inv_g);
+  forget<Elem, kSteps>(y);
+  forget<Elem, kSteps>(g);
+  if constexpr (kMode != kNoGate) forget<Elem, kSteps>(z);
 
-  auto write = [&](int64_t c0) {
-    const int nc = channels_left<CV>(p, c0);
-    float dw[CV], row_y[CV], row_z[CV];
-    Square<Elem, kSteps> dys, dzs;
+  float dw[CV], row_y[CV], row_z[CV];
+  Square<Elem, kSteps> dys, dzs;
 #pragma unroll
-    for (int c = 0; c < CV; ++c) {
-      float dy[kSteps], dz[kSteps];
-      dw[c] = 0.0f;
+  for (int c = 0; c < CV; ++c) {
+    float dy[kSteps], dz[kSteps];
+    dw[c] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) {
-        const float yv = y.at(c, t), gv = g.at(c, t);
-        float s = 1.0f, ds = 0.0f;
-        if constexpr (kMode != kNoGate) {
-          const float zv = z.at(c, t), sg = kHeld ? sigma[c][t] : sigmoid_f(zv);
-          s = zv * sg;
-          ds = __builtin_fmaf(s, 1.0f - sg, sg);
-        }
-        const float gr = gv * r[t], v = kMode == kNoGate ? yv : yv * s;
-        dw[c] = __builtin_fmaf(gr, v, dw[c]);
-        if constexpr (kMode == kNormFirst) {
-          const float a1 = w[c] * gr;
-          dy[t] = __builtin_fmaf(-yv, m[t], a1 * s);
-          dz[t] = a1 * (yv * ds);
-        } else {
-          const float dv = __builtin_fmaf(-v, m[t], w[c] * gr);
-          dy[t] = dv * s;
-          dz[t] = dv * (yv * ds);
-        }
+    for (int t = 0; t < kSteps; ++t) {
+      const float yv = y.at(c, t), gv = g.at(c, t);
+      float s = 1.0f, ds = 0.0f;
+      if constexpr (kMode != kNoGate) {
+        const float zv = z.at(c, t), sg = kPhase == kWhole ? sigma[c][t] : sigmoid_f(zv);
+        s = zv * sg;
+        ds = __builtin_fmaf(s, 1.0f - sg, sg);
       }
-      put<Elem, kSteps>(dys, c, dy, row_y);
-      if constexpr (kMode != kNoGate) put<Elem, kSteps>(dzs, c, dz, row_z);
-      // A channel's words go out of use as its gradients' words come into it, if the channels
-      // are not interleaved (nor its sums put off).
-      if constexpr (kSteps > 1) {
-        asm volatile("" : "+v"(dw[c]));
-        forget_word(dys.w[c]);
-        if constexpr (kMode != kNoGate) forget_word(dzs.w[c]);
-        __builtin_amdgcn_sched_barrier(0);
+      const float gr = gv * r[t], v = kMode == kNoGate ? yv : yv * s;
+      dw[c] = __builtin_fmaf(gr, v, dw[c]);
+      if constexpr (kMode == kNormFirst) {
+        const float a1 = w[c] * gr;
+        dy[t] = __builtin_fmaf(-yv, m[t], a1 * s);
+        dz[t] = a1 * (yv * ds);
+      } else {
+        const float dv = __builtin_fmaf(-v, m[t], w[c] * gr);
+        dy[t] = dv * s;
+        dz[t] = dv * (yv * ds);
       }
     }
-    store_square<Elem, kSteps>(p.dy, a.b, base + c0, a.t0, nc, a.nt, dys);
-    if constexpr (kMode != kNoGate) store_square<Elem, kSteps>(p.dz, a.b, base + c0, a.t0, nc, a.nt, dzs);
-    // over the lanes along time, then one store per channel
-    sum_wave<true>(dw, a.map);
-    if (a.map.time() == 0)
-      store_run<float, CV>(p.part + (int64_t(a.b) * p.tiles + a.tile) * (int64_t(p.groups) * p.g) + base + c0,
-                           nc, dw);
-  };
-  if constexpr (kHeld) {
-    if constexpr (kSteps > 1) {
-      forget<Elem, kSteps>(y);
-      forget<Elem, kSteps>(g);
-      if constexpr (kMode != kNoGate) forget<Elem, kSteps>(z);
-    }
-    write(a.c0);
-  } else {
-    for (int k = 0; k < p.blocks; ++k) {
-      read(a.c0 + k * round);
-      write(a.c0 + k * round);
-    }
+    put<Elem, kSteps>(dys, c, dy, row_y);
+    if constexpr (kMode != kNoGate) put<Elem, kSteps>(dzs, c, dz, row_z);
+    // A channel's words go out of use as its gradients' words come into it, if the channels
+    // are not interleaved (nor its sums put off).
+    asm volatile("" : "+v"(dw[c]));
+    forget_word(dys.w[c]);
+    if constexpr (kMode != kNoGate) forget_word(dzs.w[c]);
+    __builtin_amdgcn_sched_barrier(0);
   }
+  store_square<Elem, kSteps>(p.dy, a.b, base, a.t0, nc, a.nt, dys);
+  if constexpr (kMode != kNoGate) store_square<Elem, kSteps>(p.dz, a.b, base, a.t0, nc, a.nt, dzs);
+  // over the lanes along time, then one store per channel
+  sum_wave<true>(dw, a.map);
+  if (a.map.time() == 0)
+    store_run<float, CV>(p.part + (int64_t(a.b) * p.tiles + a.tile) * (int64_t(p.groups) * p.g) + base, nc, dw);
 }
 
 constexpr int kReduceCols = 32, kReduceSlices = 32;
@@ -507,59 +520,75 @@ NormParams params_of(const NormArgs& a, const NormShape& s) {
   p.groups = int(a.groups);
   p.seqlen = int(a.seqlen);
   p.lanes_log2 = s.lanes_log2;
-  p.blocks = int(s.blocks);
   p.tiles = uint32_t(s.tiles);
-  p.total = uint32_t(s.tiles * a.groups * a.batch);
+  p.cblocks = uint32_t(s.cblocks);
+  p.total = uint32_t(s.tiles * s.cblocks * a.groups * a.batch);
   return p;
 }
 
-template <typename Elem, int kSteps, bool kHeld, int kMode>
+template <typename Elem, int kSteps, int kPhase, int kMode>
 void launch(const NormParams& p, const NormShape& s, bool backward, hipStream_t st) {
   constexpr int io = sizeof(Elem) == 2 ? int(Io::BF16) : int(Io::F32);
   const dim3 grid(p.total), block(64 * s.waves);
-  const size_t lds = size_t(s.waves) * (64 >> s.lanes_log2) * kSteps * 4;
+  const size_t lds = kPhase == kApply ? size_t(64) * s.waves * 4
+                                      : size_t(s.waves) * (64 >> s.lanes_log2) * kSteps * 4;
   if constexpr (kSteps == kNormBwdSteps[io]) {
-    if (backward) hipLaunchKernelGGL((norm_bwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
+    if (backward) hipLaunchKernelGGL((norm_bwd_kernel<Elem, kSteps, kPhase, kMode>), grid, block, lds, st, p);
   }
   if constexpr (kSteps == 1 || kSteps == kNormFwdSteps[io]) {
-    if (!backward) hipLaunchKernelGGL((norm_fwd_kernel<Elem, kSteps, kHeld, kMode>), grid, block, lds, st, p);
+    if (!backward) hipLaunchKernelGGL((norm_fwd_kernel<Elem, kSteps, kPhase, kMode>), grid, block, lds, st, p);
   }
 }
 
-template <typename Elem, int kSteps, bool kHeld>
-void run_mode(const NormParams& p, const NormShape& s, bool backward, bool norm_first, hipStream_t st) {
+template <typename Elem, int kSteps, int kPhase>
+void run_phase(const NormParams& p, const NormShape& s, bool backward, bool norm_first, hipStream_t st) {
   if (!p.z.p)
-    launch<Elem, kSteps, kHeld, kNoGate>(p, s, backward, st);
+    launch<Elem, kSteps, kPhase, kNoGate>(p, s, backward, st);
   else if (norm_first)
-    launch<Elem, kSteps, kHeld, kNormFirst>(p, s, backward, st);
+    launch<Elem, kSteps, kPhase, kNormFirst>(p, s, backward, st);
   else
-    launch<Elem, kSteps, kHeld, kGateFirst>(p, s, backward, st);
+    launch<Elem, kSteps, kPhase, kGateFirst>(p, s, backward, st);
 }
 
 template <typename Elem, int kSteps>
 void run_steps(const NormParams& p, const NormShape& s, bool backward, bool norm_first, hipStream_t st) {
-  s.blocks == 1 ? run_mode<Elem, kSteps, true>(p, s, backward, norm_first, st)
-                : run_mode<Elem, kSteps, false>(p, s, backward, norm_first, st);
+  if (!s.split) return run_phase<Elem, kSteps, kWhole>(p, s, backward, norm_first, st);
+  if constexpr (kSteps > 1) {
+    run_phase<Elem, kSteps, kSums>(p, s, backward, norm_first, st);
+    run_phase<Elem, kSteps, kApply>(p, s, backward, norm_first, st);
+  }
 }
 
 template <typename Elem>
 void run(const NormParams& p, const NormShape& s, bool backward, bool norm_first, hipStream_t st) {
   constexpr int io = sizeof(Elem) == 2 ? int(Io::BF16) : int(Io::F32);
-  if (s.steps == 1)
-    run_steps<Elem, 1>(p, s, false, norm_first, st);
-  else if (backward)
+  if (backward)
     run_steps<Elem, kNormBwdSteps[io]>(p, s, true, norm_first, st);
+  else if (s.steps == 1)
+    run_steps<Elem, 1>(p, s, false, norm_first, st);
   else
     run_steps<Elem, kNormFwdSteps[io]>(p, s, false, norm_first, st);
+}
+
+// The tensors of a launch, for the choice of its shape.
+NormOrders orders_of(const NormArgs& a, std::initializer_list<const View*> views) {
+  NormOrders o{true, true};
+  const int64_t esz = a.io == Io::BF16 ? 2 : 4;
+  for (const View* v : views) {
+    if (!v->p || v->order == Order::Channel) continue;
+    o.all_channel = false;
+    if (reinterpret_cast<uintptr_t>(v->p) % 4 || v->s.channel * esz % 4 || (a.batch > 1 && v->s.batch * esz % 4))
+      o.dword_rows = false;
+  }
+  return o;
 }
 
 }  // namespace
 
 int launch_norm_fwd(const NormArgs& a, void* stream) {
-  const bool chan = a.y.order == Order::Channel && (!a.z.p || a.z.order == Order::Channel) &&
-                    a.out.order == Order::Channel;
-  const NormShape s = norm_fwd_shape(a.dim, a.groups, a.seqlen, a.io, chan);
-  const NormParams p = params_of(a, s);
+  const NormShape s = norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, orders_of(a, {&a.y, &a.z, &a.out}));
+  NormParams p = params_of(a, s);
+  p.split = a.workspace;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.io == Io::BF16)
     run<uint16_t>(p, s, false, a.norm_first, st);
@@ -572,18 +601,17 @@ int launch_norm_bwd(const NormArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   int64_t rows = 0;
   if (a.batch > 0 && a.seqlen > 0) {
-    const bool chan = a.y.order == Order::Channel && a.dout.order == Order::Channel &&
-                      a.dy.order == Order::Channel &&
-                      (!a.z.p || (a.z.order == Order::Channel && a.dz.order == Order::Channel));
-    const NormShape s = norm_bwd_shape(a.dim, a.groups, a.seqlen, a.io, chan);
-    const NormParams p = params_of(a, s);
+    const NormShape s = norm_bwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io,
+                                       orders_of(a, {&a.y, &a.z, &a.dout, &a.dy, &a.dz}));
+    NormParams p = params_of(a, s);
+    rows = norm_partials(a.batch, s);
+    p.split = a.workspace + rows * a.dim;
     if (a.io == Io::BF16)
       run<uint16_t>(p, s, true, a.norm_first, st);
     else
       run<float>(p, s, true, a.norm_first, st);
     const int err = int(hipGetLastError());
     if (err) return err;
-    rows = norm_partials(a.batch, s);
   }
   hipLaunchKernelGGL(norm_bwd_reduce, dim3(unsigned((a.dim + kReduceCols - 1) / kReduceCols)),
                      dim3(kReduceCols * kReduceSlices), 0, st, a.workspace, a.dweight, rows, a.dim);

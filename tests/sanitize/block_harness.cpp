@@ -28,11 +28,20 @@ const int64_t kMax = 2147483647;
 
 // Workgroups and waves of a shape, as the launches form them, within a grid's limits.
 void fits_norm(const ssm::NormArgs& a, const ssm::NormShape& s) {
-  EXPECT(s.waves >= 1 && s.waves <= 16 && s.blocks >= 1 && s.tiles >= 1 && s.lanes_log2 >= 0 && s.lanes_log2 <= 6);
-  EXPECT(s.tiles <= kMax / a.groups / a.batch);
+  EXPECT(s.waves >= 1 && s.waves <= 16 && s.cblocks >= 1 && s.tiles >= 1 && s.lanes_log2 >= 0 && s.lanes_log2 <= 6);
+  EXPECT(s.tiles * s.cblocks <= kMax / a.groups / a.batch);
   const int64_t cv = a.io == ssm::Io::BF16 ? 8 : 4, g = a.dim / a.groups;
-  EXPECT(s.blocks * s.waves * (cv << s.lanes_log2) >= g);
+  EXPECT(s.cblocks * s.waves * (cv << s.lanes_log2) >= g);
   EXPECT(s.tiles * s.steps * (64 >> s.lanes_log2) >= a.seqlen);
+  EXPECT(s.split || s.cblocks == 1);
+  EXPECT(!s.split || a.workspace);
+}
+
+void fits_norm(const ssm::NormArgs& a, bool backward) {
+  for (const ssm::NormOrders o : {ssm::NormOrders{true, true}, ssm::NormOrders{false, true},
+                                  ssm::NormOrders{false, false}})
+    fits_norm(a, backward ? ssm::norm_bwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, o)
+                          : ssm::norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, o));
 }
 }  // namespace
 
@@ -62,16 +71,12 @@ int launch_state_step(const StepArgs& a, void*) {
 }
 int launch_norm_fwd(const NormArgs& a, void*) {
   ++g_launches;
-  fits_norm(a, norm_fwd_shape(a.dim, a.groups, a.seqlen, a.io, true));
-  fits_norm(a, norm_fwd_shape(a.dim, a.groups, a.seqlen, a.io, false));
+  fits_norm(a, false);
   return 0;
 }
 int launch_norm_bwd(const NormArgs& a, void*) {
   ++g_launches;
-  if (a.batch > 0 && a.seqlen > 0) {
-    fits_norm(a, norm_bwd_shape(a.dim, a.groups, a.seqlen, a.io, true));
-    fits_norm(a, norm_bwd_shape(a.dim, a.groups, a.seqlen, a.io, false));
-  }
+  if (a.batch > 0 && a.seqlen > 0) fits_norm(a, true);
   return 0;
 }
 }  // namespace ssm
@@ -153,7 +158,7 @@ void norms() {
   const int64_t token[3] = {2048 * 2048, 1, 2048};
   int before = g_launches;
   EXPECT(ssm_norm_fwd(at(0), nullptr, at(1), token, at<const float>(2), 1e-5f, SSM_IO_BF16, at(3), token,
-                      at<float>(4), 4, 2048, 1, 2048, nullptr) == SSM_OK);
+                      at<float>(4), at(5), 1 << 20, 4, 2048, 1, 2048, nullptr) == SSM_OK);
   EXPECT(g_launches == ++before);
   for (int64_t b : kBig)
     for (int64_t d : kBig)
@@ -161,7 +166,8 @@ void norms() {
         for (int64_t g : {int64_t(1), int64_t(5), int64_t(65535), int64_t(0), INT64_MAX, int64_t(-1)})
           for (uint32_t io : {SSM_IO_F32, SSM_IO_BF16}) {
             EXPECT(status(ssm_norm_fwd(at(0), nullptr, at(1), nullptr, at<const float>(2), 0.0f, io, at(3), nullptr,
-                                       at<float>(4), b, d, g, L, nullptr)));
+                                       at<float>(4), at(5), ssm_norm_fwd_workspace_bytes(b, d, g, L, io), b, d, g, L,
+                                       nullptr)));
             const int64_t ws = ssm_norm_bwd_workspace_bytes(b, d, g, L, io);
             EXPECT(ws >= -1);
             EXPECT(status(ssm_norm_bwd(at(0), nullptr, nullptr, nullptr, at<const float>(2), at<const float>(3), at(4),
@@ -173,8 +179,8 @@ void norms() {
       for (int64_t stp : kFew)
         for (int64_t L : {int64_t(1), int64_t(9)}) {
           const int64_t s[3] = {sb, sc, stp};
-          EXPECT(status(ssm_norm_fwd(at(0), s, at(1), s, at<const float>(2), 1e-5f, SSM_IO_F32, at(3), s, nullptr, 4,
-                                     6, 2, L, nullptr)));
+          EXPECT(status(ssm_norm_fwd(at(0), s, at(1), s, at<const float>(2), 1e-5f, SSM_IO_F32, at(3), s, nullptr, at(4),
+                                     1 << 20, 4, 6, 2, L, nullptr)));
         }
 }
 

@@ -162,7 +162,7 @@ def test_step_sizes():
 
 def norm(**kw):
     a = dict(y=P[0], ys=None, z=None, zs=None, w=P[1], eps=1e-5, flags=BF, out=P[2], os=None,
-             rstd=None, batch=2, dim=4, groups=1, seqlen=8, stream=None)
+             rstd=None, ws=P[9], wsb=1 << 20, batch=2, dim=4, groups=1, seqlen=8, stream=None)
     a.update(kw)
     return ssm.ssm_norm_fwd(*a.values())
 
@@ -172,14 +172,19 @@ def test_norm_refusals():
         dict(y=None), dict(w=None), dict(out=None), dict(batch=-1), dict(dim=-1),
         dict(seqlen=-1), dict(groups=0), dict(groups=3), dict(eps=-1.0), dict(eps=float("nan")),
         dict(flags=BF | 1 << 11), dict(out=P[0]), dict(z=P[2]), dict(rstd=P[2]), dict(rstd=P[1]),
-        dict(os=st(8, 8, 1)), dict(os=st(32, 1, 3)), dict(ys=st(-1, 8, 1))])
+        dict(os=st(8, 8, 1)), dict(os=st(32, 1, 3)), dict(ys=st(-1, 8, 1)), dict(ws=None),
+        dict(wsb=0), dict(ws=P[0]),
+        dict(wsb=ssm.ssm_norm_fwd_workspace_bytes(2, 4, 1, 8, BF) - 1)])
     refused(norm, ssm.SSM_ERR_UNSUPPORTED, [
         dict(flags=2), dict(ys=st(64, 16, 2)), dict(z=P[3], zs=st(64, 16, 2)),
         dict(os=st(64, 16, 2)), dict(batch=1 << 20, seqlen=1 << 20), dict(seqlen=1 << 31),
         dict(batch=1 << 31, seqlen=1)])
     refused(norm, ssm.SSM_ERR_MISALIGNED, [
         dict(y=P[0] + 1), dict(z=P[3] + 1), dict(out=P[2] + 1), dict(w=P[1] + 2),
-        dict(rstd=P[3] + 2)])
+        dict(rstd=P[3] + 2), dict(ws=P[9] + 64)])
+    ws = ssm.ssm_norm_fwd_workspace_bytes
+    assert ws(2, 4, 1, 8, BF) == 2 * 8 * 4 and ws(3, 1024, 2, 5, F32) == 3 * 2 * 4 * 5 * 4
+    assert ws(0, 4, 1, 8, BF) == 0 and ws(1, 4, 3, 8, BF) == ws(1, -4, 1, 8, BF) == -1
     assert norm(batch=0) == norm(dim=0) == norm(seqlen=0) == ssm.SSM_OK
 
 
