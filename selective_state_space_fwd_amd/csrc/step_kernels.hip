@@ -39,9 +39,30 @@ struct StepParams {
   int batch, dim, dstate, headdim, softplus;
 };
 
-// Four states from p on, those at and past n zero (not read).
+// Four states from p on, those at and past n zero (not read), and back. kStream: past the
+// caches (non-temporal).
+template <bool kStream>
 __device__ __forceinline__ void load4(const float* p, int n, float (&v)[4]) {
+  if constexpr (kStream) {
+    typedef float quad __attribute__((ext_vector_type(4), aligned(4)));
+    if (n >= 4) {
+      const quad q = __builtin_nontemporal_load(reinterpret_cast<const quad*>(p));
+      v[0] = q.x;
+      v[1] = q.y;
+      v[2] = q.z;
+      v[3] = q.w;
+      return;
+    }
+  }
   load_run<float, 4>(p, n, v);
+}
+
+template <bool kStream>
+__device__ __forceinline__ void store4(float* p, int n, const float (&v)[4]) {
+  if (kStream && n >= 4)
+    store_run_stream<float, 4>(p, n, v);
+  else
+    store_run<float, 4>(p, n, v);
 }
 
 template <typename Elem>
@@ -57,7 +78,7 @@ struct Channel {
 };
 
 // LG: log2 of the lanes per channel. CH: channels per lane, at most 2^LG (a lane per channel).
-template <typename Elem, int LG, int CH, bool kHeads>
+template <typename Elem, int LG, int CH, bool kHeads, bool kStream>
 __global__ __launch_bounds__(64 * kWaves) void state_step_kernel(StepParams p) {
   constexpr int CPW = 64 >> LG;  // channels per wave and access
   static_assert(CH * CPW <= 64, "a lane per channel");
@@ -93,13 +114,17 @@ __global__ __launch_bounds__(64 * kWaves) void state_step_kernel(StepParams p) {
     if (own) static_cast<Elem*>(p.out)[int64_t(r) * p.dim + mine] = Elem(0);
     return;
   }
+  // (all of the states first: between loads of A, which many rows share, they take a fifth longer)
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int64_t ch = first_ch + k * CPW;
-    const int n = ch < p.dim ? nn : 0;
-    load4(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, n, h[k]);
-    if constexpr (!kHeads) {
-      load4(p.A + ch * p.dstate + n0, n, a[k]);
+    load4<kStream>(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, ch < p.dim ? nn : 0, h[k]);
+  }
+  if constexpr (!kHeads) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t ch = first_ch + k * CPW;
+      load4<false>(p.A + ch * p.dstate + n0, ch < p.dim ? nn : 0, a[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[k][i] *= kLog2e;
     }
@@ -151,33 +176,39 @@ __global__ __launch_bounds__(64 * kWaves) void state_step_kernel(StepParams p) {
   for (int k = 0; k < CH; ++k) {
     const int64_t ch = first_ch + k * CPW;
     const int n = ch < p.dim ? nn : 0;
-    store_run<float, 4>(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, n, h[k]);
+    store4<kStream>(p.state + (int64_t(slot) * p.dim + ch) * p.dstate + n0, n, h[k]);
   }
 }
 
-template <typename Elem, int LG, int CH>
+template <typename Elem, int LG, int CH, bool kStream>
 void run_ch(const StepArgs& a, const StepParams& p, hipStream_t s) {
   constexpr int per = kWaves * CH * (64 >> LG);
-  const dim3 grid(unsigned((a.dim + per - 1) / per), unsigned(a.batch));
+  const dim3 grid(unsigned((a.dim + per - 1) / per), unsigned(a.batch)), block(64 * kWaves);
   if (a.headdim)
-    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, true>), grid, dim3(64 * kWaves), 0, s, p);
+    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, true, kStream>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, false>), grid, dim3(64 * kWaves), 0, s, p);
+    hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, false, kStream>), grid, block, 0, s, p);
 }
 
 // Eight channels per lane (fewer where a wave has no lane per channel) while that leaves a wave
 // for every slot of the device, 8192; two below, for more waves. Mamba-2, 64 heads x 64, 128
-// states: 256 rows take 197 us with eight channels (205 with four, 284 with two, 200 with
-// sixteen), 5.5 TB/s, as a large copy; 32 heads, 8 rows take 5.9 us with two (5.9 with four,
-// 7.9 with one).
+// states, 256 rows, all through the caches: 197 us with eight channels, 205 with four, 284 with
+// two, 200 with sixteen; 32 heads, 8 rows take 5.0 us with two (as with four, 7.9 with one).
+// States of 128 MiB or more, half of what holds the last call's, go past the caches, which they
+// would fill for nothing: those 256 rows then take 179 us, 6.0 TB/s (a copy of as much: 5.2).
+// With three caches in turn, us, past and through: Mamba-1 256 rows of 4096 channels, 64 states
+// 107 and 164, 512 rows, 16 states 60 and 85, Mamba-2 256 rows, 64 heads x 64, 64 states 96 and
+// 107; but of 64 MiB, 256 rows of 4096 channels, 16 states, 40 and 32.
 template <typename Elem, int LG>
 void run_lg(const StepArgs& a, const StepParams& p, hipStream_t s) {
   constexpr int most = (1 << LG) < 8 ? (1 << LG) : 8;
   constexpr int few = most < 2 ? most : 2;
   if (a.dim * a.batch / (most * (64 >> LG)) < 8192)
-    run_ch<Elem, LG, few>(a, p, s);
+    run_ch<Elem, LG, few, false>(a, p, s);
+  else if (a.batch * a.dim * a.dstate * 4 < (int64_t(1) << 27))
+    run_ch<Elem, LG, most, false>(a, p, s);
   else
-    run_ch<Elem, LG, most>(a, p, s);
+    run_ch<Elem, LG, most, true>(a, p, s);
 }
 
 template <typename Elem>

@@ -137,6 +137,40 @@ def test_step_cache_past_32_bits():
     check(out, ref, WATCH["bf16"], "out")
 
 
+@pytest.mark.parametrize("heads,dim,n,b", [(None, 5617, 100, 70), (64, 4288, 30, 290)])
+def test_step_states_past_the_caches(heads, dim, n, b):
+    """More states than the caches hold (128 MiB and more): every row as in calls of a few
+    rows, which take another variant, bit for bit, repeated and missing slots among them; and
+    two of them against the oracle."""
+    announce(f"step of {b * dim * n * 4 >> 20} MiB of states, heads {heads}")
+    t = torch()
+    v = make(b, dim, n, heads, "bf16", 3, 575)
+    state = v["state"][0].repeat((b + 2) // 3 + 2, 1, 1)
+    nslots = state.shape[0]
+    slots = [(i * 7 + 3) % nslots for i in range(b)]
+    slots[5], slots[b - 1], slots[9] = slots[2], slots[2], -1
+    entry = ssm.scan_step if heads is None else ssm.ssd_step
+    names = ("delta_bias", "delta_softplus") if heads is None else ("dt_bias", "dt_softplus")
+
+    def call(lo, hi, st):
+        r = {k: v[k][0][lo:hi] for k in ("x", "dt", "B", "C", "z")}
+        return entry(r["x"], r["dt"], v["A"][0], r["B"], r["C"], st, D=v["D"][0], z=r["z"],
+                     slots=t.tensor(slots[lo:hi], dtype=t.int32, device="cuda"),
+                     **dict(zip(names, (v["bias"][0], True))))
+    few = state.clone()
+    parts = t.cat([call(lo, min(lo + 10, b), few) for lo in range(0, b, 10)])
+    out = call(0, b, state)
+    assert same(out, parts) and same(state, few)
+    rows = [1, b - 2]
+    assert slots.count(slots[1]) == slots.count(slots[b - 2]) == 1
+    before = v["state"][1][[slots[i] % 3 for i in rows]]
+    ref, after = ob.step_ref(*(v[k][1][rows] for k in ("x", "dt")), host(v["A"][0]),
+                             v["B"][1][rows], v["C"][1][rows], before, v["D"][1],
+                             v["z"][1][rows], v["bias"][1], True, None)
+    check(out[rows], ref, WATCH["bf16"], "out")
+    check(state[[slots[i] for i in rows]], after, STATE_TOL, "state")
+
+
 def test_step_nonfinite_rows_stay_apart():
     announce("step non-finite")
     t = torch()
