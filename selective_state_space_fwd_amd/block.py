@@ -137,10 +137,11 @@ def ssm_norm_bwd_workspace_bytes(batch, dim, groups, seqlen, flags) -> int:
 
 # ------------------------------------------------------------------ checks and the call
 #
-# A decode loop makes these calls once per layer and token. Where every argument is what the C ABI
-# takes as it stands, the functions below go through csrc/binding.cpp, which looks at them in C++ and returns None, having done nothing, when one is not; the checks
-# here then copy what needs copying and name what is wrong. (conv_step of 8 rows: 4.5 us a call
-# there, 8.4 here, of which the launch is 3; ssd_step 5.0 and 11.6.)
+# A decode loop makes these calls once per layer and token. Where every argument is what the C
+# ABI takes as it stands, the functions below go through csrc/binding.cpp, which looks at them in
+# C++ and returns None, having done nothing, when one is not; the checks here then copy what
+# needs copying and name what is wrong. (conv_step of 8 rows: 4.5 us a call there, 8.4 here, of
+# which the launch is 3; ssd_step 5.0 and 11.6.)
 
 def _io_flag(name, t) -> int:
     dtype = t.dtype

@@ -1,7 +1,7 @@
 // The short way from Python into the entry points of block.py (conv, conv_step, scan_step,
 // ssd_step, norm and the gradients), which a decode loop or a training step makes once per layer
-// and where marshalling through ctypes can take longer than the kernels. Each function here takes the arguments of its Python
-// namesake in order, and either
+// and where marshalling through ctypes can take longer than the kernels. Each function here takes
+// the arguments of its Python namesake in order, and either
 //   * makes the call, when every argument is what the C ABI takes as it stands (a device tensor
 //     of the right dtype and shape, on the current device, contiguous or strided where the ABI
 //     takes strides), and returns its result, or
@@ -96,13 +96,20 @@ int device_of(const Arg& t) {
 
 void* stream_of(int dev) { return c10::hip::getCurrentHIPStream(dev).stream(); }
 
+// The interpreter's lock given up, and taken back however the scope ends.
+struct Unlocked {
+  PyThreadState* s = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(s); }
+};
+
 // The call f() without the interpreter's lock; false with the error set if it fails.
 template <typename F>
 bool made(F f) {
   int status;
-  Py_BEGIN_ALLOW_THREADS;
-  status = f();
-  Py_END_ALLOW_THREADS;
+  {
+    const Unlocked u;
+    status = f();
+  }
   if (status == SSM_OK) return true;
   PyObject* e = PyObject_CallFunction(g_error, "i", status);
   if (e) {
@@ -312,11 +319,13 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor made_out, rstd;
   if (!out) made_out = token ? at::empty({b, L, d}, y->options()) : at::empty({b, d, L}, y->options());
   if (save) rstd = at::empty({b, groups, L}, y->options().dtype(at::kFloat));
-  // (not needed, and not made, for a decode step: channels contiguous throughout)
+  // Not needed, and not made, for a decode step: channels contiguous throughout, and nothing that
+  // the library could take for steps contiguous (one channel, or both at once).
   at::Tensor made_ws;
   int64_t bytes = 0;
   void* wp = nullptr;
-  if (y->stride(1) != 1 || (z && z->stride(1) != 1) || !(token || L == 1) || d / groups > 4096) {
+  const auto channels = [&](const Arg& t) { return t->stride(1) == 1 && (L == 1 || t->stride(2) != 1); };
+  if (d == 1 || !channels(y) || (z && !channels(z)) || !(token || L == 1) || d / groups > 4096) {
     wp = workspace_of(Arg(Py_None, &ok), g_norm_fwd_ws(b, d, groups, L, uint32_t(io)), dev, *y.t, &made_ws, &bytes);
     SSM_NEED(wp);
   }

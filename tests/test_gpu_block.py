@@ -15,6 +15,7 @@ from gpu_util import announce, dev, host, torch
 from oracle import block as ob
 from ssm_workloads import RTOL, RTOL_STATE, WATCH
 from test_gpu_graph import unrelated_eager_work
+from test_gpu_norm import grad_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -316,6 +317,106 @@ def test_both_ways_of_marshalling_agree(monkeypatch):
     monkeypatch.setattr(block, "_binding", Never)
     for a, c in zip(native, calls()):
         assert a.shape == c.shape and a.stride() == c.stride() and same(a.contiguous(), c.contiguous())
+
+
+@pytest.mark.parametrize("L", [1, 5])
+@pytest.mark.parametrize("d", [1, 6])
+def test_norm_of_views_contiguous_both_ways(d, L):
+    """One channel, one step, and overlapping views whose steps and channels are both one element
+    apart: every such y and z, both results' orders, gradients included."""
+    announce(f"norm views contiguous both ways d{d} L{L}")
+    t = torch()
+    r = Rand(770 + 10 * d + L)
+    b = 2
+    kinds = []
+    for _ in range(2):
+        v = r((b, d, L))
+        token = v[0].transpose(1, 2).contiguous().transpose(1, 2)
+        flat = r((b * (d + L),))[0]
+        both = flat.as_strided((b, d, L), (d + L - 1, 1, 1))
+        kinds.append([v[0], token, both])
+    w, w64 = r((d,))
+    dout, dout64 = r((b, d, L))
+    for y in kinds[0]:
+        for z in [None] + kinds[1]:
+            for token in (False, True):
+                z64 = None if z is None else host(z)
+                out, rstd = ssm.norm_train(y, w, z=z, token_major=token)
+                ref, rref = ob.norm_ref(host(y), w64, z64, 1e-5, 1)
+                check(out, ref.transpose(0, 2, 1) if token else ref, TOL["f32"], "out")
+                g = ssm.norm_backward(y, w, rstd, dout.transpose(1, 2) if token else dout, z=z,
+                                      token_major=token)
+                c = ssm.norm_backward(y.contiguous(), w, rstd, dout,
+                                      z=None if z is None else z.contiguous())
+                for k in g:
+                    assert g[k] is c[k] is None or same(g[k].contiguous(), c[k].contiguous()), k
+
+
+@pytest.mark.parametrize("L", [1, 9])
+def test_gradients_of_sums(L):
+    """The gradient that a sum hands back is one element read everywhere (strides of zero)."""
+    announce(f"gradients of sums L{L}")
+    t = torch()
+    r = Rand(780 + L)
+    v = {k: r(s) for k, s in
+         (("y", (2, 20, L)), ("w", (20, 4)), ("weight", (20,)), ("z", (2, 20, L)))}
+    x, w, nw, z = (v[k][0].requires_grad_() for k in ("y", "w", "weight", "z"))
+    ones = np.ones((2, 20, L))
+    v["dout"] = (None, ones)
+    tol = grad_tol("f32", v, (2, 20, L, 1), "gate_first")
+    ref = ob.norm_bwd_ref(v["y"][1], v["weight"][1], ones, v["z"][1], 1e-5)
+    for token in (False, True):
+        out = ssm.gated_norm(x, nw, z=z, token_major=token)
+        dy, dweight, dz = t.autograd.grad(out.sum(), [x, nw, z])
+        check(dy, ref["dy"], tol, "dy")
+        check(dz, ref["dz"], tol, "dz")
+        check(dweight, ref["dweight"], sum_tol(2 * L), "norm dweight")
+    ref = ob.conv_bwd_ref(v["y"][1], v["w"][1], ones, silu=True, dfinal=np.ones((2, 20, 3)))
+    out, fin = ssm.causal_conv(x, w, silu=True)
+    dx, dw = t.autograd.grad(out.sum() + fin.sum(), [x, w])
+    check(dx, ref["dx"], TOL["f32"], "dx")
+    check(dw, ref["dweight"], sum_tol(2 * L), "conv dweight")
+
+
+@pytest.mark.parametrize("order", ["time", "channel"])
+def test_tensors_past_32_bits(order):
+    """More than 2^31 elements: the last batch row of the convolution and of the norm, both
+    directions, as a call of that row alone gives it, bit for bit."""
+    announce(f"tensors past 32 bits {order}")
+    t = torch()
+    d, L = 1031, 1050001
+    assert 2 * d * L > 1 << 31
+    g = t.Generator("cuda").manual_seed(790)
+    shape = (2, d, L) if order == "time" else (2, L, d)
+    draw = lambda: t.randn(shape, device="cuda", dtype=t.bfloat16, generator=g)
+    view = (lambda v: v) if order == "time" else (lambda v: v.transpose(1, 2))
+    x = view(draw())
+    w, nw = t.randn(d, 4, device="cuda", generator=g), t.randn(d, device="cuda", generator=g)
+    lengths = t.tensor([5, L - 3], dtype=t.int32, device="cuda")
+
+    def equal(a, c, label):
+        assert a.stride()[1:] == c.stride()[1:]
+        dense = lambda v: v if v.is_contiguous() else v.transpose(1, 2)
+        assert t.equal(dense(a[1:]).view(t.int16 if a.dtype == t.bfloat16 else t.int32),
+                       dense(c).view(t.int16 if a.dtype == t.bfloat16 else t.int32)), label
+
+    out, fin = ssm.conv(x, w, silu=True, lengths=lengths)
+    out1, fin1 = ssm.conv(x[1:], w, silu=True, lengths=lengths[1:])
+    equal(out, out1, "conv")
+    equal(fin, fin1, "final state")
+    assert not out[0, :, 5:].any()
+    dx = ssm.conv_backward(x, w, out, silu=True, lengths=lengths)["dx"]
+    equal(dx, ssm.conv_backward(x[1:], w, out1, silu=True, lengths=lengths[1:])["dx"], "conv dx")
+    del out, out1, dx
+    out, rstd = ssm.norm_train(x, nw, z=x, token_major=order == "channel")
+    out1, rstd1 = ssm.norm_train(x[1:], nw, z=x[1:], token_major=order == "channel")
+    equal(out, out1, "norm")
+    equal(rstd, rstd1, "rstd")
+    gr = ssm.norm_backward(x, nw, rstd, out, z=x, token_major=order == "channel")
+    gr1 = ssm.norm_backward(x[1:], nw, rstd1, out1, z=x[1:], token_major=order == "channel")
+    equal(gr["dy"], gr1["dy"], "norm dy")
+    equal(gr["dz"], gr1["dz"], "norm dz")
+    assert bool(t.isfinite(gr["dweight"]).all())
 
 
 def test_outputs_given_and_arguments_copied():
