@@ -16,7 +16,7 @@
 // length do not count; its outputs there are zeros.
 //
 // b4, 2304 channels, 2048 steps, bf16 (75 MB in and out, 12 us by a library copy of that size):
-// 15.5 us channel order, 16 us time order, by the kernel trace. What that took: no branch
+// 15.2 us channel order, 16 us time order, by the kernel trace. What that took: no branch
 // around a load (23 -> 16 us, with the weights of a workgroup in LDS instead of a load per
 // channel that is waited for), index arithmetic of 32 bits (time order 20 -> 16: it was VALU
 // bound), stores past L2 (1 us). Eight channels a lane 17.7 us, sixteen-channel waves 28 us.
