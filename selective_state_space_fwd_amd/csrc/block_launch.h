@@ -213,7 +213,11 @@ inline int64_t norm_run_bytes(const NormShape& s, Io io) {
 inline NormShape norm_fwd_shape(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, Io io,
                                 NormOrders o) {
   const int steps = kNormFwdSteps[int(io)];
-  const NormShape s = norm_whole_shape(dim / groups, seqlen, io, o.all_channel ? 1 : steps, 8);
+  NormShape s = norm_whole_shape(dim / groups, seqlen, io, o.all_channel ? 1 : steps, 8);
+  if (!o.all_channel && norm_run_bytes(s, io) < 32) {
+    const NormShape more = norm_whole_shape(dim / groups, seqlen, io, steps, kNormMostWaves);
+    if (more.tiles * groups * batch >= 192 && norm_run_bytes(more, io) >= 32) s = more;
+  }
   const bool split = s.waves > kNormMostWaves ||
                      (!o.all_channel && !o.dword_rows && norm_run_bytes(s, io) < 32 && seqlen > steps);
   return split ? norm_split_shape(dim / groups, seqlen, io, steps) : s;

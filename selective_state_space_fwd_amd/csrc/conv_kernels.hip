@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_time(ConvParams p) {
 
 // ---------------------------------------------------------------- channel order
 
-// Words of the steps t .. t + N - 1, of nc channels from p's on. A step outside the sequence
+// Words of the steps t .. t + N - 1, of nc (> 0) channels from p's on. A step outside the sequence
 // takes the nearest one's word, so that the loads need no branch: the callers replace what lies
 // before the first step by the initial state and let nothing at or behind a row's end count.
 template <typename Elem, int CV>
@@ -217,10 +217,16 @@ __device__ __forceinline__ void load_rows(const Elem* p, int64_t pitch, int64_t 
 #pragma unroll
     for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const Word<Elem, CV>*>(at[i]);
   } else {
+    Elem e[N][CV];  // (past nc the last channel again: no branch around a load here either)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < CV; ++c) e[i][c] = at[i][c < nc ? c : nc - 1];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[CV];
-      load_few<Elem, CV>(at[i], nc, v);
+#pragma unroll
+      for (int c = 0; c < CV; ++c) v[c] = c < nc ? widen<Elem>(e[i][c]) : 0.0f;
       pack_few<Elem, CV>(v, raw[i]);
     }
   }
@@ -544,9 +550,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 4 : 3) void conv_bwd_
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) g[S + i] = few_elem<Elem>(gnext[c], i);
       } else {
-#pragma unroll
-        for (int i = 0; i < S + W - 1; ++i)
-          g[i] = c < a.nc && i < n ? widen<Elem>(gb[int64_t(c) * p.seqlen + i]) : 0.0f;
+        load_part_of<Elem, S + W - 1>(gb + int64_t(c) * p.seqlen, c >= a.nc ? 0 : n < S + W - 1 ? n : S + W - 1, g);
       }
 #pragma unroll
       for (int i = 0; i < S + 2 * (W - 1); ++i) e[i] = few_elem<Elem>(raw[i], c);

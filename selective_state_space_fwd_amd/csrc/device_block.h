@@ -76,6 +76,22 @@ __device__ __forceinline__ uint4 narrow_raw16<uint16_t>(const float* v) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+// The n (< C) values from p on, the rest zero (nothing past n is read). What lies past n takes
+// the last value's address instead of a branch, so that the loads are one trip to memory and not
+// one each.
+template <typename Elem, int C>
+__device__ __forceinline__ void load_part_of(const Elem* p, int n, float (&v)[C]) {
+  Elem e[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) e[i] = Elem(0);
+  if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) e[i] = p[i < n ? i : n - 1];
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] = i < n ? widen<Elem>(e[i]) : 0.0f;
+}
+
 // v[i] = p[i] for i < n, 0 past it (nothing past it is read). S a multiple of the word.
 template <typename Elem, int S>
 __device__ __forceinline__ void load_run(const Elem* p, int n, float (&v)[S]) {
@@ -84,8 +100,7 @@ __device__ __forceinline__ void load_run(const Elem* p, int n, float (&v)[S]) {
 #pragma unroll
     for (int q = 0; q < S / N; ++q) widen_raw16<Elem>(load16_any(p + q * N), v + q * N);
   } else {
-#pragma unroll
-    for (int i = 0; i < S; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
+    load_part_of<Elem, S>(p, n, v);
   }
 }
 
@@ -152,8 +167,7 @@ __device__ __forceinline__ void load_few(const Elem* p, int n, float (&v)[C]) {
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = few_elem<Elem>(d, i);
   } else {
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
+    load_part_of<Elem, C>(p, n, v);
   }
 }
 

@@ -15,7 +15,7 @@
 // Bound by memory: 3 reads and writes per element forward, 5 backward. b4, 2048 channels, 2048
 // steps, bf16, y in the scan's order, z and the result in a projection's: forward 19.5 us (100
 // MB, 5.2 TB/s, the rate of a large copy), gradient 44 us (168 MB, 3.8 TB/s) and 4 for the sums
-// of dweight. The gradient's loads and its arithmetic (20 us, with four transcendentals per
+// of dweight. The gradient's loads and its arithmetic (20 us, with two transcendentals per
 // element) overlap in part only: a CU holds one workgroup of sixteen waves.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
