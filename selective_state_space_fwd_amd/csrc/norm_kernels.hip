@@ -128,32 +128,76 @@ __device__ __forceinline__ void store_part(Elem* p, int n, const Dwords<C * int(
   store_few<Elem, C>(p, n, v);
 }
 
-// The square at (b, channel c0, step t0): nc channels and nt steps of it exist (<= 0: none).
-// Whole squares take straight-line loads of whole words; the others go word by word.
+// d moved down by k elements (zeros come in at the top).
+template <typename Elem, int N>
+__device__ __forceinline__ void move_down(Dwords<N>& d, int k) {
+  const int dwords = sizeof(Elem) == 2 ? k >> 1 : k;
+#pragma unroll
+  for (int s = 1; s < N; s *= 2) {
+    const bool on = (dwords & s) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) d.w[i] = on ? (i + s < N ? d.w[i + s < N ? i + s : 0] : 0u) : d.w[i];
+  }
+  if constexpr (sizeof(Elem) == 2) {
+    const bool on = (k & 1) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t above = i + 1 < N ? d.w[i + 1 < N ? i + 1 : 0] : 0u;
+      d.w[i] = on ? (d.w[i] >> 16) | (above << 16) : d.w[i];
+    }
+  }
+}
+
+// N words `pitch` apart from p on, of which the first n (0 < n) exist, and of each its first nv (0 <
+// nv) of kSize elements, zeros for the rest. What does not exist is not read: a word past n is
+// the last one again, and each is read from kSize - nv elements further down, which exist, and
+// moved. No branch around a load, so one trip to memory for all.
+template <typename Elem, int kSize, int N>
+__device__ __forceinline__ void load_edge(const Elem* p, int64_t pitch, int n, int nv,
+                                          Dwords<kSize * int(sizeof(Elem)) / 4> (&d)[N]) {
+  const int k = kSize - nv;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    d[i] = *reinterpret_cast<const Dwords<kSize * int(sizeof(Elem)) / 4>*>(p - k + (i < n ? i : n - 1) * pitch);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    move_down<Elem>(d[i], k);
+#pragma unroll
+    for (uint32_t& w : d[i].w) w = i < n ? w : 0u;
+  }
+}
+
+// The square at (b, channel c0, step t0): nc channels and nt steps of it exist (<= 0: none), zeros
+// for the rest. Whole squares take straight-line loads of whole words; those that the end of the
+// group or the sequence cuts too, if either is as long as a word; the others go word by word.
 template <typename Elem, int kSteps>
-__device__ __forceinline__ void load_square(const Tensor& x, int b, int64_t c0, int64_t t0, int nc, int nt,
-                                            Square<Elem, kSteps>& s) {
+__device__ __forceinline__ void load_square(const NormParams& p, const Tensor& x, int b, int64_t c0, int64_t t0,
+                                            int nc, int nt, Square<Elem, kSteps>& s) {
   using Sq = Square<Elem, kSteps>;
   constexpr int CV = Sq::CV;
-  const Elem* p = static_cast<const Elem*>(x.p) + b * x.b + c0 * x.c + t0 * x.t;
+  const Elem* at = static_cast<const Elem*>(x.p) + b * x.b + c0 * x.c + t0 * x.t;
   if constexpr (kSteps == 1) {
-    load_part<Elem, CV>(p, nt > 0 ? nc : 0, s.w[0]);
+    load_part<Elem, CV>(at, nt > 0 ? nc : 0, s.w[0]);
   } else if (x.chan) {
     Dwords<4> rows[kSteps];
     if (nc == CV && nt == kSteps) {
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) rows[t] = *reinterpret_cast<const Dwords<4>*>(p + t * x.t);
+      for (int t = 0; t < kSteps; ++t) rows[t] = *reinterpret_cast<const Dwords<4>*>(at + t * x.t);
+    } else if (p.g >= CV && nc > 0 && nt > 0) {
+      load_edge<Elem, CV, kSteps>(at, x.t, nt, nc, rows);
     } else {
 #pragma unroll
-      for (int t = 0; t < kSteps; ++t) load_part<Elem, CV>(p + t * x.t, t < nt ? nc : 0, rows[t]);
+      for (int t = 0; t < kSteps; ++t) load_part<Elem, CV>(at + t * x.t, t < nt ? nc : 0, rows[t]);
     }
     turn<Elem, kSteps>(rows, s);
   } else if (nc == CV && nt == kSteps) {
 #pragma unroll
-    for (int c = 0; c < CV; ++c) s.w[c] = *reinterpret_cast<const typename Sq::Word*>(p + c * x.c);
+    for (int c = 0; c < CV; ++c) s.w[c] = *reinterpret_cast<const typename Sq::Word*>(at + c * x.c);
+  } else if (p.seqlen >= kSteps && nc > 0 && nt > 0) {
+    load_edge<Elem, kSteps, CV>(at, x.c, nc, nt, s.w);
   } else {
 #pragma unroll
-    for (int c = 0; c < CV; ++c) load_part<Elem, kSteps>(p + c * x.c, c < nc ? nt : 0, s.w[c]);
+    for (int c = 0; c < CV; ++c) load_part<Elem, kSteps>(at + c * x.c, c < nc ? nt : 0, s.w[c]);
   }
 }
 
@@ -339,9 +383,9 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParam
   float q[CV][kSteps], sum[kSteps];  // q: y s, the result but for w r
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) sum[t] = 0.0f;
-  load_square<Elem, kSteps>(p.y, a.b, base, a.t0, nc, a.nt, y);
+  load_square<Elem, kSteps>(p, p.y, a.b, base, a.t0, nc, a.nt, y);
   if constexpr (kMode == kGateFirst || (kMode == kNormFirst && kPhase != kSums))
-    load_square<Elem, kSteps>(p.z, a.b, base, a.t0, nc, a.nt, z);
+    load_square<Elem, kSteps>(p, p.z, a.b, base, a.t0, nc, a.nt, z);
 #pragma unroll
   for (int c = 0; c < CV; ++c) {
 #pragma unroll
@@ -401,9 +445,9 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParam
   const int nc = channels_left<CV>(p, a.c0);
   Square<Elem, kSteps> y, z, g;
   float w[CV], sum[kSteps], r[kSteps], sigma[CV][kSteps];
-  load_square<Elem, kSteps>(p.y, a.b, base, a.t0, nc, a.nt, y);
-  if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p.z, a.b, base, a.t0, nc, a.nt, z);
-  load_square<Elem, kSteps>(p.dout, a.b, base, a.t0, nc, a.nt, g);
+  load_square<Elem, kSteps>(p, p.y, a.b, base, a.t0, nc, a.nt, y);
+  if constexpr (kMode != kNoGate) load_square<Elem, kSteps>(p, p.z, a.b, base, a.t0, nc, a.nt, z);
+  load_square<Elem, kSteps>(p, p.dout, a.b, base, a.t0, nc, a.nt, g);
   load_run<float, CV>(p.weight + base, nc, w);
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
