@@ -158,7 +158,7 @@ struct NormShape {
 };
 
 // all_channel: every tensor has its channels contiguous. dword_rows: every row of steps of the
-// others starts at a multiple of four bytes.
+// others (forward: of the result, if it is one) starts at a multiple of four bytes.
 struct NormOrders {
   bool all_channel, dword_rows;
 };
@@ -205,11 +205,13 @@ inline int64_t norm_run_bytes(const NormShape& s, Io io) {
 }
 
 // all_channel: a lane holds one step. Else eight steps (bf16): b4, 2048 channels, 2048 steps
-// take 19.5 us with eight waves a workgroup (100 MB: 5.2 TB/s), 21.8 with four, 20.1 with
-// sixteen, and 21.4 with four steps a lane. Split where a group does not fit, and where a
-// workgroup would read 16 bytes on end at odd addresses: b1, 5691 channels, 773 steps, all
-// tensors so ordered, take 58 us whole and 32 split (776 steps: 24 and 23; b4, 2048 channels,
-// 2048 steps: 20 and 33).
+// take 20 us with eight waves a workgroup (100 MB: 5.1 TB/s), 21.8 with four, 21 with sixteen,
+// and 21.4 with four steps a lane. Sixteen waves where eight would read less than 32 bytes on
+// end, if that leaves workgroups for most CUs: b4, 2048 channels, 2048 steps, fp32, all tensors
+// so ordered, 57 and 41 us; b4, 4096 channels, 2048 steps, bf16, 57 and 43 (but b1, 4096
+// channels, 1024 steps, 64 workgroups, 11 and 15). Split where a group does not fit, and where a
+// workgroup would write 16 bytes on end of a result at odd addresses: b1, 4096 channels, 1023
+// steps, 27 us whole and 19 split; with the result in channel order 13 and 18.
 inline NormShape norm_fwd_shape(int64_t batch, int64_t dim, int64_t groups, int64_t seqlen, Io io,
                                 NormOrders o) {
   const int steps = kNormFwdSteps[int(io)];

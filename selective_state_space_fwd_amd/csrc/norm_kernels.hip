@@ -630,7 +630,8 @@ NormOrders orders_of(const NormArgs& a, std::initializer_list<const View*> views
 }  // namespace
 
 int launch_norm_fwd(const NormArgs& a, void* stream) {
-  const NormShape s = norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, orders_of(a, {&a.y, &a.z, &a.out}));
+  const NormOrders all = orders_of(a, {&a.y, &a.z, &a.out}), result = orders_of(a, {&a.out});
+  const NormShape s = norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, {all.all_channel, result.dword_rows});
   NormParams p = params_of(a, s);
   p.split = a.workspace;
   hipStream_t st = static_cast<hipStream_t>(stream);
