@@ -20,7 +20,7 @@
 // around a load (23 -> 16 us, with the weights of a workgroup in LDS instead of a load per
 // channel that is waited for), index arithmetic of 32 bits (time order 20 -> 16: it was VALU
 // bound), stores past L2 (1 us). Eight channels a lane 17.7 us, sixteen-channel waves 28 us.
-// The gradient (113 MB): 32.5 us channel order, 28.5 us time order, of which the VALU needs 21
+// The gradient (113 MB): 30.5 us channel order, 28.5 us time order, of which the VALU needs 21
 // (a sigmoid for 11 steps of each 8); 43 us with workgroups in plain order, where an XCD's
 // tiles all lie at one offset of the 4096-byte rows and so in two of its L2's channels.
 #include <hip/hip_runtime.h>
