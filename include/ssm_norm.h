@@ -19,7 +19,9 @@
  *            element once.
  *   weight, dweight : [dim] fp32
  *   rstd     : [batch, groups, seqlen] fp32, r of every token and group
- * Sums are fp32; results are rounded to the storage type once. Calls are asynchronous on
+ * Sums are fp32; results are rounded to the storage type once. The squares are fp32 too: a token
+ * whose mean square (plus eps) is no normal fp32 number, values below some 1e-18 with eps 0 or
+ * above 1e18, has no r. Calls are asynchronous on
  * `stream`, use no atomics (bitwise reproducible) and allocate nothing; every check happens
  * before any HIP call. Outputs must overlap no other argument (a strided array counts with its
  * whole extent). Returns SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (a storage type other

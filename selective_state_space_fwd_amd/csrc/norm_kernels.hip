@@ -432,8 +432,10 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_fwd_kernel(NormParam
 
 // ---------------------------------------------------------------- backward
 //
-// gate first: A = w dout;    S = sum_G A v; dv = r (A - v r^2 S / G); dy = dv s; dz = dv y s'
-// norm first: A = w dout s;  S = sum_G A y; dy = r (A - y r^2 S / G); dz = w dout y r s'
+// gate first: A = w dout;    n = v r, k = r S / G, S = sum_G A v; dv = r (A - n k); dy = dv s; dz = dv y s'
+// norm first: A = w dout s;  n = y r, k = r S / G, S = sum_G A y; dy = r (A - n k); dz = w dout n s'
+// n is of order one and k of A's, so no power of r but the first is formed: r^3 alone would leave
+// float32's range for values of 1e13 (and 1e-13, eps 0), long before their squares do.
 // dweight = sum over tokens of dout (s) times the normed value; per workgroup and channel
 // here, over workgroups by a second launch in a fixed order.
 template <typename Elem, int kSteps, int kPhase, int kMode>
@@ -478,9 +480,9 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParam
     store_sums<kSteps>(p, a, sum);
     return;
   }
-  float m[kSteps];  // r^3 S / G
+  float k[kSteps];
 #pragma unroll
-  for (int t = 0; t < kSteps; ++t) m[t] = r[t] * r[t] * r[t] * (sum[t] * p.inv_g);
+  for (int t = 0; t < kSteps; ++t) k[t] = r[t] * (sum[t] * p.inv_g);
   forget<Elem, kSteps>(y);
   forget<Elem, kSteps>(g);
   if constexpr (kMode != kNoGate) forget<Elem, kSteps>(z);
@@ -500,14 +502,16 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParam
         s = zv * sg;
         ds = __builtin_fmaf(s, 1.0f - sg, sg);
       }
-      const float gr = gv * r[t], v = kMode == kNoGate ? yv : yv * s;
-      dw[c] = __builtin_fmaf(gr, v, dw[c]);
+      const float wg = w[c] * gv;
       if constexpr (kMode == kNormFirst) {
-        const float a1 = w[c] * gr;
-        dy[t] = __builtin_fmaf(-yv, m[t], a1 * s);
-        dz[t] = a1 * (yv * ds);
+        const float n = yv * r[t];
+        dw[c] = __builtin_fmaf(gv, n * s, dw[c]);
+        dy[t] = r[t] * __builtin_fmaf(-n, k[t], wg * s);
+        dz[t] = wg * (n * ds);
       } else {
-        const float dv = __builtin_fmaf(-v, m[t], w[c] * gr);
+        const float n = (kMode == kNoGate ? yv : yv * s) * r[t];
+        dw[c] = __builtin_fmaf(gv, n, dw[c]);
+        const float dv = r[t] * __builtin_fmaf(-n, k[t], wg);
         dy[t] = dv * s;
         dz[t] = dv * (yv * ds);
       }
