@@ -69,6 +69,20 @@ constexpr int kConvLaneChannels = 4;
 constexpr int64_t kConvChannelTileSteps =
     int64_t(kConvSteps) * (64 * kConvLaneChannels / kConvWaveChannels) * kConvWaves;
 
+// Consecutive tiles of a row that a wave of the time-ordered forward takes: two in bf16, for half the
+// index arithmetic, by which bf16 is bound, once a row has two and one a wave gives twice the
+// waves the device holds at a time. b4, 2304 channels, 2048 steps: 15.4 us against 16.9 (four
+// tiles 17.9); b4, 3328 channels, 1536 steps (three tiles) 19.6 and 20.1; but b4, 4096 channels,
+// 512 steps (one) 11.3 and 9.3; b16, 6000 channels, 100 steps 17.5 and 13.6. Few waves (b5, 523
+// channels, 777 steps): 5.8 and 5.2. fp32, which memory binds (1536 channels, 65536 steps): 152
+// and 147.
+inline int conv_fwd_wave_tiles(int64_t batch, int64_t dim, int64_t seqlen, Io io) {
+  const int lg = conv_row_lanes_log2(seqlen);
+  const int64_t tile = int64_t(kConvSteps) << lg;
+  const int64_t waves = batch * dim * ((seqlen + tile - 1) / tile) >> (6 - lg);
+  return io == Io::BF16 && seqlen > tile && waves >= 16384 ? 2 : 1;
+}
+
 // Tiles of one row that one wave of the time-ordered backward walks.
 constexpr int kConvBwdTiles = 4;
 

@@ -666,19 +666,13 @@ void run_fwd_time(const ConvArgs& a, ConvParams& p, hipStream_t s) {
   hipLaunchKernelGGL((conv_fwd_time<Elem, W, T>), grid, dim3(kThreads), 0, s, p);
 }
 
-// Two tiles a wave in bf16 once one a wave gives twice the waves the device holds at a time:
-// half the index arithmetic, by which bf16 is bound (b4, 2304 channels, 2048 steps: 15.5 us
-// against 17.7; four tiles 17.9). One otherwise (b5, 523 channels, 777 steps: 5.2 us against
-// 5.8), and in fp32, which memory binds (1536 channels, 65536 steps: 147 us against 152).
 template <typename Elem, int W>
 void run_fwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
   if (a.order == Order::Time || a.seqlen == 0) {
-    const int64_t tile = int64_t(S) << p.lanes_log2;
-    const int64_t waves = a.batch * a.dim * ((a.seqlen + tile - 1) / tile) >> (6 - p.lanes_log2);
-    if (sizeof(Elem) == 2 && waves >= 16384)
-      run_fwd_time<Elem, W, 2>(a, p, s);
-    else
-      run_fwd_time<Elem, W, 1>(a, p, s);
+    if constexpr (sizeof(Elem) == 2) {
+      if (conv_fwd_wave_tiles(a.batch, a.dim, a.seqlen, a.io) == 2) return run_fwd_time<Elem, W, 2>(a, p, s);
+    }
+    run_fwd_time<Elem, W, 1>(a, p, s);
   } else {
     const dim3 grid = chan_grid(a, &p);
     hipLaunchKernelGGL((conv_fwd_chan<Elem, W>), grid, dim3(kThreads), 0, s, p);
