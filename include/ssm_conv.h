@@ -52,9 +52,10 @@ extern "C" {
  * final_state to the initial state. out and final_state must overlap no other argument (a
  * strided array counts with its whole extent).
  * Returns SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (width, a storage type other than
- * fp32/bf16, neither stride 1, batch above 65535, batch*dim or seqlen above 2^31 - 1, or a
- * launch of more than 2^31 - 1 waves along a batch row), SSM_ERR_MISALIGNED (a pointer not aligned to its element
- * size) or SSM_ERR_HIP.
+ * fp32/bf16, neither stride 1, batch above 65535, batch*dim or seqlen above 2^31 - 1, or more
+ * than a grid of 2^32 - 1 work-items takes: a batch row of some 2^35 elements, a gradient of
+ * 2^28 / (width + 1) channels), SSM_ERR_MISALIGNED (a pointer not aligned to its element size)
+ * or SSM_ERR_HIP.
  */
 SSM_API int ssm_conv_fwd(const void* x, const int64_t* x_strides, const float* weight,
                          const float* bias, const void* initial_state, const int32_t* lengths,

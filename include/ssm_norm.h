@@ -26,7 +26,9 @@
  * before any HIP call. Outputs must overlap no other argument (a strided array counts with its
  * whole extent). Returns SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (a storage type other
  * than fp32/bf16, neither stride 1, dim or seqlen above 2^31 - 1, tokens times groups and
- * 32-channel blocks above 2^31 - 1), SSM_ERR_MISALIGNED (a pointer not aligned to its element size) or SSM_ERR_HIP.
+ * 32-channel blocks above 2^31 - 1, or more than a grid of 2^32 - 1 work-items takes: some 2^34
+ * elements, less where groups of few channels meet sequences of few steps; a gradient of 2^27
+ * channels), SSM_ERR_MISALIGNED (a pointer not aligned to its element size) or SSM_ERR_HIP.
  */
 #ifndef SSM_NORM_H
 #define SSM_NORM_H

@@ -29,7 +29,8 @@
  * out and state must overlap no other argument. Calls are asynchronous on `stream`, bitwise
  * reproducible, and allocate nothing; every check happens before any HIP call. Returns SSM_OK,
  * SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (dstate outside [1, 256], batch above 65535, dim or
- * nslots above 2^31 - 1, a storage type other than fp32/bf16, sizes past int64), SSM_ERR_MISALIGNED
+ * nslots above 2^31 - 1, more channels than a grid of 2^32 - 1 work-items takes (2^29 of more
+ * than 128 states), a storage type other than fp32/bf16, sizes past int64), SSM_ERR_MISALIGNED
  * (a pointer not aligned to its element size) or SSM_ERR_HIP.
  */
 #ifndef SSM_STEP_H

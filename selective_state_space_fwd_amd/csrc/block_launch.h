@@ -4,6 +4,8 @@
 #pragma once
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "scan_launch.h"
 
 namespace ssm {
@@ -16,6 +18,18 @@ struct Strides {
 // Which of a tensor's axes is contiguous in memory. Time: runs of steps of one channel (what
 // the scan takes); Channel: runs of channels of one step (a projection's output).
 enum class Order : int { Time = 0, Channel = 1 };
+
+// A HIP launch takes fewer than 2^32 work-items along an axis of its grid; the C-ABI layer refuses
+// what would need more.
+inline bool grid_fits(int64_t workgroups, int64_t threads) {
+  return workgroups <= ((int64_t(1) << 32) - 1) / threads;
+}
+
+// Columns and slices of rows that a workgroup of the gradients' second launches sums.
+constexpr int kReduceCols = 32;
+constexpr int kConvReduceSlices = 16;
+constexpr int kNormReduceSlices = 32;
+inline int64_t reduce_groups(int64_t cols) { return (cols + kReduceCols - 1) / kReduceCols; }
 
 // ---------------------------------------------------------------- short causal convolution
 
@@ -86,6 +100,31 @@ inline int conv_fwd_wave_tiles(int64_t batch, int64_t dim, int64_t seqlen, Io io
 // Tiles of one row that one wave of the time-ordered backward walks.
 constexpr int kConvBwdTiles = 4;
 
+// The grid of a convolution's launch along its first axis (the second is the batch row): the runs of
+// `run` steps of a row, and workgroups of 64 * kConvWaves lanes.
+struct ConvGrid {
+  int64_t tiles, waves, groups;
+};
+
+// Time order, `wave_tiles` tiles of a row per wave.
+inline ConvGrid conv_time_grid(int64_t dim, int64_t seqlen, int wave_tiles) {
+  const int lg = conv_row_lanes_log2(seqlen);
+  const int64_t run = (int64_t(kConvSteps) << lg) * wave_tiles, rows = int64_t(1) << (6 - lg);
+  ConvGrid g;
+  g.tiles = seqlen > 0 ? (seqlen + run - 1) / run : 1;
+  g.waves = (dim + rows - 1) / rows * g.tiles;
+  g.groups = (g.waves + kConvWaves - 1) / kConvWaves;
+  return g;
+}
+
+inline ConvGrid conv_chan_grid(int64_t dim, int64_t seqlen) {
+  ConvGrid g;
+  g.tiles = (seqlen + kConvChannelTileSteps - 1) / kConvChannelTileSteps;
+  g.groups = g.tiles * ((dim + kConvWaveChannels - 1) / kConvWaveChannels);
+  g.waves = g.groups * kConvWaves;
+  return g;
+}
+
 // Partial sums of dweight and dbias per channel: one per batch row and run of steps.
 inline int64_t conv_partials(int64_t batch, int64_t seqlen, Order order) {
   const int64_t run = order == Order::Channel
@@ -134,6 +173,42 @@ struct StepArgs {
   bool softplus;
 };
 constexpr int64_t kStepMaxState = 256;
+constexpr int kStepWaves = 4;
+
+// Lanes of a channel: four states each, a power of two.
+inline int step_lanes_log2(int64_t dstate) {
+  int lg = 0;
+  while ((int64_t(4) << lg) < dstate) ++lg;
+  return lg;
+}
+
+// Channels a lane may hold (its wave has a lane for each), and those of small calls.
+constexpr int step_most_channels(int lg) { return (1 << lg) < 8 ? (1 << lg) : 8; }
+constexpr int step_few_channels(int lg) { return step_most_channels(lg) < 2 ? 1 : 2; }
+
+// Eight channels per lane (fewer where a wave has no lane per channel) while that leaves a wave
+// for every slot of the device, 8192; two below, for more waves. Mamba-2, 64 heads x 64, 128
+// states, 256 rows, all through the caches: 197 us with eight channels, 205 with four, 284 with
+// two, 200 with sixteen; 32 heads, 8 rows take 5.0 us with two (as with four, 7.9 with one).
+// States of 128 MiB or more, half of what holds the last call's, go past the caches, which they
+// would fill for nothing: those 256 rows then take 179 us, 6.0 TB/s (a copy of as much: 5.2).
+// With three caches in turn, us, past and through: Mamba-1 256 rows of 4096 channels, 64 states
+// 107 and 164, 512 rows, 16 states 60 and 85, Mamba-2 256 rows, 64 heads x 64, 64 states 96 and
+// 107; but of 64 MiB, 256 rows of 4096 channels, 16 states, 40 and 32.
+struct StepForm {
+  int channels;
+  bool past_caches;
+  int64_t groups;  // along the grid's first axis (the second is the row)
+};
+inline StepForm step_form(int64_t batch, int64_t dim, int64_t dstate) {
+  const int lg = step_lanes_log2(dstate), most = step_most_channels(lg), per_wave = 64 >> lg;
+  const bool many = dim * batch / (most * per_wave) >= 8192;
+  StepForm f{many ? most : step_few_channels(lg), many && batch * dim * dstate * 4 >= (int64_t(1) << 27), 0};
+  const int64_t per = int64_t(kStepWaves) * f.channels * per_wave;
+  f.groups = (dim + per - 1) / per;
+  return f;
+}
+
 int launch_state_step(const StepArgs& a, void* stream);
 
 // ---------------------------------------------------------------- gated RMS norm
@@ -255,6 +330,33 @@ inline NormShape norm_bwd_shape(int64_t batch, int64_t dim, int64_t groups, int6
                      (!o.all_channel && seqlen > steps &&
                       (norm_run_bytes(s, io) < 32 || (s.tiles * groups * batch < 64 && s.waves > kNormSplitWaves)));
   return split ? norm_split_shape(dim / groups, seqlen, io, steps) : s;
+}
+
+// The tensors of a launch, for the choice of its shape.
+inline NormOrders norm_orders(const NormArgs& a, std::initializer_list<const View*> views) {
+  NormOrders o{true, true};
+  const int64_t esz = a.io == Io::BF16 ? 2 : 4;
+  for (const View* v : views) {
+    if (!v->p || v->order == Order::Channel) continue;
+    o.all_channel = false;
+    if (reinterpret_cast<uintptr_t>(v->p) % 4 || v->s.channel * esz % 4 || (a.batch > 1 && v->s.batch * esz % 4))
+      o.dword_rows = false;
+  }
+  return o;
+}
+
+inline NormShape norm_fwd_shape(const NormArgs& a) {
+  const NormOrders all = norm_orders(a, {&a.y, &a.z, &a.out}), result = norm_orders(a, {&a.out});
+  return norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, {all.all_channel, result.dword_rows});
+}
+
+inline NormShape norm_bwd_shape(const NormArgs& a) {
+  return norm_bwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io,
+                        norm_orders(a, {&a.y, &a.z, &a.dout, &a.dy, &a.dz}));
+}
+
+inline bool norm_fits(const NormArgs& a, const NormShape& s) {
+  return grid_fits(s.tiles * s.cblocks * a.groups * a.batch, 64 * s.waves);
 }
 
 // Partial sums of dweight per channel: one per batch row and tile of steps.

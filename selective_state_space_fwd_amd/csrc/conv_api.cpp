@@ -37,24 +37,28 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t dim, int64_t width, int64
   return SSM_OK;
 }
 
-// The most waves along the grid's first axis, and workgroups in all, of any launch (one run of
-// steps per lane at least; the second axis is the batch row).
-bool launch_fits(int64_t batch, int64_t dim, int64_t seqlen) {
-  const int lg = ssm::conv_row_lanes_log2(seqlen);
-  const int64_t run = int64_t(ssm::kConvSteps) << lg, per = int64_t(1) << (6 - lg);
-  const int64_t tiles = seqlen > 0 ? (seqlen + run - 1) / run : 1;
-  int64_t waves;
-  if (!mul_ok((dim + per - 1) / per, tiles, &waves) || waves > kInt32Max) return false;
-  const int64_t crun = ssm::kConvChannelTileSteps, cw = ssm::kConvWaveChannels;
-  int64_t wgs;
-  return mul_ok((dim + cw - 1) / cw * ((seqlen + crun - 1) / crun), batch, &wgs) && wgs <= kInt32Max;
-}
-
 // A single step has runs of no length either way: the time-ordered kernels' lanes then lie
 // along the channels.
 ssm::Order order_of(const StridedArray& a, int64_t seqlen) {
   return seqlen == 1 ? ssm::Order::Time : a.order;
 }
+
+// The launches of a call within what a grid takes; the channel-ordered kernels number all their
+// workgroups in 32 bits.
+bool launch_fits(int64_t batch, int64_t dim, int64_t width, int64_t seqlen, ssm::Order order, ssm::Io io,
+                 bool backward) {
+  if (backward && !ssm::grid_fits(ssm::reduce_groups(dim * (width + 1)), ssm::kReduceCols * ssm::kConvReduceSlices))
+    return false;
+  const bool time = order == ssm::Order::Time || seqlen == 0;
+  const int wave_tiles = backward ? ssm::kConvBwdTiles : ssm::conv_fwd_wave_tiles(batch, dim, seqlen, io);
+  const ssm::ConvGrid g =
+      time ? ssm::conv_time_grid(dim, seqlen, wave_tiles) : ssm::conv_chan_grid(dim, seqlen);
+  int64_t all;
+  return ssm::grid_fits(g.groups, 64 * ssm::kConvWaves) &&
+         (time || (mul_ok(g.groups, batch, &all) && all <= kInt32Max));
+}
+
+ssm::Io io_of(uint32_t flags) { return (flags & SSM_IO_MASK) == SSM_IO_BF16 ? ssm::Io::BF16 : ssm::Io::F32; }
 
 ssm::ConvArgs common(const void* x, const StridedArray& xa, const float* weight, const float* bias,
                      const void* initial_state, const int32_t* lengths, uint32_t flags, int64_t batch,
@@ -71,7 +75,7 @@ ssm::ConvArgs common(const void* x, const StridedArray& xa, const float* weight,
   a.dim = dim;
   a.width = width;
   a.seqlen = seqlen;
-  a.io = (flags & SSM_IO_MASK) == SSM_IO_BF16 ? ssm::Io::BF16 : ssm::Io::F32;
+  a.io = io_of(flags);
   a.silu = (flags & SSM_CONV_SILU) != 0;
   return a;
 }
@@ -88,7 +92,7 @@ int ssm_conv_fwd(const void* x, const int64_t* x_strides, const float* weight, c
   if (int st = check_sizes(flags, batch, dim, width, seqlen, &z)) return st;
   StridedArray xa;
   if (int st = check_strided(x_strides, batch, dim, seqlen, z.esz, false, &xa)) return st;
-  if (!launch_fits(batch, dim, seqlen)) return SSM_ERR_UNSUPPORTED;
+  if (!launch_fits(batch, dim, width, seqlen, order_of(xa, seqlen), io_of(flags), false)) return SSM_ERR_UNSUPPORTED;
   if ((z.elems > 0 && (!x || !out)) || (dim > 0 && !weight)) return SSM_ERR_INVALID_ARG;
   const uintptr_t e = uintptr_t(z.esz);
   if (!aligned(x, e) || !aligned(out, e) || !aligned(initial_state, e) || !aligned(final_state, e) ||
@@ -135,7 +139,7 @@ int ssm_conv_bwd(const void* x, const int64_t* x_strides, const float* weight, c
   if (int st = check_strided(x_strides, batch, dim, seqlen, z.esz, false, &xa)) return st;
   if (int st = check_strided(dx_strides, batch, dim, seqlen, z.esz, true, &dxa)) return st;
   if (z.elems > 0 && order_of(xa, seqlen) != order_of(dxa, seqlen)) return SSM_ERR_UNSUPPORTED;
-  if (!launch_fits(batch, dim, seqlen)) return SSM_ERR_UNSUPPORTED;
+  if (!launch_fits(batch, dim, width, seqlen, order_of(xa, seqlen), io_of(flags), true)) return SSM_ERR_UNSUPPORTED;
   const int64_t need = ssm_conv_bwd_workspace_bytes(batch, dim, width, seqlen, flags);
   if (need < 0) return SSM_ERR_UNSUPPORTED;
   if ((z.elems > 0 && (!x || !dout || !dx)) || (dim > 0 && (!weight || !dweight))) return SSM_ERR_INVALID_ARG;
@@ -201,8 +205,7 @@ int ssm_conv_step(const void* x, int64_t x_stride, void* state, const float* wei
   if (r.clash()) return SSM_ERR_INVALID_ARG;
   if (batch == 0 || dim == 0) return SSM_OK;
   ssm::ConvStepArgs a{x, x_stride, state, weight, bias, slots, out, batch, nslots, dim, width,
-                      (flags & SSM_IO_MASK) == SSM_IO_BF16 ? ssm::Io::BF16 : ssm::Io::F32,
-                      (flags & SSM_CONV_SILU) != 0};
+                      io_of(flags), (flags & SSM_CONV_SILU) != 0};
   return ssm::launch_conv_step(a, stream) == 0 ? SSM_OK : SSM_ERR_HIP;
 }
 

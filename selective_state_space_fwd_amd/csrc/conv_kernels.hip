@@ -604,12 +604,10 @@ struct ReduceParams {
   int width;
 };
 
-constexpr int kReduceCols = 32, kReduceSlices = 16;
-
-__global__ __launch_bounds__(kReduceCols* kReduceSlices) void conv_bwd_reduce(ReduceParams p) {
-  __shared__ float buf[kReduceSlices][kReduceCols + 1];
+__global__ __launch_bounds__(kReduceCols* kConvReduceSlices) void conv_bwd_reduce(ReduceParams p) {
+  __shared__ float buf[kConvReduceSlices][kReduceCols + 1];
   const int64_t col = int64_t(blockIdx.x) * kReduceCols + threadIdx.x % kReduceCols;
-  const float a = sum_rows<kReduceCols, kReduceSlices>(p.part, p.rows, p.cols, col, buf);
+  const float a = sum_rows<kReduceCols, kConvReduceSlices>(p.part, p.rows, p.cols, col, buf);
   if (threadIdx.x >= kReduceCols || col >= p.cols) return;
   const int64_t d = col / (p.width + 1);
   const int k = int(col - d * (p.width + 1));
@@ -646,23 +644,15 @@ ConvParams params_of(const ConvArgs& a) {
   return p;
 }
 
-// Workgroups of the time-ordered kernels, `run` steps of a row per wave.
-dim3 time_grid(const ConvArgs& a, ConvParams* p, int64_t run) {
-  const int64_t per = int64_t(1) << (6 - p->lanes_log2);
-  p->tiles = a.seqlen > 0 ? uint32_t((a.seqlen + run - 1) / run) : 1;
-  p->waves = uint32_t((a.dim + per - 1) / per * p->tiles);
-  return dim3((p->waves + kConvWaves - 1) / kConvWaves, unsigned(a.batch));
-}
-
-dim3 chan_grid(const ConvArgs& a, ConvParams* p) {
-  const int64_t run = kConvChannelTileSteps;
-  p->tiles = uint32_t((a.seqlen + run - 1) / run);
-  return dim3(unsigned(p->tiles * ((a.dim + CW - 1) / CW)), unsigned(a.batch));
+dim3 grid_of(const ConvArgs& a, const ConvGrid& g, ConvParams* p) {
+  p->tiles = uint32_t(g.tiles);
+  p->waves = uint32_t(g.waves);
+  return dim3(unsigned(g.groups), unsigned(a.batch));
 }
 
 template <typename Elem, int W, int T>
 void run_fwd_time(const ConvArgs& a, ConvParams& p, hipStream_t s) {
-  const dim3 grid = time_grid(a, &p, (int64_t(S) << p.lanes_log2) * T);
+  const dim3 grid = grid_of(a, conv_time_grid(a.dim, a.seqlen, T), &p);
   hipLaunchKernelGGL((conv_fwd_time<Elem, W, T>), grid, dim3(kThreads), 0, s, p);
 }
 
@@ -674,7 +664,7 @@ void run_fwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
     }
     run_fwd_time<Elem, W, 1>(a, p, s);
   } else {
-    const dim3 grid = chan_grid(a, &p);
+    const dim3 grid = grid_of(a, conv_chan_grid(a.dim, a.seqlen), &p);
     hipLaunchKernelGGL((conv_fwd_chan<Elem, W>), grid, dim3(kThreads), 0, s, p);
   }
 }
@@ -682,10 +672,10 @@ void run_fwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
 template <typename Elem, int W>
 void run_bwd(const ConvArgs& a, ConvParams& p, hipStream_t s) {
   if (a.order == Order::Time || a.seqlen == 0) {
-    const dim3 grid = time_grid(a, &p, (int64_t(S) << p.lanes_log2) * kConvBwdTiles);
+    const dim3 grid = grid_of(a, conv_time_grid(a.dim, a.seqlen, kConvBwdTiles), &p);
     hipLaunchKernelGGL((conv_bwd_time<Elem, W>), grid, dim3(kThreads), 0, s, p);
   } else {
-    const dim3 grid = chan_grid(a, &p);
+    const dim3 grid = grid_of(a, conv_chan_grid(a.dim, a.seqlen), &p);
     hipLaunchKernelGGL((conv_bwd_chan<Elem, W>), grid, dim3(kThreads), 0, s, p);
   }
 }
@@ -718,8 +708,8 @@ int launch_conv_bwd(const ConvArgs& a, void* stream) {
   }
   ReduceParams r{a.workspace, a.dweight, a.dbias, a.batch * int64_t(p.tiles),
                  a.dim * (a.width + 1), int(a.width)};
-  const unsigned grid = unsigned((r.cols + kReduceCols - 1) / kReduceCols);
-  hipLaunchKernelGGL(conv_bwd_reduce, dim3(grid), dim3(kReduceCols * kReduceSlices), 0, s, r);
+  hipLaunchKernelGGL(conv_bwd_reduce, dim3(unsigned(reduce_groups(r.cols))), dim3(kReduceCols * kConvReduceSlices),
+                     0, s, r);
   return int(hipGetLastError());
 }
 

@@ -126,6 +126,7 @@ int ssm_norm_fwd(const void* y, const int64_t* y_strides, const void* z, const i
   a.y = v[0];
   a.z = v[1];
   a.out = v[2];
+  if (!ssm::norm_fits(a, ssm::norm_fwd_shape(a))) return SSM_ERR_UNSUPPORTED;
   return ssm::launch_norm_fwd(a, stream) == 0 ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -205,6 +206,9 @@ int ssm_norm_bwd(const void* y, const int64_t* y_strides, const void* z, const i
   a.dout = v[2];
   a.dy = v[3];
   a.dz = v[4];
+  if ((elems > 0 && !ssm::norm_fits(a, ssm::norm_bwd_shape(a))) ||
+      !ssm::grid_fits(ssm::reduce_groups(dim), ssm::kReduceCols * ssm::kNormReduceSlices))
+    return SSM_ERR_UNSUPPORTED;
   return ssm::launch_norm_bwd(a, stream) == 0 ? SSM_OK : SSM_ERR_HIP;
 }
 

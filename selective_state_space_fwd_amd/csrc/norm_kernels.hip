@@ -20,8 +20,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <initializer_list>
-
 #include "block_launch.h"
 #include "device_block.h"
 
@@ -533,13 +531,11 @@ __global__ __launch_bounds__(64 * kNormMostWaves) void norm_bwd_kernel(NormParam
     store_run<float, CV>(p.part + (int64_t(a.b) * p.tiles + a.tile) * (int64_t(p.groups) * p.g) + base, nc, dw);
 }
 
-constexpr int kReduceCols = 32, kReduceSlices = 32;
-
-__global__ __launch_bounds__(kReduceCols* kReduceSlices) void norm_bwd_reduce(const float* part, float* dweight,
+__global__ __launch_bounds__(kReduceCols* kNormReduceSlices) void norm_bwd_reduce(const float* part, float* dweight,
                                                                               int64_t rows, int64_t cols) {
-  __shared__ float buf[kReduceSlices][kReduceCols + 1];
+  __shared__ float buf[kNormReduceSlices][kReduceCols + 1];
   const int64_t col = int64_t(blockIdx.x) * kReduceCols + threadIdx.x % kReduceCols;
-  const float a = sum_rows<kReduceCols, kReduceSlices>(part, rows, cols, col, buf);
+  const float a = sum_rows<kReduceCols, kNormReduceSlices>(part, rows, cols, col, buf);
   if (threadIdx.x < kReduceCols && col < cols) dweight[col] = a;
 }
 
@@ -618,24 +614,10 @@ void run(const NormParams& p, const NormShape& s, bool backward, bool norm_first
     run_steps<Elem, kNormFwdSteps[io]>(p, s, false, norm_first, st);
 }
 
-// The tensors of a launch, for the choice of its shape.
-NormOrders orders_of(const NormArgs& a, std::initializer_list<const View*> views) {
-  NormOrders o{true, true};
-  const int64_t esz = a.io == Io::BF16 ? 2 : 4;
-  for (const View* v : views) {
-    if (!v->p || v->order == Order::Channel) continue;
-    o.all_channel = false;
-    if (reinterpret_cast<uintptr_t>(v->p) % 4 || v->s.channel * esz % 4 || (a.batch > 1 && v->s.batch * esz % 4))
-      o.dword_rows = false;
-  }
-  return o;
-}
-
 }  // namespace
 
 int launch_norm_fwd(const NormArgs& a, void* stream) {
-  const NormOrders all = orders_of(a, {&a.y, &a.z, &a.out}), result = orders_of(a, {&a.out});
-  const NormShape s = norm_fwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io, {all.all_channel, result.dword_rows});
+  const NormShape s = norm_fwd_shape(a);
   NormParams p = params_of(a, s);
   p.split = a.workspace;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -650,8 +632,7 @@ int launch_norm_bwd(const NormArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   int64_t rows = 0;
   if (a.batch > 0 && a.seqlen > 0) {
-    const NormShape s = norm_bwd_shape(a.batch, a.dim, a.groups, a.seqlen, a.io,
-                                       orders_of(a, {&a.y, &a.z, &a.dout, &a.dy, &a.dz}));
+    const NormShape s = norm_bwd_shape(a);
     NormParams p = params_of(a, s);
     rows = norm_partials(a.batch, s);
     p.split = a.workspace + rows * a.dim;
@@ -662,8 +643,8 @@ int launch_norm_bwd(const NormArgs& a, void* stream) {
     const int err = int(hipGetLastError());
     if (err) return err;
   }
-  hipLaunchKernelGGL(norm_bwd_reduce, dim3(unsigned((a.dim + kReduceCols - 1) / kReduceCols)),
-                     dim3(kReduceCols * kReduceSlices), 0, st, a.workspace, a.dweight, rows, a.dim);
+  hipLaunchKernelGGL(norm_bwd_reduce, dim3(unsigned(reduce_groups(a.dim))),
+                     dim3(kReduceCols * kNormReduceSlices), 0, st, a.workspace, a.dweight, rows, a.dim);
   return int(hipGetLastError());
 }
 

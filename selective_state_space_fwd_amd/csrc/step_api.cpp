@@ -42,7 +42,8 @@ int step_impl(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride
   const int64_t esz = io == SSM_IO_BF16 ? 2 : 4;
   int64_t dim, cache, cache_bytes, xb, tb, bb, cb, zb;
   if (!mul_ok(heads, per_head ? headdim : 1, &dim) || dim > kInt32Max || batch > 65535 ||
-      nslots > kInt32Max || !mul_ok(nslots, dim, &cache) || !mul_ok(cache, dstate * 4, &cache_bytes))
+      nslots > kInt32Max || !mul_ok(nslots, dim, &cache) || !mul_ok(cache, dstate * 4, &cache_bytes) ||
+      !ssm::grid_fits(ssm::step_form(batch, dim, dstate).groups, 64 * ssm::kStepWaves))
     return SSM_ERR_UNSUPPORTED;
   int st;
   if ((st = rows_bytes(batch, dim, x_stride, esz, &xb)) || (st = rows_bytes(batch, heads, dt_stride, esz, &tb)) ||

@@ -20,7 +20,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kStepWaves;
 
 struct StepParams {
   const void* x;
@@ -181,41 +181,29 @@ __global__ __launch_bounds__(64 * kWaves) void state_step_kernel(StepParams p) {
 }
 
 template <typename Elem, int LG, int CH, bool kStream>
-void run_ch(const StepArgs& a, const StepParams& p, hipStream_t s) {
-  constexpr int per = kWaves * CH * (64 >> LG);
-  const dim3 grid(unsigned((a.dim + per - 1) / per), unsigned(a.batch)), block(64 * kWaves);
+void run_ch(const StepArgs& a, const StepParams& p, const StepForm& f, hipStream_t s) {
+  const dim3 grid(unsigned(f.groups), unsigned(a.batch)), block(64 * kWaves);
   if (a.headdim)
     hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, true, kStream>), grid, block, 0, s, p);
   else
     hipLaunchKernelGGL((state_step_kernel<Elem, LG, CH, false, kStream>), grid, block, 0, s, p);
 }
 
-// Eight channels per lane (fewer where a wave has no lane per channel) while that leaves a wave
-// for every slot of the device, 8192; two below, for more waves. Mamba-2, 64 heads x 64, 128
-// states, 256 rows, all through the caches: 197 us with eight channels, 205 with four, 284 with
-// two, 200 with sixteen; 32 heads, 8 rows take 5.0 us with two (as with four, 7.9 with one).
-// States of 128 MiB or more, half of what holds the last call's, go past the caches, which they
-// would fill for nothing: those 256 rows then take 179 us, 6.0 TB/s (a copy of as much: 5.2).
-// With three caches in turn, us, past and through: Mamba-1 256 rows of 4096 channels, 64 states
-// 107 and 164, 512 rows, 16 states 60 and 85, Mamba-2 256 rows, 64 heads x 64, 64 states 96 and
-// 107; but of 64 MiB, 256 rows of 4096 channels, 16 states, 40 and 32.
 template <typename Elem, int LG>
 void run_lg(const StepArgs& a, const StepParams& p, hipStream_t s) {
-  constexpr int most = (1 << LG) < 8 ? (1 << LG) : 8;
-  constexpr int few = most < 2 ? most : 2;
-  if (a.dim * a.batch / (most * (64 >> LG)) < 8192)
-    run_ch<Elem, LG, few, false>(a, p, s);
-  else if (a.batch * a.dim * a.dstate * 4 < (int64_t(1) << 27))
-    run_ch<Elem, LG, most, false>(a, p, s);
+  constexpr int most = step_most_channels(LG), few = step_few_channels(LG);
+  const StepForm f = step_form(a.batch, a.dim, a.dstate);
+  if (f.past_caches)
+    run_ch<Elem, LG, most, true>(a, p, f, s);
+  else if (f.channels == most)
+    run_ch<Elem, LG, most, false>(a, p, f, s);
   else
-    run_ch<Elem, LG, most, true>(a, p, s);
+    run_ch<Elem, LG, few, false>(a, p, f, s);
 }
 
 template <typename Elem>
 void run(const StepArgs& a, const StepParams& p, hipStream_t s) {
-  int lg = 0;
-  while ((int64_t(4) << lg) < a.dstate) ++lg;  // dstate <= 256, so lg <= 6
-  switch (lg) {
+  switch (step_lanes_log2(a.dstate)) {  // dstate <= 256, so at most 6
     case 0: return run_lg<Elem, 0>(a, p, s);
     case 1: return run_lg<Elem, 1>(a, p, s);
     case 2: return run_lg<Elem, 2>(a, p, s);
