@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Dict, Optional, Tuple
 
 from . import (SSM_DELTA_SOFTPLUS, SSM_ERR_UNSUPPORTED, SSM_IO_BF16, SSM_IO_F32, SSM_OK,
@@ -40,6 +41,17 @@ SSM_NORM_BEFORE_GATE = 1 << 12
 
 _Strides = ctypes.c_int64 * 3
 _bound = _binding = None
+
+
+class _NoModule:
+    """In the place of the extension module where none was built: it makes no call, so that the
+    checks below make every one."""
+
+    @staticmethod
+    def _makes_none(*args):
+        return None
+
+    conv = conv_step = state_step = norm = conv_backward = norm_backward = _makes_none
 
 
 def _lib() -> ctypes.CDLL:
@@ -72,8 +84,11 @@ def _lib() -> ctypes.CDLL:
     L.ssm_conv_bwd_workspace_bytes.restype = i64
     L.ssm_norm_bwd_workspace_bytes.restype = i64
     if not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"{BINDING_PATH} is missing: build it first "
-                           "(python -m selective_state_space_fwd_amd.build)")
+        warnings.warn(f"{BINDING_PATH} is missing (python -m selective_state_space_fwd_amd.build): "
+                      "every call is marshalled in Python, a few microseconds more each")
+        _binding = _NoModule
+        _bound = L
+        return L
     from . import _binding as module
 
     address = lambda name: ctypes.cast(getattr(L, name), vp).value

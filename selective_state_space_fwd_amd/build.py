@@ -9,9 +9,11 @@ not know that feature, which is harmless.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import tempfile
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -65,6 +67,24 @@ def _link(sources, target, verbose, extra=()):
     return _compile([hipcc(), *compile_flags(), *extra], sources, target, verbose)
 
 
+def _binding_lacks():
+    """What the extension module's build needs and this machine has not, or None."""
+    import sysconfig
+
+    cxx = os.environ.get("CXX", "g++")
+    if shutil.which(cxx) is None:
+        return f"no C++ compiler ({cxx})"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "no Python.h"
+    try:
+        from torch.utils.cpp_extension import include_paths
+    except ImportError as e:
+        return f"no torch ({e})"
+    if not any(os.path.exists(os.path.join(p, "ATen", "ATen.h")) for p in include_paths(device_type="cuda")):
+        return "no headers of torch"
+    return None
+
+
 def _build_binding(verbose: bool) -> str:
     """_binding.so: g++ against torch's and Python's headers and torch's libraries (found in the
     process by then: the module is imported after torch)."""
@@ -82,14 +102,23 @@ def _build_binding(verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Build libssmscan.so (the scan library), libssmprobe.so (the VALU probes),
-    libssmscan_shape2.so (the test-only second launch shape) and _binding.so (the binding's
-    extension module)."""
-    _build_binding(verbose)
+    """Build libssmprobe.so (the VALU probes), libssmscan_shape2.so (the test-only second launch
+    shape), libssmscan.so (the scan library), which hipcc alone makes, and then _binding.so (the
+    binding's extension module). Where the last cannot be built for want of a C++ compiler, torch
+    or headers, a warning says so and none is left behind: the binding then marshals every call
+    in Python."""
     _link([PROBE_SOURCE], PROBE_LIB_PATH, verbose)
     _link([os.path.join(CSRC, s) for s in SHAPE2_SOURCES], SHAPE2_LIB_PATH, verbose,
           SHAPE2_DEFINES)
-    return _link([os.path.join(CSRC, s) for s in SOURCES], LIB_PATH, verbose)
+    _link([os.path.join(CSRC, s) for s in SOURCES], LIB_PATH, verbose)
+    lacks = _binding_lacks()
+    if lacks is None:
+        _build_binding(verbose)
+    else:
+        if os.path.exists(BINDING_PATH):
+            os.unlink(BINDING_PATH)  # of other sources, perhaps
+        warnings.warn(f"{os.path.basename(BINDING_PATH)} not built: {lacks}")
+    return LIB_PATH
 
 
 if __name__ == "__main__":
