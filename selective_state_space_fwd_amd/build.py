@@ -59,6 +59,9 @@ def _compile(cmd, sources, target, verbose):
     if r.returncode != 0:
         os.unlink(tmp)
         raise RuntimeError(f"{cmd[0]} failed ({r.returncode}):\n{r.stderr}")
+    umask = os.umask(0)
+    os.umask(umask)
+    os.chmod(tmp, 0o777 & ~umask)  # (mkstemp's file is its owner's alone, and g++ keeps that)
     os.replace(tmp, target)
     return target
 

@@ -106,3 +106,24 @@ def test_results_without_the_module(monkeypatch, tmp_path):
         without = calls()
     assert block._binding is block._NoModule
     assert all(t.equal(a, b) for a, b in zip(with_it, without))
+
+
+def test_built_files_are_readable_by_others(tmp_path, monkeypatch):
+    """What the compilers write goes by the umask, also where they write into the file they are given
+    (made for its owner alone)."""
+    import os
+    import shutil
+
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("gcc not available")
+    source, target = tmp_path / "one.c", tmp_path / "one.so"
+    source.write_text("int one(void) { return 1; }\n")
+    monkeypatch.setattr(hip_build, "PKG", str(tmp_path))
+    before = os.umask(0o022)
+    try:
+        hip_build._compile([cc, "-fPIC"], [str(source)], str(target), False)
+    finally:
+        os.umask(before)
+    assert target.stat().st_mode & 0o777 == 0o755
+    assert sorted(p.name for p in tmp_path.iterdir()) == ["one.c", "one.so"]
