@@ -852,13 +852,9 @@ void run_step_rows(const ConvStepArgs& a, const ConvStepParams& p, hipStream_t s
   hipLaunchKernelGGL((conv_step_kernel<Elem, W, R>), grid, dim3(256), 0, s, p);
 }
 
-// Two rows per lane once the rows fill the device's 8192 wave slots, one before that. 384 rows
-// of 4352 bf16 channels: 9.6 us with one row, 8.8 with two, 10.2 with four; 8 rows of 2304:
-// 2.9 us with one.
 template <typename Elem, int W>
 void run_step(const ConvStepArgs& a, const ConvStepParams& p, hipStream_t s) {
-  const int64_t waves = (a.dim * int64_t(sizeof(Elem)) / 256 + 1) * a.batch;
-  if (waves > 8192)
+  if (conv_step_rows(a.batch, a.dim, a.io) == 2)
     run_step_rows<Elem, W, 2>(a, p, s);
   else
     run_step_rows<Elem, W, 1>(a, p, s);

@@ -17,6 +17,13 @@ int main(int argc, char** argv) {
       const int64_t b = num(), d = num(), L = num();
       const ssm::Io io = num() ? ssm::Io::BF16 : ssm::Io::F32;
       printf("%d\n", ssm::conv_fwd_wave_tiles(b, d, L, io));
+    } else if (!strcmp(name, "conv_step")) {  // batch dim io
+      const int64_t b = num(), d = num();
+      printf("%d\n", ssm::conv_step_rows(b, d, num() ? ssm::Io::BF16 : ssm::Io::F32));
+    } else if (!strcmp(name, "state_step")) {  // batch dim dstate: channels past_caches
+      const int64_t b = num(), d = num();
+      const ssm::StepForm f = ssm::step_form(b, d, num());
+      printf("%d %d\n", f.channels, int(f.past_caches));
     } else if (!strcmp(name, "norm_fwd") || !strcmp(name, "norm_bwd")) {
       // batch dim groups seqlen io all_channel dword_rows: steps lanes_log2 waves split
       const int64_t b = num(), d = num(), g = num(), L = num();
