@@ -185,43 +185,6 @@ __device__ __forceinline__ void store_few(Elem* p, int n, const float (&v)[C]) {
   }
 }
 
-// The storage word of n <= kN elements, zeros past them.
-template <typename Elem>
-__device__ __forceinline__ uint4 load_word_n(const Elem* p, int n) {
-  constexpr int N = Vec<Elem>::kN;
-  if (n >= N) return load16_any(p);
-  float v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = i < n ? widen<Elem>(p[i]) : 0.0f;
-  return narrow_raw16<Elem>(v);
-}
-
-// Element c (a constant after unrolling) of a storage word, widened.
-template <typename Elem>
-__device__ __forceinline__ float word_elem(const uint4& w, int c);
-template <>
-__device__ __forceinline__ float word_elem<float>(const uint4& w, int c) {
-  return __uint_as_float(c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w);
-}
-template <>
-__device__ __forceinline__ float word_elem<uint16_t>(const uint4& w, int c) {
-  const uint32_t d = c < 2 ? w.x : c < 4 ? w.y : c < 6 ? w.z : w.w;
-  return (c & 1) ? bf16_hi(d) : bf16_lo(d);
-}
-
-// The first n elements of a storage word.
-template <typename Elem>
-__device__ __forceinline__ void store_word_n(Elem* p, int n, const uint4& w) {
-  constexpr int N = Vec<Elem>::kN;
-  if (n >= N) {
-    store16_any(p, w);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = narrow<Elem>(word_elem<Elem>(w, i));
-  }
-}
-
 // silu(p) = p sigmoid(p), and its derivative sigmoid(p) (1 + p (1 - sigmoid(p))).
 __device__ __forceinline__ float sigmoid_f(float p) {
   return rcp_hw(1.0f + exp2_hw(-p * kLog2e));
