@@ -13,9 +13,7 @@
 //            channel, which turns the order through registers alone. A wave covers 64
 //            channels by 32 steps, a workgroup 128 steps.
 // Sums are fp32; a result is rounded once, at its store. A row's steps at and behind its
-// length are not read; its outputs there are zeros, and a workgroup wholly behind it stores them and
-// does no more (channel order, b16, 2304 channels, 2048 steps, rows from a quarter to three quarters
-// long: 67 -> 42 us; the gradient, b4: 33 -> 29.3).
+// length are not read, and its outputs there are zeros.
 //
 // b4, 2304 channels, 2048 steps, bf16 (75 MB in and out, 12 us by a library copy of that size):
 // 15.2 us channel order, 16 us time order, by the kernel trace. What that took: no branch
@@ -199,7 +197,10 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_time(ConvParams p) {
 // Words of the steps t .. t + N - 1, of nc (> 0) channels from p's on. A step outside the row (end > 0
 // is its length) takes the nearest one's word, so that the loads need no branch and what lies
 // behind the row is not read: the callers replace what lies before the first step by the initial
-// state and let nothing at or behind the end count.
+// state and let nothing at or behind the end count. (A row of no steps takes no words; theirs are
+// then what the registers held, and count as little. Stopping a workgroup behind its row's end
+// ahead of its loads made whole rows 4% slower; as it is, b16, 2304 channels, 2048 steps, rows of
+// a quarter to three quarters, bf16, take 40.5 us, 66.9 with their padding read.)
 template <typename Elem, int CV>
 using Word = Dwords<CV * int(sizeof(Elem)) / 4>;
 
@@ -304,37 +305,19 @@ struct Weights {
   }
 };
 
-// The results of a workgroup wholly behind its row's end, for which nothing of x is read: zeros, and
-// a row of no steps hands on its initial state.
-template <typename Elem, int W>
-__device__ __forceinline__ void pad_out(const ConvParams& p, const Elem* xb, const ChanLane<kConvLaneChannels>& a,
-                                        uint32_t len) {
-  const int64_t row0 = int64_t(a.b) * p.dim + a.c0;
-  Elem* orow = static_cast<Elem*>(p.out) + row0 * p.seqlen + a.t0;
-  const float zero[S] = {};
-  for (int c = 0; c < kConvLaneChannels && c < a.nc; ++c) {
-    store_run_stream<Elem, S>(orow + int64_t(c) * p.seqlen, steps_left(p.seqlen, a.t0), zero);
-    if (p.final_state && a.t0 == 0) store_final<Elem, W>(p, xb + c, row0 + c, len);
-  }
-}
-
 template <typename Elem, int W>
 __global__ __launch_bounds__(kThreads) void conv_fwd_chan(ConvParams p) {
   constexpr int CV = kConvLaneChannels;
   __shared__ float sw[CW * (W + 1)];
   const ChanLane<CV> a = chan_lane<CV, false>(p);
+  Weights<W> weights;
+  weights.load(p, a.cb);
   const int b = a.b;
   const bool live = a.nc > 0 && a.t0 < p.seqlen;
   const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + a.c0;
   const uint32_t len = row_length(p, b);
-  if (len <= a.tile * uint32_t(kConvChannelTileSteps)) {  // wholly behind the row's end
-    if (live) pad_out<Elem, W>(p, xb, a, len);
-    return;
-  }
-  Weights<W> weights;
-  weights.load(p, a.cb);
   Word<Elem, CV> raw[S + W - 1];
-  if (live) load_rows<Elem, CV, S + W - 1>(xb, p.xt, int64_t(a.t0) - (W - 1), len, a.nc, raw);
+  if (live && len > 0) load_rows<Elem, CV, S + W - 1>(xb, p.xt, int64_t(a.t0) - (W - 1), len, a.nc, raw);
   weights.stage(sw);
   if (!live) return;
   const int n = steps_left(len, a.t0), all = steps_left(p.seqlen, a.t0);
@@ -508,28 +491,6 @@ struct StepWords {
   }
 };
 
-// As pad_out: no gradient but dfinal's, which a row of no steps hands to its initial state.
-template <typename Elem, int W>
-__device__ __forceinline__ void pad_grad(const ConvParams& p, const Elem* xb, const Elem* gb,
-                                         const ChanLane<kConvLaneChannels>& a, bool live, uint32_t len) {
-  constexpr int CV = kConvLaneChannels, cols = CW * (W + 1);
-  if (live) {
-    const int64_t row0 = int64_t(a.b) * p.dim + a.c0;
-    Elem* dxb = static_cast<Elem*>(p.dx) + a.b * p.dxb + a.c0 + a.t0 * p.dxt;
-    const float zero[CV] = {};
-    for (int i = 0; i < steps_left(p.seqlen, a.t0) && i < S; ++i) store_few<Elem, CV>(dxb + i * p.dxt, a.nc, zero);
-    if (p.dinitial && a.t0 == 0) {
-      const float none[W] = {};
-      for (int c = 0; c < CV && c < a.nc; ++c)
-        store_dinitial<Elem, W>(p, xb + c, gb + int64_t(c) * p.seqlen, row0 + c, len, none, 0.0f);
-    }
-  }
-  for (int i = threadIdx.x; i < cols; i += kThreads) {
-    const int64_t col = int64_t(a.cb) * cols + i;
-    if (col < int64_t(p.dim) * (W + 1)) p.part[(int64_t(a.b) * p.tiles + a.tile) * p.dim * (W + 1) + col] = 0.0f;
-  }
-}
-
 // Channel order: as the forward, dout's words of all channels in flight with x's; the lanes'
 // sums meet in LDS.
 template <typename Elem, int W>
@@ -539,23 +500,19 @@ __global__ __launch_bounds__(kThreads, sizeof(Elem) == 2 ? 4 : 3) void conv_bwd_
   constexpr int kRows = kConvWaves * L::TB;  // of sums: a lane along time each
   __shared__ float sw[CW * (W + 1)], sums[kRows][CW * K + 1];
   const L a = chan_lane<CV, true>(p);
+  Weights<W> weights;
+  weights.load(p, a.cb);
   const int b = a.b;
   const bool live = a.nc > 0 && a.t0 < p.seqlen;
   const uint32_t len = row_length(p, b);
   const int64_t row0 = int64_t(b) * p.dim + a.c0;
   const Elem* xb = static_cast<const Elem*>(p.x) + b * p.xb + a.c0;
   const Elem* gb = static_cast<const Elem*>(p.dout) + row0 * p.seqlen + a.t0;
-  if (len <= a.tile * uint32_t(kConvChannelTileSteps)) {  // wholly behind the row's end
-    pad_grad<Elem, W>(p, xb, gb, a, live, len);
-    return;
-  }
-  Weights<W> weights;
-  weights.load(p, a.cb);
   const int n = live ? steps_left(len, a.t0) : 0;
   Word<Elem, CV> raw[S + 2 * (W - 1)];
   Word<Elem, S> graw[CV];
   Word<Elem, 4> gnext[CV];
-  if (live) load_rows<Elem, CV, S + 2 * (W - 1)>(xb, p.xt, int64_t(a.t0) - (W - 1), len, a.nc, raw);
+  if (live && len > 0) load_rows<Elem, CV, S + 2 * (W - 1)>(xb, p.xt, int64_t(a.t0) - (W - 1), len, a.nc, raw);
   const bool whole = a.nc >= CV && n >= S + 4;
   // The steps behind a block are the next lane's first where that lies in the wave and is whole.
   const bool last = a.tb == L::TB - 1 || n < 2 * S + 4;
