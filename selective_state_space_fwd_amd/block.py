@@ -226,6 +226,14 @@ def _run(fn, dev, *args):
         raise SsmScanError(status)
 
 
+def _wrote(*tensors):
+    """A call wrote these (or None) in place: autograd, if it holds one for a backward pass, has to
+    see that."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            _torch().autograd.graph.increment_version(t)
+
+
 def _in_place(t):
     """t, or a contiguous copy of a view with neither steps nor channels contiguous."""
     b, d, L = t.shape
@@ -306,6 +314,7 @@ def conv(x, weight, bias=None, silu: bool = False, initial_state=None, lengths=N
     _run(_lib().ssm_conv_fwd, dev, x.data_ptr(), _strides(x), weight.data_ptr(), _ptr(bias),
          _ptr(initial_state), _ptr(lengths), flags | (SSM_CONV_SILU if silu else 0),
          out.data_ptr(), _ptr(final_state), batch, dim, width, seqlen)
+    _wrote(out, final_state)
     return out, final_state
 
 
@@ -371,6 +380,7 @@ def conv_step(x, state, weight, bias=None, silu: bool = False, slots=None, out=N
     _run(_lib().ssm_conv_step, dev, x.data_ptr(), x.stride(0), state.data_ptr(),
          weight.data_ptr(), _ptr(bias), _ptr(slots), flags | (SSM_CONV_SILU if silu else 0),
          out.data_ptr(), batch, nslots, dim, past + 1)
+    _wrote(state, out)
     return out
 
 
@@ -409,6 +419,7 @@ def _step(fn, heads, x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, out,
          B.data_ptr(), B.stride(0), C.data_ptr(), C.stride(0), _ptr(D), z_ptr, z_stride,
          _ptr(dt_bias), _ptr(slots), flags | (SSM_DELTA_SOFTPLUS if softplus else 0),
          state.data_ptr(), out.data_ptr(), batch, nslots, *sizes, dstate)
+    _wrote(state, out)
     return out
 
 
@@ -486,6 +497,7 @@ def _norm_forward(y, weight, z, eps, groups, norm_before_gate, token_major, out,
          weight.data_ptr(), eps, flags | (SSM_NORM_BEFORE_GATE if norm_before_gate else 0),
          out.data_ptr(), _Strides(seqlen * dim, 1, dim) if token_major else None, _ptr(rstd),
          workspace.data_ptr(), workspace.numel(), batch, dim, groups, seqlen)
+    _wrote(out)
     return out, rstd
 
 

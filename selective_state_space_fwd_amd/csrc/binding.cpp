@@ -54,6 +54,11 @@ struct Arg {
   void* mut() const { return t ? t->data_ptr() : nullptr; }
 };
 
+// A call wrote t in place: autograd, if it holds t for a backward pass, has to see that.
+void wrote(const Arg& t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 bool flag_of(PyObject* o, bool* ok) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) {
@@ -219,6 +224,8 @@ PyObject* conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           op, fp, b, d, W, L, stream_of(dev));
       }))
     return nullptr;
+  wrote(out);
+  wrote(fin);
   PyObject* o = give(a[6], made_out);
   PyObject* f = fin || want ? give(a[7], made_fin) : (Py_INCREF(Py_None), Py_None);
   PyObject* both = PyTuple_Pack(2, o, f);
@@ -251,6 +258,8 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            uint32_t(io) | (silu ? SSM_CONV_SILU : 0), op, b, ns, d, past + 1, stream_of(dev));
       }))
     return nullptr;
+  wrote(state);
+  wrote(out);
   return give(a[6], made_out);
   END_HANDLE_TH_ERRORS
 }
@@ -292,6 +301,8 @@ PyObject* state_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                       flags, st, op, b, ns, d, N, stream_of(dev));
       }))
     return nullptr;
+  wrote(state);
+  wrote(out);
   return give(a[12], made_out);
   END_HANDLE_TH_ERRORS
 }
@@ -341,6 +352,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           stream_of(dev));
       }))
     return nullptr;
+  wrote(out);
   PyObject* o = give(a[7], made_out);
   PyObject* r = save ? THPVariable_Wrap(rstd) : (Py_INCREF(Py_None), Py_None);
   PyObject* both = PyTuple_Pack(2, o, r);
