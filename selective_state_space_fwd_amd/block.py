@@ -180,7 +180,7 @@ def _check(name, t, shape, dtype, dev):
 
 def _check_out(name, t, shape, dtype, dev):
     _check(name, t, shape, dtype, dev)
-    if not t.is_contiguous():
+    if not t.is_contiguous() or t.is_neg():
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -189,7 +189,7 @@ def _param(name, t, shape, dtype, dev):
     if t is None:
         return None
     _check(name, t, shape, dtype, dev)
-    return t if t.is_contiguous() else t.contiguous()
+    return t.resolve_neg().contiguous()
 
 
 def _device(name, t) -> int:
@@ -236,12 +236,14 @@ def _wrote(*tensors):
 
 def _in_place(t):
     """t, or a contiguous copy of a view with neither steps nor channels contiguous."""
+    t = t.resolve_neg()  # (its memory may hold the negative of its values)
     b, d, L = t.shape
     return t if L <= 1 or t.stride(2) == 1 or (d > 1 and t.stride(1) == 1) else t.contiguous()
 
 
 def _rows(t):
     """t, or a copy with its last axis contiguous."""
+    t = t.resolve_neg()
     return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
 
 

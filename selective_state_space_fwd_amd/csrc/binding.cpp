@@ -38,12 +38,12 @@ decltype(&ssm_norm_fwd_workspace_bytes) g_norm_fwd_ws;
 PyObject* g_error;  // SsmScanError
 
 // An argument as a tensor: a plain torch.Tensor, or None (`t` undefined). `ok` turns false for
-// anything else.
+// anything else, a view whose memory holds the negative of its values among them.
 struct Arg {
   const at::Tensor* t = nullptr;
   Arg(PyObject* o, bool* ok) {
     if (o == Py_None) return;
-    if (THPVariable_CheckExact(o))
+    if (THPVariable_CheckExact(o) && !THPVariable_Unpack(o).is_neg())
       t = &THPVariable_Unpack(o);
     else
       *ok = false;
