@@ -16,13 +16,14 @@
 // length are not read, and its outputs there are zeros.
 //
 // b4, 2304 channels, 2048 steps, bf16 (75 MB in and out, 12 us by a library copy of that size):
-// 15.2 us channel order, 16 us time order, by the kernel trace. What that took: no branch
+// 14.7 us channel order by the kernel trace; 14.9 and 15.6 (time order) a call. What that took: no branch
 // around a load (23 -> 16 us, with the weights of a workgroup in LDS instead of a load per
 // channel that is waited for), index arithmetic of 32 bits (time order 20 -> 16: it was VALU
 // bound), stores past L2 (1 us). Eight channels a lane 17.7 us, sixteen-channel waves 28 us.
-// The gradient (113 MB): 30.5 us channel order, 28.5 us time order, of which the VALU needs 21
-// (a sigmoid for 11 steps of each 8); 43 us with workgroups in plain order, where an XCD's
-// tiles all lie at one offset of the 4096-byte rows and so in two of its L2's channels.
+// The gradient (113 MB): 30.6 us channel order by the trace, of which the VALU needs 21 (a sigmoid
+// for 11 steps of each 8), and 4.8 the second launch; 33.4 and 31.6 (time order) a call. 43 us with
+// workgroups in plain order, where an XCD's tiles all lie at one offset of the 4096-byte rows and
+// so in two of its L2's channels. fp32, channel order: 50.5 a call (227 MB).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -13,10 +13,12 @@
 // and some whose steps it would read in too small pieces, take two launches instead (Phase).
 //
 // Bound by memory: 3 reads and writes per element forward, 5 backward. b4, 2048 channels, 2048
-// steps, bf16, y in the scan's order, z and the result in a projection's: forward 19.5 us (100
-// MB, 5.2 TB/s, the rate of a large copy), gradient 44 us (168 MB, 3.8 TB/s) and 4 for the sums
-// of dweight. The gradient's loads and its arithmetic (20 us, with two transcendentals per
-// element) overlap in part only: a CU holds one workgroup of sixteen waves.
+// steps, bf16, y in the scan's order, z and the result in a projection's: forward 20 us (101
+// MB, 5.0 TB/s, the rate of a large copy), gradient 44.4 us (168 MB, 3.8 TB/s) and 4.7 for the sums
+// of dweight, 46.8 a call. The gradient's loads and its arithmetic (20 us, with two transcendentals
+// per element) overlap in part only: a CU holds one workgroup of sixteen waves. Norm first, bf16:
+// forward 23.3 us, of 18 registers spilled. Groups above 2048 channels take the gradient's two
+// launches, which read its inputs twice (4096 channels, 1024 steps: 56.6 us a call).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
