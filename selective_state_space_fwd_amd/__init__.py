@@ -15,7 +15,9 @@ ABI of include/ssm_scan.h. PyTorch supplies device memory and the current stream
                        # differentiable: scan_train forward, scan_backward under autograd
 
 and, from ``block.py``, the operators around the scan: ``conv``, ``causal_conv``, ``conv_step``,
-``scan_step``, ``ssd_step``, ``norm``, ``gated_norm``.
+``scan_step``, ``ssd_step``, ``norm``, ``gated_norm``; from ``linattn.py``, linear attention with a
+decay for each head and the norm and rotation of its queries and keys: ``linattn``,
+``linear_attention``, ``linattn_step``, ``qk_norm``, ``rotary_qk_norm``.
 
 Inputs may be strided views: the functions above copy them to contiguous tensors first
 (outputs passed in must be contiguous). The ``ssm_scan_*`` functions are the raw C entry
@@ -55,7 +57,10 @@ EXPORTED = ("ssm_scan_fwd", "ssm_scan_strerror", "ssm_scan_abi_version",
             "ssm_ssd_workspace_bytes", "ssm_ssd_fwd", "ssm_ssd_fwd_noalloc",
             "ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_bwd_workspace_bytes", "ssm_conv_step",
             "ssm_scan_step", "ssm_ssd_step", "ssm_norm_fwd", "ssm_norm_bwd",
-            "ssm_norm_fwd_workspace_bytes", "ssm_norm_bwd_workspace_bytes")
+            "ssm_norm_fwd_workspace_bytes", "ssm_norm_bwd_workspace_bytes",
+            "ssm_linattn_fwd", "ssm_linattn_fwd_workspace_bytes", "ssm_linattn_bwd",
+            "ssm_linattn_bwd_workspace_bytes", "ssm_linattn_step", "ssm_qk_norm_fwd",
+            "ssm_qk_norm_bwd", "ssm_qk_norm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -522,3 +527,10 @@ from .block import (SSM_CONV_SILU, SSM_NORM_BEFORE_GATE, causal_conv, conv,  # n
                     scan_step, ssd_step, ssm_conv_bwd, ssm_conv_bwd_workspace_bytes,
                     ssm_conv_fwd, ssm_conv_step, ssm_norm_bwd, ssm_norm_bwd_workspace_bytes,
                     ssm_norm_fwd, ssm_norm_fwd_workspace_bytes, ssm_scan_step, ssm_ssd_step)
+# Linear attention, and the norm of its queries and keys (after the helpers they take from block.py).
+from .linattn import (SSM_LINATTN_HEAD_DG, SSM_QK_INTERLEAVED, linattn,  # noqa: E402,F401
+                      linattn_backward, linattn_step, linear_attention, qk_norm,
+                      qk_norm_backward, rotary_qk_norm, ssm_linattn_bwd,
+                      ssm_linattn_bwd_workspace_bytes, ssm_linattn_fwd,
+                      ssm_linattn_fwd_workspace_bytes, ssm_linattn_step, ssm_qk_norm_bwd,
+                      ssm_qk_norm_bwd_workspace_bytes, ssm_qk_norm_fwd)

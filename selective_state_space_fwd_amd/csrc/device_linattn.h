@@ -1,0 +1,303 @@
+// Device helpers of the linear-attention kernels: tiles of head rows staged in LDS, operands of the
+// matrix instructions read from them along rows or columns, fp32 values as bf16 pieces, and the
+// running decays of a chunk of steps.
+//
+// Operand layout (v_mfma_f32_16x16x32_bf16): lane l, r = l % 16, g = l / 16, holds the contraction
+// values 8g..8g+7 of row r of the first operand, and of column r of the second; the result
+// has rows 4g..4g+3 of column r. A fragment is the same for both sides, so swapping the two
+// transposes the result. fp32 storage takes v_mfma_f32_16x16x4_f32 eight times on the same
+// fragments: its lane group g supplies contraction value g, here value 8g + i of the i-th.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_block.h"
+#include "linattn_launch.h"
+
+namespace ssm {
+
+typedef __bf16 la_bf16x8 __attribute__((ext_vector_type(8)));
+typedef float la_f32x4 __attribute__((ext_vector_type(4)));
+typedef short la_s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) la_s16x4 la_lds_s16x4;
+
+constexpr int kLaThreads = 256;
+
+template <typename Elem>
+constexpr int chunk_of() {
+  return linattn_chunk(sizeof(Elem) == 2 ? Io::BF16 : Io::F32);
+}
+
+// A barrier for LDS only: loads on their way from memory and results on their way out go on
+// across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Eight contraction values of one row (or column).
+template <typename Elem>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+  uint4 w;
+};
+template <>
+struct Frag<float> {
+  float v[8];
+};
+
+__device__ __forceinline__ la_f32x4 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, la_f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf16x8, a.w),
+                                                 __builtin_bit_cast(la_bf16x8, b.w), c, 0, 0, 0);
+}
+__device__ __forceinline__ la_f32x4 mma(const Frag<float>& a, const Frag<float>& b, la_f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// Eight fp32 values as an operand next to storage type Elem: N bf16 pieces, each the rounding of
+// what the ones before leave (8 bits of the significand each, so three hold all 24), or the
+// values themselves in fp32.
+template <typename Elem, int N>
+struct Pieces;
+template <int N>
+struct Pieces<uint16_t, N> {
+  Frag<uint16_t> f[N];
+  __device__ __forceinline__ void split(const float (&x)[8]) {
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = x[i];
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
+        rest[2 * i] -= bf16_lo(w[i]);
+        rest[2 * i + 1] -= bf16_hi(w[i]);
+      }
+      f[p].w = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
+template <int N>
+struct Pieces<float, N> {
+  Frag<float> f;
+  __device__ __forceinline__ void split(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = x[i];
+  }
+};
+
+template <int N>
+__device__ __forceinline__ la_f32x4 mma(const Pieces<uint16_t, N>& a, const Frag<uint16_t>& b, la_f32x4 c) {
+#pragma unroll
+  for (int p = N - 1; p >= 0; --p) c = mma(a.f[p], b, c);  // the small ones first
+  return c;
+}
+template <int N>
+__device__ __forceinline__ la_f32x4 mma(const Pieces<float, N>& a, const Frag<float>& b, la_f32x4 c) {
+  return mma(a.f, b, c);
+}
+template <int N>
+__device__ __forceinline__ la_f32x4 mma(const Frag<uint16_t>& a, const Pieces<uint16_t, N>& b, la_f32x4 c) {
+#pragma unroll
+  for (int p = N - 1; p >= 0; --p) c = mma(a, b.f[p], c);
+  return c;
+}
+template <int N>
+__device__ __forceinline__ la_f32x4 mma(const Frag<float>& a, const Pieces<float, N>& b, la_f32x4 c) {
+  return mma(a, b.f, c);
+}
+
+__device__ __forceinline__ void widen_frag(const Frag<uint16_t>& f, float (&v)[8]) {
+  widen_raw16<uint16_t>(f.w, v);
+}
+__device__ __forceinline__ void widen_frag(const Frag<float>& f, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f.v[i];
+}
+
+// Elements between rows of a staged tile of D columns: 16 bytes more than the row, so that the 16
+// rows of an operand read start in different banks.
+template <typename Elem>
+__host__ __device__ constexpr int la_pitch(int D) {
+  return D + 16 / int(sizeof(Elem));
+}
+
+// Contraction values k0 + 8g .. + 7 of row `row`.
+__device__ __forceinline__ Frag<uint16_t> row_frag(const uint16_t* tile, int pitch, int row, int k0) {
+  const int g = (threadIdx.x & 63) >> 4;
+  Frag<uint16_t> f;
+  f.w = *reinterpret_cast<const uint4*>(tile + row * pitch + k0 + 8 * g);
+  return f;
+}
+__device__ __forceinline__ Frag<float> row_frag(const float* tile, int pitch, int row, int k0) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const float4 a = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 8 * g);
+  const float4 b = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 8 * g + 4);
+  return Frag<float>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// The same 32 values in the order in which two stacked result tiles hold them: k0 + 4g .. + 3, then
+// k0 + 16 + 4g .. + 3 (so that a state kept as results is an operand as it stands).
+__device__ __forceinline__ Frag<uint16_t> row_frag_stacked(const uint16_t* tile, int pitch, int row, int k0) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const uint2 a = *reinterpret_cast<const uint2*>(tile + row * pitch + k0 + 4 * g);
+  const uint2 b = *reinterpret_cast<const uint2*>(tile + row * pitch + k0 + 16 + 4 * g);
+  return Frag<uint16_t>{make_uint4(a.x, a.y, b.x, b.y)};
+}
+__device__ __forceinline__ Frag<float> row_frag_stacked(const float* tile, int pitch, int row, int k0) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const float4 a = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 4 * g);
+  const float4 b = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 16 + 4 * g);
+  return Frag<float>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// Column c0 + r, contraction over rows: values of rows s0 + 8g .. + 7. bf16 through the transposing
+// LDS read: of each 16 lanes, lane i supplies the address of four columns (4 (i % 4) on) of
+// row i / 4 and receives column i of the four rows.
+__device__ __forceinline__ Frag<uint16_t> col_frag(const uint16_t* tile, int pitch, int s0, int c0) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  const uint16_t* p = tile + (s0 + 8 * g + (r >> 2)) * pitch + c0 + 4 * (r & 3);
+  const la_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s16x4*)p);
+  const la_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s16x4*)(p + 4 * pitch));
+  const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+  return Frag<uint16_t>{make_uint4(x.x, x.y, y.x, y.y)};
+}
+__device__ __forceinline__ Frag<float> col_frag(const float* tile, int pitch, int s0, int c0) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  Frag<float> f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.v[i] = tile[(s0 + 8 * g + i) * pitch + c0 + r];
+  return f;
+}
+
+// Four values of a result (rows 4g .. 4g + 3 of a column) as a run of four storage elements in LDS.
+__device__ __forceinline__ void put4(uint16_t* p, const la_f32x4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void put4(float* p, const la_f32x4& v) { *reinterpret_cast<la_f32x4*>(p) = v; }
+
+// Four storage elements of LDS.
+__device__ __forceinline__ la_f32x4 get4(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return la_f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+}
+__device__ __forceinline__ la_f32x4 get4(const float* p) { return *reinterpret_cast<const la_f32x4*>(p); }
+
+// A tile of C steps x D columns on its way from memory to LDS, spread over the workgroup's threads.
+template <typename Elem, int C, int D>
+struct TileLoad {
+  static constexpr int kN = Vec<Elem>::kN, kRow = D / kN, kWords = C * kRow / kLaThreads;
+  static_assert(C * kRow % kLaThreads == 0, "whole words for every thread");
+  uint4 w[kWords];
+
+  // Rows [0, rows) of `dim` elements, `step` apart; zeros elsewhere (nothing there is read).
+  __device__ __forceinline__ void load(const Elem* base, int64_t step, int rows, int dim) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int at = int(threadIdx.x) + i * kLaThreads, row = at / kRow, col = (at % kRow) * kN;
+      const int n = row < rows ? dim - col : 0;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (n >= kN) {
+        w[i] = load16_any(base + row * step + col);
+      } else if (n > 0) {
+        float v[kN];
+        load_part_of<Elem, kN>(base + row * step + col, n, v);
+        w[i] = narrow_raw16<Elem>(v);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(Elem* tile) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int at = int(threadIdx.x) + i * kLaThreads, row = at / kRow, col = (at % kRow) * kN;
+      *reinterpret_cast<uint4*>(tile + row * la_pitch<Elem>(D) + col) = w[i];
+    }
+  }
+};
+
+// ---------------------------------------------------------------- decays
+
+__device__ __forceinline__ double dpp_f64(double v, int lane_of) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  int2 o;
+  o.x = __builtin_amdgcn_readlane(w.x, lane_of);
+  o.y = __builtin_amdgcn_readlane(w.y, lane_of);
+  return __builtin_bit_cast(double, o);
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp_add_f64(double v) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  int2 o;
+  o.x = __builtin_amdgcn_update_dpp(0, w.x, kCtrl, 0xf, 0xf, true);
+  o.y = __builtin_amdgcn_update_dpp(0, w.y, kCtrl, 0xf, 0xf, true);
+  return v + __builtin_bit_cast(double, o);
+}
+// Inclusive sums over the lanes of a wave, in 64 bits.
+__device__ __forceinline__ double wave_prefix_f64(double v) {
+  v = dpp_add_f64<0x111>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add_f64<0x112>(v);
+  v = dpp_add_f64<0x114>(v);
+  v = dpp_add_f64<0x118>(v);
+  const double a = dpp_f64(v, 15), b = dpp_f64(v, 31), c = dpp_f64(v, 47);
+  const int row = int(threadIdx.x & 63) >> 4;
+  return v + (row >= 1 ? a : 0.0) + (row >= 2 ? b : 0.0) + (row >= 3 ? c : 0.0);
+}
+
+// The log decay of a step in units of log 2. Below -1e4 it is -1e4, whose exponential is zero all
+// the same, so that a reset (-inf) leaves finite sums; NaN stays.
+__device__ __forceinline__ double log2_decay(float g) {
+  const float x = g < -1e4f ? -1e4f : g;
+  return double(x) * 1.4426950408889634074;
+}
+
+// A chunk's running decays in log 2: the sums in 64 bits kept as two floats each, because the
+// decay between two steps is a difference of sums that may be far larger than it.
+template <int C>
+struct Decays {
+  float hi[C], lo[C];  // sum over the steps up to and with t
+  float into[C];       // exp of it: from the chunk's start to t
+  float onto[C];       // from s to the chunk's end
+  float total;         // over the chunk
+
+  // Lane t < C of one wave holds the step's log2 decay (0 behind the end). Returns the sum.
+  __device__ __forceinline__ double set(double step) {
+    const int l = threadIdx.x & 63;
+    const double cs = wave_prefix_f64(step), all = dpp_f64(cs, C - 1);
+    if (l < C) {
+      const float h = float(cs);
+      hi[l] = h;
+      lo[l] = float(cs - double(h));
+      into[l] = exp2_hw(h);
+      onto[l] = exp2_hw(float(all - cs));
+      if (l == 0) total = exp2_hw(float(all));
+    }
+    return all;
+  }
+  __device__ __forceinline__ float between(int t, int s) const {
+    return exp2_hw((hi[t] - hi[s]) + (lo[t] - lo[s]));
+  }
+};
+
+// The log2 decay of step t0 + lane, 0 at and past `rows` (nothing there is read).
+__device__ __forceinline__ double load_decay(const float* g, int64_t step, int64_t t0, int rows) {
+  const int l = threadIdx.x & 63;
+  return g && l < rows ? log2_decay(g[(t0 + l) * step]) : 0.0;
+}
+
+__device__ __forceinline__ int64_t row_end(const int32_t* lengths, int64_t b, int64_t seqlen) {
+  if (!lengths) return seqlen;
+  const int64_t n = lengths[b];
+  return n < 0 ? 0 : n > seqlen ? seqlen : n;
+}
+
+// The causal 16 x 16 tiles of a chunk's pairs of steps, row by row: tile `at` is (i, j), j <= i.
+__device__ __forceinline__ void causal_tile(int at, int& i, int& j) {
+  i = at >= 6 ? 3 : at >= 3 ? 2 : at >= 1 ? 1 : 0;
+  j = at - i * (i + 1) / 2;
+}
+
+}  // namespace ssm

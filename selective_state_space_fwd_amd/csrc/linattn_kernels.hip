@@ -1,0 +1,561 @@
+// Linear attention with a decay for each head on the gfx950 matrix cores (include/ssm_linattn.h).
+//
+//   S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+//
+// In chunks of C steps, with cs_t the running sum of g over the chunk:
+//
+//   o_t   = scale sum_{s<=t} exp(cs_t - cs_s) (q_t . k_s) v_s + scale exp(cs_t) S_in q_t
+//   S_out = exp(cs_end) S_in + sum_s exp(cs_end - cs_s) v_s k_s^T
+//
+// linattn_fwd_kernel: one workgroup walks the chunks of a (batch row, head, tile of 64 or 128 value
+// channels, segment of the sequence), the state dk x its channels in the accumulators of its
+// four waves (16 or 32 channels each), which are the state's product's operand as they stand.
+// A sequence is one segment where batch rows and heads fill the device; else
+// linattn_state_kernel finds what each segment adds to the state, linattn_join_kernel the state
+// at each segment's start, and the segments run side by side.
+//
+// Roundings: the pairs' weights are rounded to bf16 once, as an operand, like the result (its error
+// is as large as the result's own rounding). The state enters its product in two bf16 pieces
+// (16 bits): in one its error would add to that of the weights. What is added to the state enters
+// in three pieces, all 24 bits, since the state is a result in fp32.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_linattn.h"
+#include "linattn_launch.h"
+
+namespace ssm {
+namespace {
+
+// ---------------------------------------------------------------- forward
+
+struct FwdParams {
+  HeadRows q, k, v;
+  const float* g;
+  int64_t g_batch, g_step, g_head;
+  const float* initial;
+  const int32_t* lengths;
+  void* out;
+  float* final_state;
+  const float* states;   // nullable: [batch, heads, segments, pad(dv), pad(dk)], segment starts
+  int64_t seqlen, chunks, per, segments;
+  int64_t kpad, state_floats;
+  int heads, group, dk, dv, value_tiles;
+  float scale;
+};
+
+template <typename Elem, int KP, int NV>
+__global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_kernel(FwdParams p) {
+  constexpr int C = chunk_of<Elem>(), T = C / 16, SB = C / 32, VT = 64 * NV, KB = KP / 32;
+  constexpr int kPairs = T * (T + 1) / 2, QP = la_pitch<Elem>(KP), VP = la_pitch<Elem>(VT),
+                PP = la_pitch<Elem>(C);
+  __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * VP], sP[C * PP];
+  __shared__ Decays<C> dec;
+
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  int64_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int vt = int(at % p.value_tiles);
+  at /= p.value_tiles;
+  const int h = int(at % p.heads);
+  at /= p.heads;
+  const int64_t seg = at % p.segments, b = at / p.segments;
+  const int hk = h / p.group, v0 = vt * VT;
+  const Elem* q = static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head;
+  const Elem* k = static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head;
+  const Elem* v = static_cast<const Elem*>(p.v.p) + b * p.v.batch + h * p.v.head + v0;
+  const float* gates = p.g ? p.g + b * p.g_batch + h * p.g_head : nullptr;
+  Elem* out = static_cast<Elem*>(p.out) + (b * p.seqlen * p.heads + h) * p.dv;
+  const int64_t out_step = int64_t(p.heads) * p.dv;
+  const int64_t end = row_end(p.lengths, b, p.seqlen);
+  const int64_t c0 = seg * p.per, c1 = c0 + p.per < p.chunks ? c0 + p.per : p.chunks;
+
+  // The state: tile (j, n) is rows k = 16 j + 4 g + i of column v = vcol + 16 n + r.
+  const int vcol = v0 + 16 * NV * w;
+  la_f32x4 S[KP / 16][NV];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int vc = vcol + 16 * n + r;
+    const float* from = nullptr;
+    if (vc < p.dv) {
+      if (p.states)
+        from = p.states + ((b * p.heads + h) * p.segments + seg) * p.state_floats + vc * p.kpad;
+      else if (p.initial)
+        from = p.initial + ((b * p.heads + h) * p.dv + vc) * p.dk;
+    }
+#pragma unroll
+    for (int j = 0; j < KP / 16; ++j) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int kr = 16 * j + 4 * g;
+      if (from && kr < p.dk) load_few<float, 4>(from + kr, p.dk - kr, s);
+      S[j][n] = la_f32x4{s[0], s[1], s[2], s[3]};
+    }
+  }
+  // Tiles of pairs above the diagonal that share an operand with one below it.
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int i = 0; i < T; i += 2) put4(&sP[(16 * i + r) * PP + 16 * (i + 1) + 4 * g], la_f32x4{0, 0, 0, 0});
+  }
+
+  TileLoad<Elem, C, KP> lq, lk;
+  TileLoad<Elem, C, VT> lv;
+  double gate = 0.0;
+  auto fetch = [&](int64_t c) {
+    const int64_t t0 = c * C;
+    const int rows = t0 >= end || c >= c1 ? 0 : end - t0 < C ? int(end - t0) : C;
+    lq.load(q + t0 * p.q.step, p.q.step, rows, p.dk);
+    lk.load(k + t0 * p.k.step, p.k.step, rows, p.dk);
+    lv.load(v + t0 * p.v.step, p.v.step, rows, p.dv - v0);
+    if (w == 0) gate = load_decay(gates, p.g_step, t0, rows);
+  };
+  fetch(c0);
+  for (int64_t c = c0; c < c1; ++c) {
+    const int64_t t0 = c * C;
+    const int rows = p.seqlen - t0 < C ? int(p.seqlen - t0) : C;       // of out
+    const int live = end <= t0 ? 0 : end - t0 < C ? int(end - t0) : C;  // that hold steps
+    if (live > 0) {
+      lds_barrier();  // every wave has read the chunk before
+      lq.store(sQ);
+      lk.store(sK);
+      lv.store(sV);
+      if (w == 0) dec.set(gate);
+      lds_barrier();
+      fetch(c + 1);
+      // The weights of the pairs s <= t, with the decay between them: tile (i, j) as rows s of
+      // columns t, stored by rows t.
+#pragma unroll
+      for (int x = 0; x < (kPairs + 3) / 4; ++x) {
+        const int pair = w + 4 * x;
+        if (pair < kPairs) {
+          int i, j;
+          causal_tile(pair, i, j);
+          la_f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+            a = mma(row_frag(sK, QP, 16 * j + r, 32 * kb), row_frag(sQ, QP, 16 * i + r, 32 * kb), a);
+          const int t = 16 * i + r;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int s = 16 * j + 4 * g + e;
+            a[e] = s <= t ? a[e] * p.scale * dec.between(t, s) : 0.0f;
+          }
+          put4(&sP[t * PP + 16 * j + 4 * g], a);
+        }
+      }
+      Frag<Elem> vf[SB][NV];
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) vf[sb][n] = col_frag(sV, VP, 32 * sb, 16 * (NV * w + n));
+      Pieces<Elem, 2> sp[KB][NV];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          const la_f32x4 x = S[2 * kb][n], y = S[2 * kb + 1][n];
+          sp[kb][n].split({x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+        }
+      lds_barrier();
+      // Results as rows v of columns t.
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        la_f32x4 o[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) o[n] = la_f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const Frag<Elem> f = row_frag_stacked(sQ, QP, 16 * i + r, 32 * kb);
+#pragma unroll
+          for (int n = 0; n < NV; ++n) o[n] = mma(sp[kb][n], f, o[n]);
+        }
+        const int t = 16 * i + r;
+        const float into = dec.into[t] * p.scale;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= into;
+#pragma unroll
+        for (int sb = 0; sb <= i / 2; ++sb) {
+          const Frag<Elem> f = row_frag(sP, PP, 16 * i + r, 32 * sb);
+#pragma unroll
+          for (int n = 0; n < NV; ++n) o[n] = mma(vf[sb][n], f, o[n]);
+        }
+        if (t < rows) {
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const int vr = vcol + 16 * n + 4 * g;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = t < live ? o[n][e] : 0.0f;
+            if (vr < p.dv) store_few<Elem, 4>(out + (t0 + t) * out_step + vr, p.dv - vr, y);
+          }
+        }
+      }
+      // The state at the chunk's end.
+      const float total = dec.total;
+      Pieces<Elem, 3> add[SB][NV];
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) {
+        float on[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) on[e] = dec.onto[32 * sb + 8 * g + e];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          float x[8];
+          widen_frag(vf[sb][n], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= on[e];
+          add[sb][n].split(x);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KP / 16; ++j) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[j][n][e] *= total;
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) {
+          const Frag<Elem> f = col_frag(sK, QP, 32 * sb, 16 * j);
+#pragma unroll
+          for (int n = 0; n < NV; ++n) S[j][n] = mma(f, add[sb][n], S[j][n]);
+        }
+      }
+    } else {
+      // Behind the row's end: zeros, and the state stays.
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const int t = 16 * i + r;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          const int vr = vcol + 16 * n + 4 * g;
+          const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (t < rows && vr < p.dv) store_few<Elem, 4>(out + (t0 + t) * out_step + vr, p.dv - vr, zero);
+        }
+      }
+    }
+  }
+  if (p.final_state && seg == p.segments - 1) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int vc = vcol + 16 * n + r;
+      if (vc >= p.dv) continue;
+      float* to = p.final_state + ((b * p.heads + h) * p.dv + vc) * p.dk;
+#pragma unroll
+      for (int j = 0; j < KP / 16; ++j) {
+        const int kr = 16 * j + 4 * g;
+        const float s[4] = {S[j][n][0], S[j][n][1], S[j][n][2], S[j][n][3]};
+        if (kr < p.dk) store_few<float, 4>(to + kr, p.dk - kr, s);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- states of segments
+
+// What the steps of a segment add to a state: sum_s weight_s y_s x_s^T, rows y, x contiguous. Forward
+// (x = k, y = v, or exchanged): weight_s = exp(sum of g behind s in the segment). Reverse (the
+// adjoint: x and y of dout and q): weight_t = scale exp(sum of g from the segment's start to t).
+struct StateParams {
+  HeadRows x, y;
+  int x_group, y_group;   // heads of the sequence to one of the array's
+  int xd, yd;
+  bool reverse;
+  float scale;
+  float* states;          // [batch, heads, segments, pad(yd), pad(xd)]
+};
+
+struct StatesParams {
+  StateParams dir[2];
+  const float* g;
+  int64_t g_batch, g_step, g_head;
+  const int32_t* lengths;
+  float* totals;          // [batch, heads, segments]: log2 decay over the segment
+  int64_t seqlen, chunks, per, segments, rows;  // rows = batch * heads * segments
+  int heads, y_tiles;
+};
+
+template <typename Elem, int XP, int NY>
+__global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_kernel(StatesParams p) {
+  constexpr int C = chunk_of<Elem>(), SB = C / 32, YT = 64 * NY;
+  constexpr int XPITCH = la_pitch<Elem>(XP), YPITCH = la_pitch<Elem>(YT);
+  __shared__ __attribute__((aligned(16))) Elem sX[C * XPITCH], sY[C * YPITCH];
+  __shared__ Decays<C> dec;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  int64_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int yt = int(at % p.y_tiles);
+  at /= p.y_tiles;
+  const int which = at >= p.rows ? 1 : 0;
+  const StateParams& d = p.dir[which];
+  at -= which ? p.rows : 0;
+  const int64_t state = at;
+  const int64_t seg = at % p.segments;
+  at /= p.segments;
+  const int h = int(at % p.heads);
+  const int64_t b = at / p.heads;
+  const int y0 = yt * YT;
+  const Elem* x = static_cast<const Elem*>(d.x.p) + b * d.x.batch + (h / d.x_group) * d.x.head;
+  const Elem* y = static_cast<const Elem*>(d.y.p) + b * d.y.batch + (h / d.y_group) * d.y.head + y0;
+  const float* gates = p.g ? p.g + b * p.g_batch + h * p.g_head : nullptr;
+  const int64_t end = row_end(p.lengths, b, p.seqlen);
+  const int64_t c0 = seg * p.per, c1 = c0 + p.per < p.chunks ? c0 + p.per : p.chunks, n = c1 - c0;
+
+  la_f32x4 S[XP / 16][NY];
+#pragma unroll
+  for (int j = 0; j < XP / 16; ++j)
+#pragma unroll
+    for (int m = 0; m < NY; ++m) S[j][m] = la_f32x4{0, 0, 0, 0};
+  double all = 0.0;
+  TileLoad<Elem, C, XP> lx;
+  TileLoad<Elem, C, YT> ly;
+  double gate = 0.0;
+  auto fetch = [&](int64_t i) {
+    const int64_t c = d.reverse ? c1 - 1 - i : c0 + i, t0 = c * C;
+    const int rows = i >= n || t0 >= end ? 0 : end - t0 < C ? int(end - t0) : C;
+    lx.load(x + (rows ? t0 : 0) * d.x.step, d.x.step, rows, d.xd);
+    ly.load(y + (rows ? t0 : 0) * d.y.step, d.y.step, rows, d.yd - y0);
+    if (w == 0) gate = load_decay(gates, p.g_step, t0, rows);
+  };
+  fetch(0);
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t c = d.reverse ? c1 - 1 - i : c0 + i;
+    if (c * C >= end) {
+      fetch(i + 1);
+      continue;
+    }
+    lds_barrier();
+    lx.store(sX);
+    ly.store(sY);
+    if (w == 0) all += dec.set(gate);
+    lds_barrier();
+    fetch(i + 1);
+    const float total = dec.total;
+    Pieces<Elem, 3> add[SB][NY];
+#pragma unroll
+    for (int sb = 0; sb < SB; ++sb) {
+      float weight[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int s = 32 * sb + 8 * g + e;
+        weight[e] = d.reverse ? dec.into[s] * d.scale : dec.onto[s];
+      }
+#pragma unroll
+      for (int m = 0; m < NY; ++m) {
+        float v[8];
+        widen_frag(col_frag(sY, YPITCH, 32 * sb, 16 * (NY * w + m)), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= weight[e];
+        add[sb][m].split(v);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < XP / 16; ++j) {
+#pragma unroll
+      for (int m = 0; m < NY; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][m][e] *= total;
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) {
+        const Frag<Elem> f = col_frag(sX, XPITCH, 32 * sb, 16 * j);
+#pragma unroll
+        for (int m = 0; m < NY; ++m) S[j][m] = mma(f, add[sb][m], S[j][m]);
+      }
+    }
+  }
+  const int xpad = int(linattn_pad(d.xd, 32)), ypad = int(linattn_pad(d.yd, 32));
+  float* to = d.states + state * (int64_t(xpad) * ypad);
+#pragma unroll
+  for (int m = 0; m < NY; ++m) {
+    const int yc = y0 + 16 * (NY * w + m) + r;
+    if (yc >= ypad) continue;
+#pragma unroll
+    for (int j = 0; j < XP / 16; ++j)
+      if (16 * j < xpad) *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 16 * j + 4 * g) = S[j][m];
+  }
+  if (which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
+}
+
+// ---------------------------------------------------------------- the states at segments' starts
+
+// In place, over the segments of a (batch row, head) in order: each state is exchanged for the one
+// before it (forward: the state at the segment's start; reverse: the adjoint behind the
+// segment). Four values a thread, loads eight segments ahead of the sums.
+struct JoinDir {
+  float* states;
+  const float* first;   // nullable: [batch, heads, dv, dk]
+  float* last;          // nullable: the same
+  bool reverse;
+};
+struct JoinParams {
+  JoinDir dir[2];
+  const float* totals;
+  int64_t segments, state_floats;
+  int cols;                     // of a stored row, padded
+  int row_count, col_count;     // without padding
+  int64_t row_stride, col_stride;  // of `first` and `last`
+  int64_t ext_floats;
+  int64_t blocks;                  // workgroups of a head
+};
+
+__global__ __launch_bounds__(256) void linattn_join_kernel(JoinParams p) {
+  const JoinDir& d = p.dir[blockIdx.y];
+  const int64_t head = blockIdx.x / uint32_t(p.blocks);
+  const int64_t at = (int64_t(blockIdx.x % uint32_t(p.blocks)) * 256 + threadIdx.x) * 4;
+  if (at >= p.state_floats) return;
+  const int row = int(at / p.cols), col = int(at % p.cols);
+  float* base = d.states + head * p.segments * p.state_floats + at;
+  const float* totals = p.totals + head * p.segments;
+  const bool in = row < p.row_count;
+  const int64_t ext = head * p.ext_floats + row * p.row_stride + col * p.col_stride;
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = d.first && in && col + i < p.col_count ? d.first[ext + i * p.col_stride] : 0.0f;
+  constexpr int kAhead = 8;
+  for (int64_t n = 0; n < p.segments; n += kAhead) {
+    la_f32x4 add[kAhead];
+    float total[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t m = n + i < p.segments ? n + i : p.segments - 1, seg = d.reverse ? p.segments - 1 - m : m;
+      add[i] = *reinterpret_cast<const la_f32x4*>(base + seg * p.state_floats);
+      total[i] = totals[seg];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n + i < p.segments) {
+        const int64_t seg = d.reverse ? p.segments - 1 - (n + i) : n + i;
+        *reinterpret_cast<la_f32x4*>(base + seg * p.state_floats) = la_f32x4{s[0], s[1], s[2], s[3]};
+        const float keep = exp2_hw(total[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(keep, s[e], add[i][e]);
+      }
+    }
+  }
+  if (d.last && in) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < p.col_count) d.last[ext + i * p.col_stride] = s[i];
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename Elem, int XP, int NY>
+void run_states(const StatesParams& p, int dirs, hipStream_t s) {
+  hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY>), dim3(uint32_t(p.rows * p.y_tiles * dirs)),
+                     dim3(kLaThreads), 0, s, p);
+}
+
+template <typename Elem>
+void run_states_of(StatesParams& p, int dirs, hipStream_t s) {
+  const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = yd <= 64 || xd > 128 ? 1 : 2;
+  p.y_tiles = (yd + 64 * ny - 1) / (64 * ny);
+  if (ny == 1) {
+    if (xd <= 64) return run_states<Elem, 64, 1>(p, dirs, s);
+    if (xd <= 128) return run_states<Elem, 128, 1>(p, dirs, s);
+    return run_states<Elem, 256, 1>(p, dirs, s);
+  }
+  if (xd <= 64) return run_states<Elem, 64, 2>(p, dirs, s);
+  run_states<Elem, 128, 2>(p, dirs, s);
+}
+
+template <typename Elem>
+void run_fwd(const FwdParams& p, int64_t groups, hipStream_t s) {
+  const dim3 grid{uint32_t(groups)}, block{kLaThreads};
+  if (linattn_value_tile(p.dk, p.dv) == 64) {
+    if (p.dk <= 64) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 64, 1>), grid, block, 0, s, p);
+    else if (p.dk <= 128) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 128, 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 256, 1>), grid, block, 0, s, p);
+  } else {
+    if (p.dk <= 64) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 64, 2>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 128, 2>), grid, block, 0, s, p);
+  }
+}
+
+}  // namespace
+
+// Both directions' states of every chunk, for the backward, as [dk][dv]; then the states at the
+// chunks' starts and the adjoints behind them. Workspace: states, adjoints, totals.
+int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t c = linattn_chunk(a.io), chunks = (a.seqlen + c - 1) / c;
+  const int64_t floats = linattn_state_floats(a.dk, a.dv), rows = a.batch * a.heads * chunks;
+  const int group = int(a.heads / a.qk_heads);
+  float* adjoints = a.workspace + rows * floats;
+  StatesParams p{};
+  p.dir[0] = StateParams{a.v, a.k, 1, group, int(a.dv), int(a.dk), false, 1.0f, a.workspace};
+  p.dir[1] = StateParams{a.dout, a.q, 1, group, int(a.dv), int(a.dk), true, a.scale, adjoints};
+  p.g = a.g;
+  p.g_batch = a.g_batch, p.g_step = a.g_step, p.g_head = a.g_head;
+  p.lengths = a.lengths;
+  p.totals = adjoints + rows * floats;
+  p.seqlen = a.seqlen, p.chunks = chunks, p.per = 1, p.segments = chunks, p.rows = rows;
+  p.heads = int(a.heads);
+  if (chunks > 0) {
+    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 2, s);
+    else run_states_of<float>(p, 2, s);
+    if (hipGetLastError() != hipSuccess) return -1;
+  }
+  JoinParams j{};
+  j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
+  j.dir[1] = JoinDir{adjoints, a.dfinal, a.dinitial, true};
+  j.totals = p.totals;
+  j.segments = chunks, j.state_floats = floats;
+  j.cols = int(linattn_pad(a.dv, 32));
+  j.row_count = int(a.dk), j.col_count = int(a.dv);
+  j.row_stride = 1, j.col_stride = a.dk, j.ext_floats = a.dk * a.dv;
+  j.blocks = linattn_join_blocks(floats);
+  if (a.batch == 0) return 0;
+  hipLaunchKernelGGL(linattn_join_kernel, dim3(uint32_t(j.blocks * a.batch * a.heads), 2), dim3(256), 0, s, j);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const LinattnSegments seg = linattn_segments(a.batch, a.heads, a.dk, a.dv, a.seqlen, a.io);
+  const int64_t floats = linattn_state_floats(a.dv, a.dk), rows = a.batch * a.heads * seg.count;
+  const int group = int(a.heads / a.qk_heads);
+  if (seg.count > 1) {
+    StatesParams p{};
+    p.dir[0] = StateParams{a.k, a.v, group, 1, int(a.dk), int(a.dv), false, 1.0f, a.workspace};
+    p.g = a.g;
+    p.g_batch = a.g_batch, p.g_step = a.g_step, p.g_head = a.g_head;
+    p.lengths = a.lengths;
+    p.totals = a.workspace + rows * floats;
+    p.seqlen = a.seqlen, p.chunks = seg.chunks, p.per = seg.per, p.segments = seg.count, p.rows = rows;
+    p.heads = int(a.heads);
+    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 1, s);
+    else run_states_of<float>(p, 1, s);
+    if (hipGetLastError() != hipSuccess) return -1;
+    JoinParams j{};
+    j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
+    j.totals = p.totals;
+    j.segments = seg.count, j.state_floats = floats;
+    j.cols = int(linattn_pad(a.dk, 32));
+    j.row_count = int(a.dv), j.col_count = int(a.dk);
+    j.row_stride = a.dk, j.col_stride = 1, j.ext_floats = a.dk * a.dv;
+    j.blocks = linattn_join_blocks(floats);
+    hipLaunchKernelGGL(linattn_join_kernel, dim3(uint32_t(j.blocks * a.batch * a.heads)), dim3(256), 0, s, j);
+    if (hipGetLastError() != hipSuccess) return -1;
+  }
+  FwdParams p{};
+  p.q = a.q, p.k = a.k, p.v = a.v;
+  p.g = a.g;
+  p.g_batch = a.g_batch, p.g_step = a.g_step, p.g_head = a.g_head;
+  p.initial = a.initial;
+  p.lengths = a.lengths;
+  p.out = a.out;
+  p.final_state = a.final_state;
+  p.states = seg.count > 1 ? a.workspace : nullptr;
+  p.seqlen = a.seqlen, p.chunks = seg.chunks, p.per = seg.per, p.segments = seg.count;
+  p.kpad = linattn_pad(a.dk, 32), p.state_floats = floats;
+  p.heads = int(a.heads), p.group = group, p.dk = int(a.dk), p.dv = int(a.dv);
+  p.value_tiles = int(linattn_value_tiles(a.dk, a.dv));
+  p.scale = a.scale;
+  if (a.io == Io::BF16) run_fwd<uint16_t>(p, rows * p.value_tiles, s);
+  else run_fwd<float>(p, rows * p.value_tiles, s);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace ssm

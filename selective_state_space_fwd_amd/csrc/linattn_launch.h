@@ -1,0 +1,122 @@
+// Internal interface between the C-ABI layer of linear attention (linattn_api.cpp) and its
+// kernels. Not installed; the public ABI is include/ssm_linattn.h.
+#pragma once
+#include <stdint.h>
+
+#include "block_launch.h"
+
+namespace ssm {
+
+constexpr int kLinattnMaxDim = 256;  // dk and dv
+
+// Steps of a chunk: 64, or 32 in fp32, whose tiles would not fit LDS at 256 columns otherwise.
+constexpr int linattn_chunk(Io io) { return io == Io::BF16 ? 64 : 32; }
+
+// A [batch, seqlen, heads, dim] array whose last axis is contiguous; element strides.
+struct HeadRows {
+  const void* p;
+  int64_t batch, step, head;
+};
+
+struct LinattnArgs {
+  HeadRows q, k, v;
+  const float* g;            // nullable: log decays, strides below (0 along broadcast axes)
+  int64_t g_batch, g_step, g_head;
+  const float* initial;      // nullable: [batch, heads, dv, dk]
+  const int32_t* lengths;    // nullable: [batch]
+  void* out;                 // [batch, seqlen, heads, dv]
+  float* final_state;        // nullable: [batch, heads, dv, dk]
+  // backward
+  HeadRows dout;
+  const float* dfinal;       // nullable
+  void *dq, *dk_, *dv_;      // contiguous
+  float* dg;                 // nullable: [batch, seqlen, heads], or [heads] where dg_per_head
+  bool dg_per_head;
+  float* dinitial;           // nullable
+  float* workspace;
+  int64_t batch, seqlen, qk_heads, heads, dk, dv;
+  float scale;
+  Io io;
+};
+
+// Columns of dv that a workgroup of the forward takes: its waves keep the state of dk x that many
+// in registers, with room for the operands next to it.
+constexpr int linattn_value_tile(int64_t dk, int64_t dv) { return dv <= 64 || dk > 128 ? 64 : 128; }
+constexpr int64_t linattn_value_tiles(int64_t dk, int64_t dv) {
+  return (dv + linattn_value_tile(dk, dv) - 1) / linattn_value_tile(dk, dv);
+}
+constexpr int64_t linattn_pad(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// How the forward cuts a sequence into segments that run side by side, each from a state that
+// two small launches before it find.
+struct LinattnSegments {
+  int64_t chunks;   // of a row
+  int64_t per;      // chunks of a segment
+  int64_t count;
+};
+inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk, int64_t dv, int64_t seqlen,
+                                        Io io) {
+  LinattnSegments s;
+  const int64_t c = linattn_chunk(io);
+  s.chunks = (seqlen + c - 1) / c;
+  const int64_t base = batch * heads * linattn_value_tiles(dk, dv);
+  int64_t want = base > 0 && base < 384 ? (512 + base - 1) / base : 1;
+  const int64_t most = s.chunks / 4 > 0 ? s.chunks / 4 : 1;  // four chunks a segment at least
+  if (want > most) want = most;
+  s.per = s.chunks > 0 ? (s.chunks + want - 1) / want : 1;
+  s.count = s.chunks > 0 ? (s.chunks + s.per - 1) / s.per : 1;
+  return s;
+}
+
+// Floats of one state in the workspace of the backward, [dk][dv], both padded so that operand
+// reads stay inside.
+inline int64_t linattn_state_floats(int64_t rows, int64_t cols) {
+  return linattn_pad(rows, 32) * linattn_pad(cols, 32);
+}
+
+inline int64_t linattn_join_blocks(int64_t state_floats) { return (state_floats / 4 + 255) / 256; }
+
+int launch_linattn_chunk_states(const LinattnArgs& a, void* stream);
+int launch_linattn_fwd(const LinattnArgs& a, void* stream);
+int launch_linattn_bwd(const LinattnArgs& a, void* stream);
+
+// ---------------------------------------------------------------- single tokens
+
+constexpr int kLinattnStepWaves = 4;
+
+// Rows of the state per lane, of 2^lg lanes a row (no more than a lane for each row's v): many
+// where the call fills the device, so that a lane has as many loads in flight; few else.
+constexpr int linattn_step_most_rows(int lg) { return lg >= 3 ? 8 : 1 << lg; }
+constexpr int linattn_step_few_rows(int lg) { return lg >= 1 ? 2 : 1; }
+
+struct LinattnStepForm {
+  int rows;
+  bool past_caches;         // the states are too many for the GPU's caches to keep
+  int64_t tiles, groups;    // workgroups of a head, and of a batch row
+};
+inline LinattnStepForm linattn_step_form(int64_t batch, int64_t heads, int64_t dk, int64_t dv) {
+  const int lg = step_lanes_log2(dk), most = linattn_step_most_rows(lg), per = 64 >> lg;
+  const bool many = batch * heads * dv / (most * per) >= 8192;
+  LinattnStepForm f{};
+  f.rows = many ? most : linattn_step_few_rows(lg);
+  f.past_caches = many && batch * heads * dk * dv * 4 >= (int64_t(1) << 27);
+  const int64_t tile = int64_t(kLinattnStepWaves) * f.rows * per;
+  f.tiles = (dv + tile - 1) / tile;
+  f.groups = f.tiles * heads;
+  return f;
+}
+
+struct LinattnStepArgs {
+  HeadRows q, k, v;          // (no step axis)
+  const float* g;            // nullable
+  int64_t g_batch, g_head;
+  float* state;              // [nslots, heads, dv, dk]
+  const int32_t* slots;      // nullable
+  void* out;                 // [batch, heads, dv]
+  int64_t batch, nslots, qk_heads, heads, dk, dv;
+  float scale;
+  Io io;
+};
+int launch_linattn_step(const LinattnStepArgs& a, void* stream);
+
+}  // namespace ssm
