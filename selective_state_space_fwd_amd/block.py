@@ -52,6 +52,8 @@ class _NoModule:
         return None
 
     conv = conv_step = state_step = norm = conv_backward = norm_backward = _makes_none
+    bind_linattn = linattn = linattn_backward = linattn_step = _makes_none
+    qk_norm = qk_norm_backward = _makes_none
 
 
 def _lib() -> ctypes.CDLL:

@@ -61,9 +61,8 @@ inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk
   s.chunks = (seqlen + c - 1) / c;
   const int64_t base = batch * heads * linattn_value_tiles(dk, dv);
   int64_t want = base > 0 && base < 384 ? (512 + base - 1) / base : 1;
-  const int64_t most = s.chunks / 4 > 0 ? s.chunks / 4 : 1;  // four chunks a segment at least
-  if (want > most) want = most;
-  s.per = s.chunks > 0 ? (s.chunks + want - 1) / want : 1;
+  if (want > s.chunks) want = s.chunks;
+  s.per = want > 0 ? (s.chunks + want - 1) / want : 1;
   s.count = s.chunks > 0 ? (s.chunks + s.per - 1) / s.per : 1;
   return s;
 }

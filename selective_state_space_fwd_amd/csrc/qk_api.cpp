@@ -17,7 +17,7 @@ using ssm_api::Ranges;
 namespace {
 
 struct Sizes {
-  int64_t esz, q_bytes, k_bytes, table_bytes, groups;
+  int64_t esz, q_bytes, k_bytes, table_bytes, workspace;
 };
 
 int check_sizes(uint32_t flags, int64_t batch, int64_t seqlen, int64_t q_heads, int64_t k_heads, int64_t dim,
@@ -34,10 +34,12 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t seqlen, int64_t q_heads, 
   z->table_bytes = product({table_rows, rot / 2, 4});
   const int64_t steps = product({batch, seqlen, 4}), rows = product({batch, seqlen, q_heads + k_heads});
   if (z->q_bytes < 0 || z->k_bytes < 0 || z->table_bytes < 0 || steps < 0 || rows < 0) return SSM_ERR_UNSUPPORTED;
-  const int lg = ssm::qk_lanes_log2(dim, rot);
-  z->groups = ssm::qk_groups(
-      ssm::qk_items(batch, seqlen, q_heads, k_heads, ssm::qk_rows(batch, seqlen, q_heads + k_heads, lg)).items, lg);
-  return ssm::grid_fits(z->groups, 64 * ssm::kQkWaves) ? SSM_OK : SSM_ERR_UNSUPPORTED;
+  const int lg = ssm::qk_lanes_log2(dim, rot), per = ssm::qk_rows(batch, seqlen, q_heads + k_heads, lg);
+  const int64_t q_items = ssm::qk_items(batch, seqlen, q_heads, per), k_items = ssm::qk_items(batch, seqlen, k_heads, per);
+  if (seqlen > kInt32Max || q_items > ssm::kQkMostItems || k_items > ssm::kQkMostItems) return SSM_ERR_UNSUPPORTED;
+  const int64_t q_groups = ssm::qk_groups(q_items, lg), k_groups = ssm::qk_groups(k_items, lg);
+  z->workspace = (ssm::qk_partials(q_groups) + ssm::qk_partials(k_groups)) * dim * 4;
+  return ssm::grid_fits(q_groups + k_groups, 64 * ssm::kQkWaves) ? SSM_OK : SSM_ERR_UNSUPPORTED;
 }
 
 ssm::QkArgs common(const ssm::HeadRows& q, const ssm::HeadRows& k, const float* q_weight, const float* k_weight,
@@ -103,7 +105,7 @@ int64_t ssm_qk_norm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t q
                                         int64_t rot, uint32_t flags) {
   Sizes z;
   if (check_sizes(flags, batch, seqlen, q_heads, k_heads, dim, rot, 0, &z) != SSM_OK) return -1;
-  return ssm::qk_partials(z.groups) * 2 * dim * 4;
+  return z.workspace;
 }
 
 int ssm_qk_norm_bwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
@@ -124,7 +126,7 @@ int ssm_qk_norm_bwd(const void* q, const int64_t* q_strides, const void* k, cons
       (st = check_heads(dk_out, dk_out_strides, batch, seqlen, k_heads, dim, z.esz, &dkr, &dkb)))
     return st;
   const bool sums = dq_weight || dk_weight;
-  const int64_t need = sums ? ssm::qk_partials(z.groups) * 2 * dim * 4 : 0;
+  const int64_t need = sums ? z.workspace : 0;
   if ((qb > 0 && (!q || !dq_out || !dq)) || (kb > 0 && (!k || !dk_out || !dk)) ||
       (z.table_bytes > 0 && (!cos || !sin)) || (need > 0 && (!workspace || workspace_bytes < need)))
     return SSM_ERR_INVALID_ARG;

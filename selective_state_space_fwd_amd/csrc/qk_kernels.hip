@@ -29,17 +29,20 @@ struct QkSide {
   int64_t dy_batch, dy_step, dy_head;
   const float* weight;
   void* out;
+  float* partials;           // backward, nullable: [workgroups, dim]
+  uint32_t items, parts;     // all, and of a step
   int heads;
 };
 
 struct QkParams {
   QkSide side[2];
+  uint32_t q_groups;         // workgroups of q, before those of k
   const float *cos, *sin;
   const int32_t* positions;
   float eps, inv_dim;
-  float* partials;           // backward, nullable: [workgroups, 2, dim]
-  int64_t items, seqlen, table_rows;
-  int q_parts, parts, dim, rot, turning;  // turning: lanes of a row that hold pairs
+  int64_t table_rows;
+  uint32_t seqlen;
+  int dim, rot, turning;     // turning: lanes of a row that hold pairs
   int interleaved;
 };
 
@@ -108,27 +111,26 @@ __device__ __forceinline__ void turn(float (&v)[8], const float (&c)[4], const f
   for (int i = 0; i < 8; ++i) v[i] = o[i];
 }
 
-// One item: its side, heads, step and angles.
+// One item: its heads, step and angles.
 struct Item {
-  int side, head0;
-  int64_t b, t;
+  uint32_t b, t;
+  int head0;
   bool live, at_table;
 };
 
-__device__ __forceinline__ Item item_of(int64_t at, const QkParams& p, int rows) {
+__device__ __forceinline__ Item item_of(uint32_t at, const QkSide& d, uint32_t seqlen, int rows) {
   Item x;
-  x.live = at < p.items;
-  const int64_t step = (x.live ? at : 0) / p.parts;
-  const int part = int((x.live ? at : 0) % p.parts);
-  x.side = part >= p.q_parts ? 1 : 0;
-  x.head0 = (x.side ? part - p.q_parts : part) * rows;
-  x.b = step / p.seqlen;
-  x.t = step % p.seqlen;
+  x.live = at < d.items;
+  at = x.live ? at : 0;
+  const uint32_t step = at / d.parts;
+  x.head0 = int(at - step * d.parts) * rows;
+  x.b = step / seqlen;
+  x.t = step - x.b * seqlen;
   return x;
 }
 
 __device__ __forceinline__ void load_angles(const QkParams& p, Item& x, const Runs& u, float (&c)[4], float (&s)[4]) {
-  const int64_t pos = p.positions ? p.positions[x.b * p.seqlen + x.t] : x.t;
+  const int64_t pos = p.positions ? p.positions[int64_t(x.b) * p.seqlen + x.t] : x.t;
   x.at_table = p.rot == 0 || (pos >= 0 && pos < p.table_rows);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -144,11 +146,13 @@ __device__ __forceinline__ void load_angles(const QkParams& p, Item& x, const Ru
 
 template <typename Elem, int LG, int R>
 __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkParams p) {
+  constexpr uint32_t kPer = kThreads >> LG;  // items of a workgroup
   const int lane = threadIdx.x & ((1 << LG) - 1);
-  const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> LG;
-  Item x = item_of(at, p, R);
+  const int side = blockIdx.x >= p.q_groups ? 1 : 0;
+  const QkSide& d = p.side[side];
+  const uint32_t group = blockIdx.x - (side ? p.q_groups : 0);
+  Item x = item_of(group * kPer + (threadIdx.x >> LG), d, p.seqlen, R);
   if (!x.live) return;
-  const QkSide& d = p.side[x.side];
   const Runs u = runs_of(lane, p);
   const Elem* from = static_cast<const Elem*>(d.x) + x.b * d.batch + x.t * d.step + x.head0 * d.head;
   const int rows = d.heads - x.head0 < R ? d.heads - x.head0 : R;
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkParams p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 1.0f;
   if (d.weight) load_runs<float>(d.weight, u, w);
-  Elem* to = static_cast<Elem*>(d.out) + ((x.b * p.seqlen + x.t) * d.heads + x.head0) * p.dim;
+  Elem* to = static_cast<Elem*>(d.out) + ((int64_t(x.b) * p.seqlen + x.t) * d.heads + x.head0) * p.dim;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float sum = 0.0f;
@@ -177,23 +181,22 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkParams p) {
 }
 
 template <typename Elem, int LG, int R>
-__global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkParams p) {
-  constexpr int kPer = kThreads >> LG;  // items of a workgroup at a time
+__global__ __launch_bounds__(kThreads, R > 1 ? 4 : 1) void qk_bwd_kernel(QkParams p, uint32_t groups) {
+  constexpr uint32_t kPer = kThreads >> LG;  // items of a workgroup at a time
   const int lane = threadIdx.x & ((1 << LG) - 1), mine = threadIdx.x >> LG;
+  const int side = blockIdx.x >= p.q_groups ? 1 : 0;
+  const QkSide& d = p.side[side];
+  const uint32_t group = blockIdx.x - (side ? p.q_groups : 0), step = (side ? groups - p.q_groups : p.q_groups) * kPer;
   const Runs u = runs_of(lane, p);
-  float w[2][8], dw[2][8];
+  float w[8], dw[8];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[side][e] = 1.0f;
-      dw[side][e] = 0.0f;
-    }
-    if (p.side[side].weight) load_runs<float>(p.side[side].weight, u, w[side]);
+  for (int e = 0; e < 8; ++e) {
+    w[e] = 1.0f;
+    dw[e] = 0.0f;
   }
-  for (int64_t first = int64_t(blockIdx.x) * kPer; first < p.items; first += int64_t(gridDim.x) * kPer) {
-    Item x = item_of(first + mine, p, R);  // (past the last: the first item's values, not stored)
-    const QkSide& d = p.side[x.side];
+  if (d.weight) load_runs<float>(d.weight, u, w);
+  for (uint32_t first = group * kPer; first < d.items; first += step) {
+    Item x = item_of(first + mine, d, p.seqlen, R);  // (past the last: the first item's values, not stored)
     const Elem* from = static_cast<const Elem*>(d.x) + x.b * d.batch + x.t * d.step + x.head0 * d.head;
     const Elem* dy = static_cast<const Elem*>(d.dy) + x.b * d.dy_batch + x.t * d.dy_step + x.head0 * d.dy_head;
     const int rows = !x.live ? 0 : d.heads - x.head0 < R ? d.heads - x.head0 : R;
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkParams p) {
     load_angles(p, x, u, c, s);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = -s[e];
-    Elem* to = static_cast<Elem*>(d.out) + ((x.b * p.seqlen + x.t) * d.heads + x.head0) * p.dim;
+    Elem* to = static_cast<Elem*>(d.out) + ((int64_t(x.b) * p.seqlen + x.t) * d.heads + x.head0) * p.dim;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       turn(y[i], c, s, p.interleaved != 0);
@@ -220,11 +223,10 @@ __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[i][e] *= r;
-        const float add = y[i][e] * v[i][e], we = x.side ? w[1][e] : w[0][e];
-        dw[0][e] += counts && !x.side ? add : 0.0f;
-        dw[1][e] += counts && x.side ? add : 0.0f;
-        dot = __builtin_fmaf(add, we, dot);
-        y[i][e] *= we;
+        const float add = y[i][e] * v[i][e];
+        dw[e] += counts ? add : 0.0f;
+        dot = __builtin_fmaf(add, w[e], dot);
+        y[i][e] *= w[e];
       }
       const float mean = sum_lanes<LG>(dot) * p.inv_dim;
 #pragma unroll
@@ -235,51 +237,50 @@ __global__ __launch_bounds__(kThreads) void qk_bwd_kernel(QkParams p) {
       if (i < rows) store_runs<Elem>(to + i * p.dim, u, v[i]);
     }
   }
-  if (!p.partials) return;
-  // The weight gradients of the workgroup's items, in the order of its lane groups.
+  if (!d.partials) return;
+  // The weight gradient of the workgroup's items, in the order of its lane groups.
   __shared__ float part[kPer][8 << LG];
-  for (int side = 0; side < 2; ++side) {
-    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[mine][lane * 8 + e] = side ? dw[1][e] : dw[0][e];
-    __syncthreads();
-    if (threadIdx.x < (1 << LG)) {
-      float a[8];
+  for (int e = 0; e < 8; ++e) part[mine][lane * 8 + e] = dw[e];
+  __syncthreads();
+  if (threadIdx.x < (1 << LG)) {
+    float a[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = 0.0f;
-      for (int i = 0; i < kPer; ++i)
+    for (int e = 0; e < 8; ++e) a[e] = 0.0f;
+    for (uint32_t i = 0; i < kPer; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += part[i][lane * 8 + e];
-      float* to = p.partials + (int64_t(blockIdx.x) * 2 + side) * p.dim;
-      store_runs<float>(to, u, a);
-    }
+      for (int e = 0; e < 8; ++e) a[e] += part[i][lane * 8 + e];
+    store_runs<float>(d.partials + int64_t(group) * p.dim, u, a);
   }
 }
 
-// The workgroups' partial weight gradients summed, in a fixed order.
-__global__ __launch_bounds__(kReduceCols* kNormReduceSlices) void qk_weight_kernel(const float* part, int64_t rows,
-                                                                                   int dim, float* dq_weight,
-                                                                                   float* dk_weight) {
+// The workgroups' partial weight gradients of a side summed, in a fixed order; a side the grid's
+// second axis.
+struct WeightSum {
+  const float* part;
+  int64_t rows;
+  float* to;  // nullable
+};
+__global__ __launch_bounds__(kReduceCols* kNormReduceSlices) void qk_weight_kernel(WeightSum q, WeightSum k, int dim) {
   __shared__ float buf[kNormReduceSlices][kReduceCols + 1];
-  const int64_t col = int64_t(blockIdx.x) * kReduceCols + threadIdx.x % kReduceCols, cols = 2 * dim;
-  const float a = sum_rows<kReduceCols, kNormReduceSlices>(part, rows, cols, col, buf);
-  if (threadIdx.x / kReduceCols == 0 && col < cols) {
-    float* to = col < dim ? dq_weight : dk_weight;
-    if (to) to[col < dim ? col : col - dim] = a;
-  }
+  const WeightSum& w = blockIdx.y ? k : q;
+  if (!w.to) return;
+  const int64_t col = int64_t(blockIdx.x) * kReduceCols + threadIdx.x % kReduceCols;
+  const float a = sum_rows<kReduceCols, kNormReduceSlices>(w.part, w.rows, dim, col, buf);
+  if (threadIdx.x / kReduceCols == 0 && col < dim) w.to[col] = a;
 }
 
 template <typename Elem, int LG, int R>
-void run(const QkParams& p, bool bwd, int64_t groups, hipStream_t s) {
-  const dim3 grid{uint32_t(groups)}, block{kThreads};
+void run(const QkParams& p, bool bwd, uint32_t groups, hipStream_t s) {
+  const dim3 grid{groups}, block{kThreads};
   if (bwd)
-    hipLaunchKernelGGL((qk_bwd_kernel<Elem, LG, R>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((qk_bwd_kernel<Elem, LG, R>), grid, block, 0, s, p, groups);
   else
     hipLaunchKernelGGL((qk_fwd_kernel<Elem, LG, R>), grid, block, 0, s, p);
 }
 
 template <typename Elem, int R>
-void run_lanes(const QkParams& p, int lg, bool bwd, int64_t groups, hipStream_t s) {
+void run_lanes(const QkParams& p, int lg, bool bwd, uint32_t groups, hipStream_t s) {
   switch (lg) {
     case 2: return run<Elem, 2, R>(p, bwd, groups, s);
     case 3: return run<Elem, 3, R>(p, bwd, groups, s);
@@ -292,35 +293,43 @@ void run_lanes(const QkParams& p, int lg, bool bwd, int64_t groups, hipStream_t 
 int launch(const QkArgs& a, bool bwd, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int lg = qk_lanes_log2(a.dim, a.rot), rows = qk_rows(a.batch, a.seqlen, a.q_heads + a.k_heads, lg);
-  const QkItems items = qk_items(a.batch, a.seqlen, a.q_heads, a.k_heads, rows);
-  const int64_t all = qk_groups(items.items, lg), groups = bwd ? qk_partials(all) : all;
-  const bool sums = bwd && (a.dq_weight || a.dk_weight);
+  const int64_t q_items = qk_items(a.batch, a.seqlen, a.q_heads, rows),
+                k_items = qk_items(a.batch, a.seqlen, a.k_heads, rows);
+  int64_t q_groups = qk_groups(q_items, lg), k_groups = qk_groups(k_items, lg);
+  if (bwd) {
+    q_groups = qk_partials(q_groups);
+    k_groups = qk_partials(k_groups);
+  }
+  const int64_t groups = q_groups + k_groups;
+  float *q_part = a.workspace, *k_part = a.workspace ? a.workspace + q_groups * a.dim : nullptr;
   QkParams p{};
-  p.side[0] = QkSide{a.q.p, a.q.batch, a.q.step, a.q.head, a.dyq.p, a.dyq.batch, a.dyq.step, a.dyq.head,
-                     a.q_weight, a.q_out, int(a.q_heads)};
-  p.side[1] = QkSide{a.k.p, a.k.batch, a.k.step, a.k.head, a.dyk.p, a.dyk.batch, a.dyk.step, a.dyk.head,
-                     a.k_weight, a.k_out, int(a.k_heads)};
+  p.side[0] = QkSide{a.q.p, a.q.batch, a.q.step, a.q.head, a.dyq.p, a.dyq.batch, a.dyq.step, a.dyq.head, a.q_weight,
+                     a.q_out, a.dq_weight ? q_part : nullptr, uint32_t(q_items),
+                     uint32_t((a.q_heads + rows - 1) / rows), int(a.q_heads)};
+  p.side[1] = QkSide{a.k.p, a.k.batch, a.k.step, a.k.head, a.dyk.p, a.dyk.batch, a.dyk.step, a.dyk.head, a.k_weight,
+                     a.k_out, a.dk_weight ? k_part : nullptr, uint32_t(k_items),
+                     uint32_t((a.k_heads + rows - 1) / rows), int(a.k_heads)};
+  p.q_groups = uint32_t(q_groups);
   p.cos = a.cos, p.sin = a.sin, p.positions = a.positions;
   p.eps = a.eps, p.inv_dim = 1.0f / float(a.dim);
-  p.partials = sums ? a.workspace : nullptr;
-  p.items = items.items, p.seqlen = a.seqlen, p.table_rows = a.table_rows;
-  p.q_parts = int(items.q_parts), p.parts = int(items.q_parts + items.k_parts);
+  p.seqlen = uint32_t(a.seqlen), p.table_rows = a.table_rows;
   p.dim = int(a.dim), p.rot = int(a.rot), p.turning = int((a.rot / 2 + 3) / 4);
   p.interleaved = a.interleaved;
   if (groups > 0) {
+    const uint32_t n = uint32_t(groups);
     if (a.io == Io::BF16) {
-      if (rows > 1) run_lanes<uint16_t, kQkMostRows>(p, lg, bwd, groups, s);
-      else run_lanes<uint16_t, 1>(p, lg, bwd, groups, s);
+      if (rows > 1) run_lanes<uint16_t, kQkMostRows>(p, lg, bwd, n, s);
+      else run_lanes<uint16_t, 1>(p, lg, bwd, n, s);
     } else {
-      if (rows > 1) run_lanes<float, kQkMostRows>(p, lg, bwd, groups, s);
-      else run_lanes<float, 1>(p, lg, bwd, groups, s);
+      if (rows > 1) run_lanes<float, kQkMostRows>(p, lg, bwd, n, s);
+      else run_lanes<float, 1>(p, lg, bwd, n, s);
     }
     if (hipGetLastError() != hipSuccess) return -1;
   }
-  if (sums) {
-    hipLaunchKernelGGL(qk_weight_kernel, dim3(uint32_t(reduce_groups(2 * a.dim))),
-                       dim3(kReduceCols * kNormReduceSlices), 0, s, a.workspace, groups, int(a.dim), a.dq_weight,
-                       a.dk_weight);
+  if (bwd && (a.dq_weight || a.dk_weight)) {
+    hipLaunchKernelGGL(qk_weight_kernel, dim3(uint32_t(reduce_groups(a.dim)), 2),
+                       dim3(kReduceCols * kNormReduceSlices), 0, s, WeightSum{q_part, q_groups, a.dq_weight},
+                       WeightSum{k_part, k_groups, a.dk_weight}, int(a.dim));
     if (hipGetLastError() != hipSuccess) return -1;
   }
   return 0;

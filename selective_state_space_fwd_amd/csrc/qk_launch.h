@@ -35,31 +35,27 @@ inline int qk_lanes_log2(int64_t dim, int64_t rot) {
 }
 
 // Heads of one step that a row's lanes take one after another, all loads first: they share the
-// angles. Few where the call is small, for more waves.
+// angles. One where the call is small, for more waves.
 constexpr int kQkMostRows = 4;
 inline int qk_rows(int64_t batch, int64_t seqlen, int64_t heads, int lg) {
   return ((batch * seqlen * heads) >> (6 - lg)) / kQkMostRows >= 4096 ? kQkMostRows : 1;
 }
 
-// What one group of lanes takes: `rows` heads of q or of k at one step.
-struct QkItems {
-  int64_t q_parts, k_parts;  // of a step
-  int64_t items;
-};
-inline QkItems qk_items(int64_t batch, int64_t seqlen, int64_t q_heads, int64_t k_heads, int rows) {
-  QkItems i;
-  i.q_parts = (q_heads + rows - 1) / rows;
-  i.k_parts = (k_heads + rows - 1) / rows;
-  i.items = batch * seqlen * (i.q_parts + i.k_parts);
-  return i;
+// What one group of lanes takes: `rows` heads of one side (q or k) at one step; and the workgroups
+// of a side.
+inline int64_t qk_items(int64_t batch, int64_t seqlen, int64_t heads, int rows) {
+  return batch * seqlen * ((heads + rows - 1) / rows);
 }
 inline int64_t qk_groups(int64_t items, int lg) {
   const int64_t per = int64_t(kQkWaves) << (6 - lg);
   return (items + per - 1) / per;
 }
+// Items are numbered in 32 bits.
+constexpr int64_t kQkMostItems = (int64_t(1) << 31) - 1;
 
-// Workgroups of the backward, each with one row of partial weight gradients.
-inline int64_t qk_partials(int64_t groups) { return groups < 1024 ? groups : 1024; }
+// Workgroups of a side in the backward, each with one row of partial weight gradients.
+constexpr int64_t kQkMostPartials = 2048;
+inline int64_t qk_partials(int64_t groups) { return groups < kQkMostPartials ? groups : kQkMostPartials; }
 
 int launch_qk_fwd(const QkArgs& a, void* stream);
 int launch_qk_bwd(const QkArgs& a, void* stream);

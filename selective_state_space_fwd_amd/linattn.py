@@ -33,7 +33,7 @@ from .block import (_check, _check_out, _device, _io_flag, _param, _run, _Stride
 SSM_LINATTN_HEAD_DG = 1 << 13
 SSM_QK_INTERLEAVED = 1 << 14
 
-_bound = None
+_bound = _ready = None
 
 
 def _lib() -> ctypes.CDLL:
@@ -59,6 +59,22 @@ def _lib() -> ctypes.CDLL:
         getattr(L, name).restype = ctypes.c_int
     _bound = L
     return L
+
+
+def _native():
+    """The extension module (csrc/binding.cpp), given the addresses of the entry points below. Its
+    functions make a call whose arguments are what the C ABI takes as they stand, and return None
+    without having done anything for any other, which the checks here then take."""
+    global _ready
+    module = block._binding or block._load()
+    if module is not _ready:
+        L = _lib()
+        module.bind_linattn(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "ssm_linattn_fwd", "ssm_linattn_fwd_workspace_bytes", "ssm_linattn_bwd",
+            "ssm_linattn_bwd_workspace_bytes", "ssm_linattn_step", "ssm_qk_norm_fwd",
+            "ssm_qk_norm_bwd", "ssm_qk_norm_bwd_workspace_bytes")))
+        _ready = module
+    return module
 
 
 # ------------------------------------------------------------------ raw C entry points
@@ -178,6 +194,10 @@ def linattn(q, k, v, g=None, scale: Optional[float] = None, initial_state=None, 
     state stays and nothing is read). Returns (out [batch, seqlen, heads, dv] contiguous in v's
     dtype, final_state as initial_state). workspace: a uint8 device tensor of at least
     ssm_linattn_fwd_workspace_bytes(...) bytes, allocated here when None."""
+    r = _native().linattn(q, k, v, g, scale, initial_state, lengths, out, final_state,
+                          return_final_state, workspace)
+    if r is not None:
+        return r
     z, f32 = _Sizes(q, v), _torch().float32
     q, qp, qs = _heads("q", q, z.qk, z.io, z.dev)
     k, kp, ks = _heads("k", k, z.qk, z.io, z.dev)
@@ -212,6 +232,10 @@ def linattn_backward(q, k, v, dout, g=None, scale: Optional[float] = None, initi
     default where an initial_state is given), None where not asked for. Bitwise reproducible.
     workspace: a uint8 device tensor of at least ssm_linattn_bwd_workspace_bytes(...) bytes,
     allocated here when None."""
+    r = _native().linattn_backward(q, k, v, dout, g, scale, initial_state, lengths, dfinal, want_dg,
+                                   want_dinitial, workspace)
+    if r is not None:
+        return dict(zip(("dq", "dk", "dv", "dg", "dinitial"), r))
     z, f32 = _Sizes(q, v), _torch().float32
     q, qp, qs = _heads("q", q, z.qk, z.io, z.dev)
     k, kp, ks = _heads("k", k, z.qk, z.io, z.dev)
@@ -249,6 +273,9 @@ def linattn_step(q, k, v, state, g=None, scale: Optional[float] = None, slots=No
     int32, the slot of each row (None: row i is slot i). A row whose slot lies outside [0,
     nslots) gives 0 and changes nothing; rows naming one slot are successive tokens of it.
     Returns out [batch, heads, dv]."""
+    r = _native().linattn_step(q, k, v, state, g, scale, slots, out)
+    if r is not None:
+        return r
     torch = _torch()
     dev = _device("q", q)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
@@ -318,6 +345,10 @@ def qk_norm(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=No
     float32, the angles' (None: no rotation); positions: [batch, seqlen] int32 (None: step t is
     at position t); a step whose position lies outside the table gives zeros. Pairs are (i, i +
     pairs), or, interleaved, (2 i, 2 i + 1). Returns (q_out, k_out), contiguous, in q's dtype."""
+    r = _native().qk_norm(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
+                          k_out)
+    if r is not None:
+        return r
     dev, flags, (q, k), pointers, shared, sizes = _qk_inputs(q, k, q_weight, k_weight, cos, sin,
                                                              positions, interleaved)
     if q_out is None:
@@ -341,6 +372,10 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     dq and dk (contiguous, in q's dtype), dq_weight and dk_weight (float32; None without the
     weight). Bitwise reproducible. workspace: a uint8 device tensor of at least
     ssm_qk_norm_bwd_workspace_bytes(...) bytes, allocated here when None."""
+    r = _native().qk_norm_backward(q, k, dq_out, dk_out, q_weight, k_weight, cos, sin, positions, eps,
+                                   interleaved, workspace)
+    if r is not None:
+        return dict(zip(("dq", "dk", "dq_weight", "dk_weight"), r))
     f32 = _torch().float32
     dev, flags, (q, k), pointers, shared, sizes = _qk_inputs(q, k, q_weight, k_weight, cos, sin,
                                                              positions, interleaved)
