@@ -35,8 +35,8 @@
  * no atomics (bitwise reproducible) and allocate nothing; every check happens before any HIP call.
  * Calls that share a workspace must not overlap in time. Return SSM_OK, SSM_ERR_INVALID_ARG (also a
  * workspace too small, heads no multiple of qk_heads), SSM_ERR_UNSUPPORTED (dk or dv outside [1, 256],
- * batch above 65535, sizes past int64 or a grid of 2^32 - 1 work-items, a storage type other than
- * fp32/bf16), SSM_ERR_MISALIGNED (a pointer not aligned to its element size, a workspace not to 256
+ * batch above 65535, steps of an array 16 MiB apart or more, sizes past int64 or a grid of 2^32 - 1
+ * work-items, a storage type other than fp32/bf16), SSM_ERR_MISALIGNED (a pointer not aligned to its element size, a workspace not to 256
  * bytes) or SSM_ERR_HIP.
  */
 #ifndef SSM_LINATTN_H

@@ -119,7 +119,7 @@ __device__ __forceinline__ void widen_frag(const Frag<float>& f, float (&v)[8]) 
   for (int i = 0; i < 8; ++i) v[i] = f.v[i];
 }
 
-// Elements between rows of a staged tile of D columns: 16 bytes more than the row, so that the 16
+// Elements between rows of a staged tile of D columns: a little more than the row, so that the 16
 // rows of an operand read start in different banks.
 template <typename Elem>
 __host__ __device__ constexpr int la_pitch(int D) {
@@ -140,38 +140,40 @@ __device__ __forceinline__ Frag<float> row_frag(const float* tile, int pitch, in
   return Frag<float>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
-// The same 32 values in the order in which two stacked result tiles hold them: k0 + 4g .. + 3, then
-// k0 + 16 + 4g .. + 3 (so that a state kept as results is an operand as it stands).
-__device__ __forceinline__ Frag<uint16_t> row_frag_stacked(const uint16_t* tile, int pitch, int row, int k0) {
-  const int g = (threadIdx.x & 63) >> 4;
-  const uint2 a = *reinterpret_cast<const uint2*>(tile + row * pitch + k0 + 4 * g);
-  const uint2 b = *reinterpret_cast<const uint2*>(tile + row * pitch + k0 + 16 + 4 * g);
-  return Frag<uint16_t>{make_uint4(a.x, a.y, b.x, b.y)};
-}
-__device__ __forceinline__ Frag<float> row_frag_stacked(const float* tile, int pitch, int row, int k0) {
-  const int g = (threadIdx.x & 63) >> 4;
-  const float4 a = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 4 * g);
-  const float4 b = *reinterpret_cast<const float4*>(tile + row * pitch + k0 + 16 + 4 * g);
-  return Frag<float>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-
 // Column c0 + r, contraction over rows: values of rows s0 + 8g .. + 7. bf16 through the transposing
 // LDS read: of each 16 lanes, lane i supplies the address of four columns (4 (i % 4) on) of
 // row i / 4 and receives column i of the four rows.
-__device__ __forceinline__ Frag<uint16_t> col_frag(const uint16_t* tile, int pitch, int s0, int c0) {
-  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-  const uint16_t* p = tile + (s0 + 8 * g + (r >> 2)) * pitch + c0 + 4 * (r & 3);
+__device__ __forceinline__ Frag<uint16_t> transposed(const uint16_t* p, int pitch) {
   const la_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s16x4*)p);
   const la_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_s16x4*)(p + 4 * pitch));
   const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
   return Frag<uint16_t>{make_uint4(x.x, x.y, y.x, y.y)};
 }
-__device__ __forceinline__ Frag<float> col_frag(const float* tile, int pitch, int s0, int c0) {
-  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+__device__ __forceinline__ Frag<float> transposed(const float* p, int pitch) {
   Frag<float> f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f.v[i] = tile[(s0 + 8 * g + i) * pitch + c0 + r];
+  for (int i = 0; i < 8; ++i) f.v[i] = p[i * pitch];
   return f;
+}
+__device__ __forceinline__ Frag<uint16_t> col_frag(const uint16_t* tile, int pitch, int s0, int c0) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  return transposed(tile + (s0 + 8 * g + (r >> 2)) * pitch + c0 + 4 * (r & 3), pitch);
+}
+__device__ __forceinline__ Frag<float> col_frag(const float* tile, int pitch, int s0, int c0) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  return transposed(tile + (s0 + 8 * g) * pitch + c0 + r, pitch);
+}
+
+// Half `odd` of 32 columns from c0 on, such that the results' rows 4g .. 4g + 3 of the two halves are
+// columns c0 + 8g .. + 3 and c0 + 8g + 4 .. + 7: a state kept as results then is, pair by pair, the
+// operand of its eight contraction values as it stands.
+__device__ __forceinline__ Frag<uint16_t> col_frag_paired(const uint16_t* tile, int pitch, int s0, int c0, int odd) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  return transposed(tile + (s0 + 8 * g + (r >> 2)) * pitch + c0 + 8 * (r & 3) + 4 * odd, pitch);
+}
+__device__ __forceinline__ Frag<float> col_frag_paired(const float* tile, int pitch, int s0, int c0, int odd) {
+  const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
+  return transposed(tile + (s0 + 8 * g) * pitch + c0 + 8 * (r >> 2) + (r & 3) + 4 * odd, pitch);
 }
 
 // Four values of a result (rows 4g .. 4g + 3 of a column) as a run of four storage elements in LDS.
@@ -187,26 +189,45 @@ __device__ __forceinline__ la_f32x4 get4(const uint16_t* p) {
 }
 __device__ __forceinline__ la_f32x4 get4(const float* p) { return *reinterpret_cast<const la_f32x4*>(p); }
 
+// A byte offset past every buffer: loads there read 0, stores are dropped. Loads and stores go
+// through buffer resources with it in the place of a branch, so that nothing but their use waits.
+constexpr uint32_t kLaOob = 0x80000000u;
+constexpr uint32_t kLaBytes = 0x7fffffffu;  // offsets in use are below it (linattn_reach)
+
 // A tile of C steps x D columns on its way from memory to LDS, spread over the workgroup's threads.
-template <typename Elem, int C, int D>
+// kWhole: rows of whole 16-byte words at 4-byte aligned addresses, a load a word; else a load an
+// element.
+template <typename Elem, int C, int D, bool kWhole>
 struct TileLoad {
   static constexpr int kN = Vec<Elem>::kN, kRow = D / kN, kWords = C * kRow / kLaThreads;
-  static_assert(C * kRow % kLaThreads == 0, "whole words for every thread");
+  static constexpr int kStep = kLaThreads / kRow;  // rows from one of a thread's words to the next
+  static_assert(C * kRow % kLaThreads == 0 && kLaThreads % kRow == 0, "whole words, whole rows");
   uint4 w[kWords];
 
-  // Rows [0, rows) of `dim` elements, `step` apart; zeros elsewhere (nothing there is read).
-  __device__ __forceinline__ void load(const Elem* base, int64_t step, int rows, int dim) {
+  // Rows [0, rows) of `dim` elements, `step` bytes apart; zeros elsewhere (nothing there is read).
+  __device__ __forceinline__ void load(const Elem* base, uint32_t step, int rows, int dim) {
+    constexpr uint32_t E = sizeof(Elem);
+    const Buf b(base, kLaBytes);
+    const int row = int(threadIdx.x) / kRow, col = (int(threadIdx.x) % kRow) * kN;
+    const uint32_t off = uint32_t(row) * step + uint32_t(col) * E;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int at = int(threadIdx.x) + i * kLaThreads, row = at / kRow, col = (at % kRow) * kN;
-      const int n = row < rows ? dim - col : 0;
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (n >= kN) {
-        w[i] = load16_any(base + row * step + col);
-      } else if (n > 0) {
-        float v[kN];
-        load_part_of<Elem, kN>(base + row * step + col, n, v);
-        w[i] = narrow_raw16<Elem>(v);
+      const bool on = row < rows - i * kStep;
+      const uint32_t s = uint32_t(i * kStep) * step;
+      if constexpr (kWhole) {
+        w[i] = b.load16(on && col < dim ? off : kLaOob, s);
+      } else if constexpr (E == 4) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = b.load4(on && col + e < dim ? off + s + 4 * e : kLaOob);
+        w[i] = make_uint4(x[0], x[1], x[2], x[3]);
+      } else {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = b.load2(on && col + 2 * e < dim ? off + s + 4 * e : kLaOob) |
+                 b.load2(on && col + 2 * e + 1 < dim ? off + s + 4 * e + 2 : kLaOob) << 16;
+        w[i] = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
   }
@@ -218,6 +239,29 @@ struct TileLoad {
     }
   }
 };
+
+// Four neighbouring elements at byte offset off, of which the first n are stored (none where !on).
+template <typename Elem, bool kWhole>
+__device__ __forceinline__ void store4_at(const Buf& b, uint32_t off, int n, bool on, const la_f32x4& v) {
+  if constexpr (sizeof(Elem) == 4) {
+    if constexpr (kWhole) {
+      b.store16(make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+                on && n > 0 ? off : kLaOob);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b.store4(__float_as_uint(v[e]), on && e < n ? off + 4 * e : kLaOob);
+    }
+  } else {
+    const uint2 w = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if constexpr (kWhole) {
+      b.store8(w, on && n > 0 ? off : kLaOob);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        b.store2(uint16_t((e < 2 ? w.x : w.y) >> (16 * (e & 1))), on && e < n ? off + 2 * e : kLaOob);
+    }
+  }
+}
 
 // ---------------------------------------------------------------- decays
 
@@ -258,10 +302,13 @@ __device__ __forceinline__ double log2_decay(float g) {
 // decay between two steps is a difference of sums that may be far larger than it.
 template <int C>
 struct Decays {
-  float hi[C], lo[C];  // sum over the steps up to and with t
-  float into[C];       // exp of it: from the chunk's start to t
-  float onto[C];       // from s to the chunk's end
-  float total;         // over the chunk
+  struct Sum {
+    float hi, lo;
+  };
+  Sum sum[C];     // over the steps up to and with t
+  float into[C];  // exp of it: from the chunk's start to t
+  float onto[C];  // from s to the chunk's end
+  float total;    // over the chunk
 
   // Lane t < C of one wave holds the step's log2 decay (0 behind the end). Returns the sum.
   __device__ __forceinline__ double set(double step) {
@@ -269,16 +316,15 @@ struct Decays {
     const double cs = wave_prefix_f64(step), all = dpp_f64(cs, C - 1);
     if (l < C) {
       const float h = float(cs);
-      hi[l] = h;
-      lo[l] = float(cs - double(h));
+      sum[l] = Sum{h, float(cs - double(h))};
       into[l] = exp2_hw(h);
       onto[l] = exp2_hw(float(all - cs));
       if (l == 0) total = exp2_hw(float(all));
     }
     return all;
   }
-  __device__ __forceinline__ float between(int t, int s) const {
-    return exp2_hw((hi[t] - hi[s]) + (lo[t] - lo[s]));
+  static __device__ __forceinline__ float between(const Sum& t, const Sum& s) {
+    return exp2_hw((t.hi - s.hi) + (t.lo - s.lo));
   }
 };
 
@@ -294,10 +340,26 @@ __device__ __forceinline__ int64_t row_end(const int32_t* lengths, int64_t b, in
   return n < 0 ? 0 : n > seqlen ? seqlen : n;
 }
 
-// The causal 16 x 16 tiles of a chunk's pairs of steps, row by row: tile `at` is (i, j), j <= i.
-__device__ __forceinline__ void causal_tile(int at, int& i, int& j) {
-  i = at >= 6 ? 3 : at >= 3 ? 2 : at >= 1 ? 1 : 0;
-  j = at - i * (i + 1) / 2;
+// The causal 16 x 16 tiles (i, j), j <= i, of a chunk's pairs of steps that a wave takes: a run of
+// row i, so that the row's operand is read once, and one more tile (0, 0). Of 64 steps the waves
+// take 3, 3, 3 and 1 tile (the last has the decays to do), of 32 one each but the last.
+struct WaveTiles {
+  int i, j0, j1;  // [j0, j1)
+  bool more;
+};
+template <int C>
+__device__ __forceinline__ WaveTiles wave_tiles(int w) {
+  if constexpr (C == 64) {
+    if (w == 0) return {3, 0, 3, false};
+    if (w == 1) return {2, 0, 3, false};
+    if (w == 2) return {1, 0, 2, true};
+    return {3, 3, 4, false};
+  } else {
+    static_assert(C == 32, "two rows of tiles");
+    if (w == 0) return {1, 0, 1, false};
+    if (w == 1) return {1, 1, 2, false};
+    return {0, 0, 0, w == 2};
+  }
 }
 
 }  // namespace ssm

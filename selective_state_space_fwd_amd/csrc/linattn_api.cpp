@@ -73,6 +73,13 @@ bool grids_fit(const Sizes& z, bool bwd) {
   return a >= 0 && b >= 0 && ssm::grid_fits(a, 256) && ssm::grid_fits(b, 256);
 }
 
+// The steps of every array, the results' among them.
+bool steps_fit(const Sizes& z, const ssm::LinattnArgs& a) {
+  for (int64_t step : {a.q.step, a.k.step, a.v.step, a.dout.step, z.heads * z.dv, z.qk_heads * z.dk})
+    if (!ssm::linattn_reach(step, z.esz)) return false;
+  return true;
+}
+
 int64_t fwd_workspace(const Sizes& z) {
   const ssm::LinattnSegments s = ssm::linattn_segments(z.batch, z.heads, z.dk, z.dv, z.seqlen, io_of(z.esz));
   if (s.count <= 1) return 0;
@@ -120,7 +127,7 @@ int ssm_linattn_fwd(const void* q, const int64_t* q_strides, const void* k, cons
       (st = check_heads(v, v_strides, batch, seqlen, heads, dv, z.esz, &a.v, &vb)) ||
       (st = check_gates(g, g_strides, z, &a, &gb)))
     return st;
-  if (!grids_fit(z, false)) return SSM_ERR_UNSUPPORTED;
+  if (!grids_fit(z, false) || !steps_fit(z, a)) return SSM_ERR_UNSUPPORTED;
   const int64_t need = fwd_workspace(z);
   if (need < 0) return SSM_ERR_UNSUPPORTED;
   if (z.v_bytes > 0 && (!q || !k || !v || !out)) return SSM_ERR_INVALID_ARG;
@@ -169,7 +176,7 @@ int ssm_linattn_bwd(const void* q, const int64_t* q_strides, const void* k, cons
       (st = check_heads(dout, dout_strides, batch, seqlen, heads, dv, z.esz, &a.dout, &ob)) ||
       (st = check_gates(g, g_strides, z, &a, &gb)))
     return st;
-  if (!grids_fit(z, true)) return SSM_ERR_UNSUPPORTED;
+  if (!grids_fit(z, true) || !steps_fit(z, a)) return SSM_ERR_UNSUPPORTED;
   const int64_t need = bwd_workspace(z);
   if (need < 0) return SSM_ERR_UNSUPPORTED;
   if (z.v_bytes > 0 && (!q || !k || !v || !dout || !dq_out || !dk_out || !dv_out)) return SSM_ERR_INVALID_ARG;

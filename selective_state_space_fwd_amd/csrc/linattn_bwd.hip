@@ -48,9 +48,10 @@ struct BwdParams {
   float scale;
 };
 
-template <typename Elem, int KP, int VP>
+template <typename Elem, int KP, int VP, bool kWhole>
 __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void linattn_bwd_kernel(BwdParams p) {
-  constexpr int C = chunk_of<Elem>(), T = C / 16, SB = C / 32, kPairs = T * (T + 1) / 2;
+  constexpr int C = chunk_of<Elem>(), T = C / 16, SB = C / 32;
+  constexpr uint32_t E = sizeof(Elem);
   constexpr int NK = KP / 64, NV = VP / 64;  // 16-wide tiles of dk and dv a wave owns
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
@@ -60,10 +61,10 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-  int64_t at = xcd_order(blockIdx.x, gridDim.x);
-  const int hk = int(at % p.qk_heads);
-  at /= p.qk_heads;
-  const int64_t c = at % p.chunks, b = at / p.chunks, t0 = c * C;
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int hk = int(at % uint32_t(p.qk_heads));
+  at /= uint32_t(p.qk_heads);
+  const int64_t c = at % uint32_t(p.chunks), b = at / uint32_t(p.chunks), t0 = c * C;
   const int64_t end = row_end(p.lengths, b, p.seqlen);
   const int rows = p.seqlen - t0 < C ? int(p.seqlen - t0) : C;
   const int live = end <= t0 ? 0 : end - t0 < C ? int(end - t0) : C;
@@ -78,21 +79,21 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
     for (int i = 0; i < T; ++i) aq[n][i] = ak[n][i] = la_f32x4{0, 0, 0, 0};
 
   // rows a..a+3 of dim columns, steps 16 i + r; zero behind the end.
-  auto put = [&](Elem* base, int64_t step, int i, int col, int dim, const la_f32x4& v) {
+  auto put = [&](Elem* base, int64_t step, int i, int col, int dim, la_f32x4 v) {
     const int t = 16 * i + r;
-    if (t < rows && col < dim) {
-      float y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = t < live ? v[e] : 0.0f;
-      store_few<Elem, 4>(base + t * step + col, dim - col, y);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = t < live ? v[e] : 0.0f;
+    store4_at<Elem, kWhole>(Buf(base, kLaBytes), uint32_t(t) * uint32_t(step) * E + uint32_t(col) * E, dim - col,
+                            t < rows, v);
   };
 
   if (live > 0) {
     {
-      TileLoad<Elem, C, KP> lq, lk;
-      lq.load(static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head + t0 * p.q.step, p.q.step, live, p.dk);
-      lk.load(static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head + t0 * p.k.step, p.k.step, live, p.dk);
+      TileLoad<Elem, C, KP, kWhole> lq, lk;
+      lq.load(static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head + t0 * p.q.step,
+              uint32_t(p.q.step) * E, live, p.dk);
+      lk.load(static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head + t0 * p.k.step,
+              uint32_t(p.k.step) * E, live, p.dk);
       lq.store(sQ);
       lk.store(sK);
     }
@@ -121,11 +122,12 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
     const float* S = p.states + ((b * p.heads + h) * p.chunks + c) * p.state_floats;
     const float* R = p.adjoints + ((b * p.heads + h) * p.chunks + c) * p.state_floats;
     {
-      TileLoad<Elem, C, VP> lv, lo;
+      TileLoad<Elem, C, VP, kWhole> lv, lo;
       double gate = 0.0;
-      lv.load(static_cast<const Elem*>(p.v.p) + b * p.v.batch + h * p.v.head + t0 * p.v.step, p.v.step, live, p.dv);
-      lo.load(static_cast<const Elem*>(p.dout.p) + b * p.dout.batch + h * p.dout.head + t0 * p.dout.step, p.dout.step,
-              live, p.dv);
+      lv.load(static_cast<const Elem*>(p.v.p) + b * p.v.batch + h * p.v.head + t0 * p.v.step,
+              uint32_t(p.v.step) * E, live, p.dv);
+      lo.load(static_cast<const Elem*>(p.dout.p) + b * p.dout.batch + h * p.dout.head + t0 * p.dout.step,
+              uint32_t(p.dout.step) * E, live, p.dv);
       if (w == 0) gate = load_decay(p.g ? p.g + b * p.g_batch + h * p.g_head : nullptr, p.g_step, t0, live);
       lds_barrier();  // every wave has read the head before
       lv.store(sV);
@@ -135,40 +137,49 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
     lds_barrier();
 
     // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
+    const WaveTiles mine = wave_tiles<C>(w);
+    auto pairs = [&](int i, int j, const Frag<Elem>(&qf)[KP / 32], const Frag<Elem>(&of)[VP / 32]) {
+      la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
 #pragma unroll
-    for (int x = 0; x < (kPairs + 3) / 4; ++x) {
-      const int pair = w + 4 * x;
-      if (pair < kPairs) {
-        int i, j;
-        causal_tile(pair, i, j);
-        la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
+      for (int kb = 0; kb < KP / 32; ++kb) a = mma(qf[kb], row_frag(sK, QP, 16 * j + r, 32 * kb), a);
 #pragma unroll
-        for (int kb = 0; kb < KP / 32; ++kb)
-          a = mma(row_frag(sQ, QP, 16 * i + r, 32 * kb), row_frag(sK, QP, 16 * j + r, 32 * kb), a);
+      for (int vb = 0; vb < VP / 32; ++vb) d = mma(of[vb], row_frag(sV, OP, 16 * j + r, 32 * vb), d);
+      const int s = 16 * j + r;
+      const typename Decays<C>::Sum from = dec.sum[s];
+      float wrow[4], wcol = 0.0f;
 #pragma unroll
-        for (int vb = 0; vb < VP / 32; ++vb)
-          d = mma(row_frag(sO, OP, 16 * i + r, 32 * vb), row_frag(sV, OP, 16 * j + r, 32 * vb), d);
-        const int s = 16 * j + r;
-        float wrow[4], wcol = 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * i + 4 * g + e;
+        const float m = s <= t ? p.scale * Decays<C>::between(dec.sum[t], from) : 0.0f;
+        d[e] = s <= t ? d[e] * m : 0.0f;
+        wrow[e] = s < t ? a[e] * d[e] : 0.0f;
+        a[e] = s <= t ? a[e] * m : 0.0f;
+        wcol += wrow[e];
+      }
+      put4(&sP[s * PP + 16 * i + 4 * g], a);
+      put4(&sD[s * PP + 16 * i + 4 * g], d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 16 * i + 4 * g + e;
-          const float m = s <= t ? p.scale * dec.between(t, s) : 0.0f;
-          d[e] = s <= t ? d[e] * m : 0.0f;
-          wrow[e] = s < t ? a[e] * d[e] : 0.0f;
-          a[e] = s <= t ? a[e] * m : 0.0f;
-          wcol += wrow[e];
-        }
-        put4(&sP[s * PP + 16 * i + 4 * g], a);
-        put4(&sD[s * PP + 16 * i + 4 * g], d);
+      for (int e = 0; e < 4; ++e) {
+        const float sum = sum_lanes<4>(wrow[e]);
+        if (r == 0) sRow[j][16 * i + 4 * g + e] = sum;
+      }
+      wcol += __shfl_xor(wcol, 16, 64);
+      wcol += __shfl_xor(wcol, 32, 64);
+      if (g == 0) sCol[i][s] = wcol;
+    };
+    {
+      Frag<Elem> qf[KP / 32], of[VP / 32];
+      auto rows_at = [&](int i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float sum = sum_lanes<4>(wrow[e]);
-          if (r == 0) sRow[j][16 * i + 4 * g + e] = sum;
-        }
-        wcol += __shfl_xor(wcol, 16, 64);
-        wcol += __shfl_xor(wcol, 32, 64);
-        if (g == 0) sCol[i][s] = wcol;
+        for (int kb = 0; kb < KP / 32; ++kb) qf[kb] = row_frag(sQ, QP, 16 * i + r, 32 * kb);
+#pragma unroll
+        for (int vb = 0; vb < VP / 32; ++vb) of[vb] = row_frag(sO, OP, 16 * i + r, 32 * vb);
+      };
+      rows_at(mine.i);
+      for (int j = mine.j0; j < mine.j1; ++j) pairs(mine.i, j, qf, of);
+      if (mine.more) {
+        rows_at(0);
+        pairs(0, 0, qf, of);
       }
     }
     lds_barrier();
@@ -335,14 +346,20 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(const float* sums, int6
   if (threadIdx.x == 0) dg[h] = float(part[0]);
 }
 
-template <typename Elem>
-void run_bwd(const BwdParams& p, int64_t groups, hipStream_t s) {
+template <typename Elem, int KP, int VP>
+void run_bwd_kernel(const BwdParams& p, int64_t groups, bool whole, hipStream_t s) {
   const dim3 grid{uint32_t(groups)}, block{kLaThreads};
-  if (p.dk > 128 || p.dv > 128) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, 256, 256>), grid, block, 0, s, p);
-  else if (p.dk > 64 && p.dv > 64) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, 128, 128>), grid, block, 0, s, p);
-  else if (p.dk > 64) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, 128, 64>), grid, block, 0, s, p);
-  else if (p.dv > 64) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, 64, 128>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((linattn_bwd_kernel<Elem, 64, 64>), grid, block, 0, s, p);
+  if (whole) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, KP, VP, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((linattn_bwd_kernel<Elem, KP, VP, false>), grid, block, 0, s, p);
+}
+
+template <typename Elem>
+void run_bwd(const BwdParams& p, int64_t groups, bool whole, hipStream_t s) {
+  if (p.dk > 128 || p.dv > 128) return run_bwd_kernel<Elem, 256, 256>(p, groups, whole, s);
+  if (p.dk > 64 && p.dv > 64) return run_bwd_kernel<Elem, 128, 128>(p, groups, whole, s);
+  if (p.dk > 64) return run_bwd_kernel<Elem, 128, 64>(p, groups, whole, s);
+  if (p.dv > 64) return run_bwd_kernel<Elem, 64, 128>(p, groups, whole, s);
+  run_bwd_kernel<Elem, 64, 64>(p, groups, whole, s);
 }
 
 }  // namespace
@@ -369,9 +386,10 @@ int launch_linattn_bwd(const LinattnArgs& a, void* stream) {
   p.kpad = int(linattn_pad(a.dk, 32)), p.vpad = int(linattn_pad(a.dv, 32));
   p.scale = a.scale;
   const int64_t groups = a.batch * a.qk_heads * chunks;
+  const bool whole = linattn_whole(a, true);
   if (groups > 0) {
-    if (a.io == Io::BF16) run_bwd<uint16_t>(p, groups, s);
-    else run_bwd<float>(p, groups, s);
+    if (a.io == Io::BF16) run_bwd<uint16_t>(p, groups, whole, s);
+    else run_bwd<float>(p, groups, whole, s);
     if (hipGetLastError() != hipSuccess) return -1;
   }
   if (p.dg_sums) {

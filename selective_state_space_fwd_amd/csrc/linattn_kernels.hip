@@ -44,22 +44,21 @@ struct FwdParams {
   float scale;
 };
 
-template <typename Elem, int KP, int NV>
+template <typename Elem, int KP, int NV, bool kWhole>
 __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_kernel(FwdParams p) {
   constexpr int C = chunk_of<Elem>(), T = C / 16, SB = C / 32, VT = 64 * NV, KB = KP / 32;
-  constexpr int kPairs = T * (T + 1) / 2, QP = la_pitch<Elem>(KP), VP = la_pitch<Elem>(VT),
-                PP = la_pitch<Elem>(C);
+  constexpr int QP = la_pitch<Elem>(KP), VP = la_pitch<Elem>(VT), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * VP], sP[C * PP];
-  __shared__ Decays<C> dec;
+  __shared__ __attribute__((aligned(16))) Decays<C> decays[2];  // of even and odd chunks
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-  int64_t at = xcd_order(blockIdx.x, gridDim.x);
-  const int vt = int(at % p.value_tiles);
-  at /= p.value_tiles;
-  const int h = int(at % p.heads);
-  at /= p.heads;
-  const int64_t seg = at % p.segments, b = at / p.segments;
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int vt = int(at % uint32_t(p.value_tiles));
+  at /= uint32_t(p.value_tiles);
+  const int h = int(at % uint32_t(p.heads));
+  at /= uint32_t(p.heads);
+  const int64_t seg = at % uint32_t(p.segments), b = at / uint32_t(p.segments);
   const int hk = h / p.group, v0 = vt * VT;
   const Elem* q = static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head;
   const Elem* k = static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head;
@@ -70,7 +69,8 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
   const int64_t end = row_end(p.lengths, b, p.seqlen);
   const int64_t c0 = seg * p.per, c1 = c0 + p.per < p.chunks ? c0 + p.per : p.chunks;
 
-  // The state: tile (j, n) is rows k = 16 j + 4 g + i of column v = vcol + 16 n + r.
+  // The state: tiles (2 j, n) and (2 j + 1, n) are rows k = 32 j + 8 g + i and + 4 + i of column v =
+  // vcol + 16 n + r, so that a lane has eight neighbouring k of one v.
   const int vcol = v0 + 16 * NV * w;
   la_f32x4 S[KP / 16][NV];
 #pragma unroll
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
 #pragma unroll
     for (int j = 0; j < KP / 16; ++j) {
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const int kr = 16 * j + 4 * g;
+      const int kr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
       if (from && kr < p.dk) load_few<float, 4>(from + kr, p.dk - kr, s);
       S[j][n] = la_f32x4{s[0], s[1], s[2], s[3]};
     }
@@ -97,49 +97,69 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
     for (int i = 0; i < T; i += 2) put4(&sP[(16 * i + r) * PP + 16 * (i + 1) + 4 * g], la_f32x4{0, 0, 0, 0});
   }
 
-  TileLoad<Elem, C, KP> lq, lk;
-  TileLoad<Elem, C, VT> lv;
-  double gate = 0.0;
+  TileLoad<Elem, C, KP, kWhole> lq, lk;
+  TileLoad<Elem, C, VT, kWhole> lv;
+  constexpr uint32_t E = sizeof(Elem);
+  auto rows_of = [&](int64_t c) {
+    const int64_t left = c < c1 ? end - c * C : 0;
+    return left < 0 ? 0 : left < C ? int(left) : C;
+  };
+  const int v_left = p.dv - v0 < VT ? p.dv - v0 : VT;
   auto fetch = [&](int64_t c) {
     const int64_t t0 = c * C;
-    const int rows = t0 >= end || c >= c1 ? 0 : end - t0 < C ? int(end - t0) : C;
-    lq.load(q + t0 * p.q.step, p.q.step, rows, p.dk);
-    lk.load(k + t0 * p.k.step, p.k.step, rows, p.dk);
-    lv.load(v + t0 * p.v.step, p.v.step, rows, p.dv - v0);
-    if (w == 0) gate = load_decay(gates, p.g_step, t0, rows);
+    const int rows = rows_of(c);
+    lq.load(q + t0 * p.q.step, uint32_t(p.q.step) * E, rows, p.dk);
+    lk.load(k + t0 * p.k.step, uint32_t(p.k.step) * E, rows, p.dk);
+    lv.load(v + t0 * p.v.step, uint32_t(p.v.step) * E, rows, v_left);
   };
+  // The last wave, with the fewest tiles of pairs, forms each chunk's decays a chunk ahead.
+  double gate = 0.0;
+  if (w == 3) {
+    gate = load_decay(gates, p.g_step, c0 * C, rows_of(c0));
+    const double next = load_decay(gates, p.g_step, (c0 + 1) * C, rows_of(c0 + 1));
+    decays[c0 & 1].set(gate);
+    gate = next;
+  }
   fetch(c0);
   for (int64_t c = c0; c < c1; ++c) {
     const int64_t t0 = c * C;
+    const Buf to(out + t0 * out_step, kLaBytes);
     const int rows = p.seqlen - t0 < C ? int(p.seqlen - t0) : C;       // of out
     const int live = end <= t0 ? 0 : end - t0 < C ? int(end - t0) : C;  // that hold steps
     if (live > 0) {
+      const Decays<C>& dec = decays[c & 1];
       lds_barrier();  // every wave has read the chunk before
       lq.store(sQ);
       lk.store(sK);
       lv.store(sV);
-      if (w == 0) dec.set(gate);
       lds_barrier();
+      // (ahead of the loads for the next chunk, which it would wait for)
+      if (w == 3) decays[(c + 1) & 1].set(gate);
       fetch(c + 1);
+      if (w == 3) gate = load_decay(gates, p.g_step, (c + 2) * C, rows_of(c + 2));
       // The weights of the pairs s <= t, with the decay between them: tile (i, j) as rows s of
       // columns t, stored by rows t.
+      const WaveTiles mine = wave_tiles<C>(w);
+      auto weights = [&](int i, int j, const Frag<Elem>(&qf)[KB]) {
+        la_f32x4 a = {0, 0, 0, 0};
 #pragma unroll
-      for (int x = 0; x < (kPairs + 3) / 4; ++x) {
-        const int pair = w + 4 * x;
-        if (pair < kPairs) {
-          int i, j;
-          causal_tile(pair, i, j);
-          la_f32x4 a = {0, 0, 0, 0};
+        for (int kb = 0; kb < KB; ++kb) a = mma(row_frag(sK, QP, 16 * j + r, 32 * kb), qf[kb], a);
+        const int t = 16 * i + r, s0 = 16 * j + 4 * g;
+        const typename Decays<C>::Sum to = dec.sum[t];
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-            a = mma(row_frag(sK, QP, 16 * j + r, 32 * kb), row_frag(sQ, QP, 16 * i + r, 32 * kb), a);
-          const int t = 16 * i + r;
+        for (int e = 0; e < 4; ++e)
+          a[e] = s0 + e <= t ? a[e] * p.scale * Decays<C>::between(to, dec.sum[s0 + e]) : 0.0f;
+        put4(&sP[t * PP + s0], a);
+      };
+      {
+        Frag<Elem> qf[KB];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int s = 16 * j + 4 * g + e;
-            a[e] = s <= t ? a[e] * p.scale * dec.between(t, s) : 0.0f;
-          }
-          put4(&sP[t * PP + 16 * j + 4 * g], a);
+        for (int kb = 0; kb < KB; ++kb) qf[kb] = row_frag(sQ, QP, 16 * mine.i + r, 32 * kb);
+        for (int j = mine.j0; j < mine.j1; ++j) weights(mine.i, j, qf);
+        if (mine.more) {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) qf[kb] = row_frag(sQ, QP, r, 32 * kb);
+          weights(0, 0, qf);
         }
       }
       Frag<Elem> vf[SB][NV];
@@ -164,7 +184,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
         for (int n = 0; n < NV; ++n) o[n] = la_f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-          const Frag<Elem> f = row_frag_stacked(sQ, QP, 16 * i + r, 32 * kb);
+          const Frag<Elem> f = row_frag(sQ, QP, 16 * i + r, 32 * kb);
 #pragma unroll
           for (int n = 0; n < NV; ++n) o[n] = mma(sp[kb][n], f, o[n]);
         }
@@ -180,15 +200,13 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
 #pragma unroll
           for (int n = 0; n < NV; ++n) o[n] = mma(vf[sb][n], f, o[n]);
         }
-        if (t < rows) {
 #pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            const int vr = vcol + 16 * n + 4 * g;
-            float y[4];
+        for (int n = 0; n < NV; ++n) {
+          const int vr = vcol + 16 * n + 4 * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = t < live ? o[n][e] : 0.0f;
-            if (vr < p.dv) store_few<Elem, 4>(out + (t0 + t) * out_step + vr, p.dv - vr, y);
-          }
+          for (int e = 0; e < 4; ++e) o[n][e] = t < live ? o[n][e] : 0.0f;
+          store4_at<Elem, kWhole>(to, uint32_t(t) * uint32_t(out_step) * E + uint32_t(vr) * E, p.dv - vr, t < rows,
+                                  o[n]);
         }
       }
       // The state at the chunk's end.
@@ -216,7 +234,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
           for (int e = 0; e < 4; ++e) S[j][n][e] *= total;
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb) {
-          const Frag<Elem> f = col_frag(sK, QP, 32 * sb, 16 * j);
+          const Frag<Elem> f = col_frag_paired(sK, QP, 32 * sb, 32 * (j / 2), j % 2);
 #pragma unroll
           for (int n = 0; n < NV; ++n) S[j][n] = mma(f, add[sb][n], S[j][n]);
         }
@@ -229,8 +247,8 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
           const int vr = vcol + 16 * n + 4 * g;
-          const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (t < rows && vr < p.dv) store_few<Elem, 4>(out + (t0 + t) * out_step + vr, p.dv - vr, zero);
+          store4_at<Elem, kWhole>(to, uint32_t(t) * uint32_t(out_step) * E + uint32_t(vr) * E, p.dv - vr, t < rows,
+                                  la_f32x4{0, 0, 0, 0});
         }
       }
     }
@@ -243,7 +261,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
       float* to = p.final_state + ((b * p.heads + h) * p.dv + vc) * p.dk;
 #pragma unroll
       for (int j = 0; j < KP / 16; ++j) {
-        const int kr = 16 * j + 4 * g;
+        const int kr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
         const float s[4] = {S[j][n][0], S[j][n][1], S[j][n][2], S[j][n][3]};
         if (kr < p.dk) store_few<float, 4>(to + kr, p.dk - kr, s);
       }
@@ -275,25 +293,25 @@ struct StatesParams {
   int heads, y_tiles;
 };
 
-template <typename Elem, int XP, int NY>
+template <typename Elem, int XP, int NY, bool kWhole>
 __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_kernel(StatesParams p) {
   constexpr int C = chunk_of<Elem>(), SB = C / 32, YT = 64 * NY;
   constexpr int XPITCH = la_pitch<Elem>(XP), YPITCH = la_pitch<Elem>(YT);
   __shared__ __attribute__((aligned(16))) Elem sX[C * XPITCH], sY[C * YPITCH];
-  __shared__ Decays<C> dec;
+  __shared__ __attribute__((aligned(16))) Decays<C> decays[2];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-  int64_t at = xcd_order(blockIdx.x, gridDim.x);
-  const int yt = int(at % p.y_tiles);
-  at /= p.y_tiles;
-  const int which = at >= p.rows ? 1 : 0;
+  uint32_t at = xcd_order(blockIdx.x, gridDim.x);
+  const int yt = int(at % uint32_t(p.y_tiles));
+  at /= uint32_t(p.y_tiles);
+  const int which = at >= uint32_t(p.rows) ? 1 : 0;
   const StateParams& d = p.dir[which];
-  at -= which ? p.rows : 0;
+  at -= which ? uint32_t(p.rows) : 0;
   const int64_t state = at;
-  const int64_t seg = at % p.segments;
-  at /= p.segments;
-  const int h = int(at % p.heads);
-  const int64_t b = at / p.heads;
+  const int64_t seg = at % uint32_t(p.segments);
+  at /= uint32_t(p.segments);
+  const int h = int(at % uint32_t(p.heads));
+  const int64_t b = at / uint32_t(p.heads);
   const int y0 = yt * YT;
   const Elem* x = static_cast<const Elem*>(d.x.p) + b * d.x.batch + (h / d.x_group) * d.x.head;
   const Elem* y = static_cast<const Elem*>(d.y.p) + b * d.y.batch + (h / d.y_group) * d.y.head + y0;
@@ -307,29 +325,45 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
 #pragma unroll
     for (int m = 0; m < NY; ++m) S[j][m] = la_f32x4{0, 0, 0, 0};
   double all = 0.0;
-  TileLoad<Elem, C, XP> lx;
-  TileLoad<Elem, C, YT> ly;
-  double gate = 0.0;
-  auto fetch = [&](int64_t i) {
-    const int64_t c = d.reverse ? c1 - 1 - i : c0 + i, t0 = c * C;
-    const int rows = i >= n || t0 >= end ? 0 : end - t0 < C ? int(end - t0) : C;
-    lx.load(x + (rows ? t0 : 0) * d.x.step, d.x.step, rows, d.xd);
-    ly.load(y + (rows ? t0 : 0) * d.y.step, d.y.step, rows, d.yd - y0);
-    if (w == 0) gate = load_decay(gates, p.g_step, t0, rows);
+  TileLoad<Elem, C, XP, kWhole> lx;
+  TileLoad<Elem, C, YT, kWhole> ly;
+  constexpr uint32_t E = sizeof(Elem);
+  const int y_left = d.yd - y0 < YT ? d.yd - y0 : YT;
+  auto chunk = [&](int64_t i) { return d.reverse ? c1 - 1 - i : c0 + i; };
+  auto rows_of = [&](int64_t i) {
+    const int64_t left = i < n ? end - chunk(i) * C : 0;
+    return left < 0 ? 0 : left < C ? int(left) : C;
   };
-  fetch(0);
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t c = d.reverse ? c1 - 1 - i : c0 + i;
-    if (c * C >= end) {
-      fetch(i + 1);
-      continue;
-    }
+  auto fetch = [&](int64_t i) {
+    const int64_t t0 = chunk(i) * C;
+    const int rows = rows_of(i);
+    lx.load(x + (rows ? t0 : 0) * d.x.step, uint32_t(d.x.step) * E, rows, d.xd);
+    ly.load(y + (rows ? t0 : 0) * d.y.step, uint32_t(d.y.step) * E, rows, y_left);
+  };
+  // Chunks behind the row's end leave the state as it is: the first of a reverse walk.
+  int64_t i0 = 0, i1 = n;
+  if (d.reverse)
+    while (i0 < n && rows_of(i0) == 0) ++i0;
+  else
+    while (i1 > 0 && rows_of(i1 - 1) == 0) --i1;
+  fetch(i0);
+  double gate = 0.0;
+  if (w == 0 && i0 < i1) {
+    gate = load_decay(gates, p.g_step, chunk(i0) * C, rows_of(i0));
+    const double next = load_decay(gates, p.g_step, chunk(i0 + 1) * C, rows_of(i0 + 1));
+    all = decays[i0 & 1].set(gate);
+    gate = next;
+  }
+  for (int64_t i = i0; i < i1; ++i) {
+    const Decays<C>& dec = decays[i & 1];
     lds_barrier();
     lx.store(sX);
     ly.store(sY);
-    if (w == 0) all += dec.set(gate);
     lds_barrier();
+    // (ahead of the loads for the next chunk, which it would wait for)
+    if (w == 0 && i + 1 < i1) all += decays[(i + 1) & 1].set(gate);
     fetch(i + 1);
+    if (w == 0) gate = load_decay(gates, p.g_step, chunk(i + 2) * C, rows_of(i + 2));
     const float total = dec.total;
     Pieces<Elem, 3> add[SB][NY];
 #pragma unroll
@@ -357,7 +391,7 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
         for (int e = 0; e < 4; ++e) S[j][m][e] *= total;
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
-        const Frag<Elem> f = col_frag(sX, XPITCH, 32 * sb, 16 * j);
+        const Frag<Elem> f = col_frag_paired(sX, XPITCH, 32 * sb, 32 * (j / 2), j % 2);
 #pragma unroll
         for (int m = 0; m < NY; ++m) S[j][m] = mma(f, add[sb][m], S[j][m]);
       }
@@ -371,7 +405,8 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
     if (yc >= ypad) continue;
 #pragma unroll
     for (int j = 0; j < XP / 16; ++j)
-      if (16 * j < xpad) *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 16 * j + 4 * g) = S[j][m];
+      if (16 * j < xpad)
+        *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 32 * (j / 2) + 8 * g + 4 * (j % 2)) = S[j][m];
   }
   if (which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
 }
@@ -442,35 +477,41 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(JoinParams p) {
 // ---------------------------------------------------------------- launches
 
 template <typename Elem, int XP, int NY>
-void run_states(const StatesParams& p, int dirs, hipStream_t s) {
-  hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY>), dim3(uint32_t(p.rows * p.y_tiles * dirs)),
-                     dim3(kLaThreads), 0, s, p);
+void run_states(const StatesParams& p, int dirs, bool whole, hipStream_t s) {
+  const dim3 grid{uint32_t(p.rows * p.y_tiles * dirs)}, block{kLaThreads};
+  if (whole) hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY, false>), grid, block, 0, s, p);
 }
 
 template <typename Elem>
-void run_states_of(StatesParams& p, int dirs, hipStream_t s) {
+void run_states_of(StatesParams& p, int dirs, bool whole, hipStream_t s) {
   const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = yd <= 64 || xd > 128 ? 1 : 2;
   p.y_tiles = (yd + 64 * ny - 1) / (64 * ny);
   if (ny == 1) {
-    if (xd <= 64) return run_states<Elem, 64, 1>(p, dirs, s);
-    if (xd <= 128) return run_states<Elem, 128, 1>(p, dirs, s);
-    return run_states<Elem, 256, 1>(p, dirs, s);
+    if (xd <= 64) return run_states<Elem, 64, 1>(p, dirs, whole, s);
+    if (xd <= 128) return run_states<Elem, 128, 1>(p, dirs, whole, s);
+    return run_states<Elem, 256, 1>(p, dirs, whole, s);
   }
-  if (xd <= 64) return run_states<Elem, 64, 2>(p, dirs, s);
-  run_states<Elem, 128, 2>(p, dirs, s);
+  if (xd <= 64) return run_states<Elem, 64, 2>(p, dirs, whole, s);
+  run_states<Elem, 128, 2>(p, dirs, whole, s);
+}
+
+template <typename Elem, int KP, int NV>
+void run_fwd_kernel(const FwdParams& p, int64_t groups, bool whole, hipStream_t s) {
+  const dim3 grid{uint32_t(groups)}, block{kLaThreads};
+  if (whole) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, KP, NV, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((linattn_fwd_kernel<Elem, KP, NV, false>), grid, block, 0, s, p);
 }
 
 template <typename Elem>
-void run_fwd(const FwdParams& p, int64_t groups, hipStream_t s) {
-  const dim3 grid{uint32_t(groups)}, block{kLaThreads};
+void run_fwd(const FwdParams& p, int64_t groups, bool whole, hipStream_t s) {
   if (linattn_value_tile(p.dk, p.dv) == 64) {
-    if (p.dk <= 64) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 64, 1>), grid, block, 0, s, p);
-    else if (p.dk <= 128) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 128, 1>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 256, 1>), grid, block, 0, s, p);
-  } else {
-    if (p.dk <= 64) hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 64, 2>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((linattn_fwd_kernel<Elem, 128, 2>), grid, block, 0, s, p);
+    if (p.dk <= 64) return run_fwd_kernel<Elem, 64, 1>(p, groups, whole, s);
+    if (p.dk <= 128) return run_fwd_kernel<Elem, 128, 1>(p, groups, whole, s);
+    return run_fwd_kernel<Elem, 256, 1>(p, groups, whole, s);
   }
+  if (p.dk <= 64) return run_fwd_kernel<Elem, 64, 2>(p, groups, whole, s);
+  run_fwd_kernel<Elem, 128, 2>(p, groups, whole, s);
 }
 
 }  // namespace
@@ -482,6 +523,7 @@ int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
   const int64_t c = linattn_chunk(a.io), chunks = (a.seqlen + c - 1) / c;
   const int64_t floats = linattn_state_floats(a.dk, a.dv), rows = a.batch * a.heads * chunks;
   const int group = int(a.heads / a.qk_heads);
+  const bool whole = linattn_whole(a, true);
   float* adjoints = a.workspace + rows * floats;
   StatesParams p{};
   p.dir[0] = StateParams{a.v, a.k, 1, group, int(a.dv), int(a.dk), false, 1.0f, a.workspace};
@@ -493,8 +535,8 @@ int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
   p.seqlen = a.seqlen, p.chunks = chunks, p.per = 1, p.segments = chunks, p.rows = rows;
   p.heads = int(a.heads);
   if (chunks > 0) {
-    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 2, s);
-    else run_states_of<float>(p, 2, s);
+    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 2, whole, s);
+    else run_states_of<float>(p, 2, whole, s);
     if (hipGetLastError() != hipSuccess) return -1;
   }
   JoinParams j{};
@@ -516,6 +558,7 @@ int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
   const LinattnSegments seg = linattn_segments(a.batch, a.heads, a.dk, a.dv, a.seqlen, a.io);
   const int64_t floats = linattn_state_floats(a.dv, a.dk), rows = a.batch * a.heads * seg.count;
   const int group = int(a.heads / a.qk_heads);
+  const bool whole = linattn_whole(a, false);
   if (seg.count > 1) {
     StatesParams p{};
     p.dir[0] = StateParams{a.k, a.v, group, 1, int(a.dk), int(a.dv), false, 1.0f, a.workspace};
@@ -525,8 +568,8 @@ int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
     p.totals = a.workspace + rows * floats;
     p.seqlen = a.seqlen, p.chunks = seg.chunks, p.per = seg.per, p.segments = seg.count, p.rows = rows;
     p.heads = int(a.heads);
-    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 1, s);
-    else run_states_of<float>(p, 1, s);
+    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 1, whole, s);
+    else run_states_of<float>(p, 1, whole, s);
     if (hipGetLastError() != hipSuccess) return -1;
     JoinParams j{};
     j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
@@ -553,8 +596,8 @@ int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
   p.heads = int(a.heads), p.group = group, p.dk = int(a.dk), p.dv = int(a.dv);
   p.value_tiles = int(linattn_value_tiles(a.dk, a.dv));
   p.scale = a.scale;
-  if (a.io == Io::BF16) run_fwd<uint16_t>(p, rows * p.value_tiles, s);
-  else run_fwd<float>(p, rows * p.value_tiles, s);
+  if (a.io == Io::BF16) run_fwd<uint16_t>(p, rows * p.value_tiles, whole, s);
+  else run_fwd<float>(p, rows * p.value_tiles, whole, s);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

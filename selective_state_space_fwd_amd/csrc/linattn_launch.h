@@ -75,6 +75,18 @@ inline int64_t linattn_state_floats(int64_t rows, int64_t cols) {
 
 inline int64_t linattn_join_blocks(int64_t state_floats) { return (state_floats / 4 + 255) / 256; }
 
+// Rows of whole 16-byte words at 4-byte aligned addresses: a load a word.
+inline bool linattn_whole(const LinattnArgs& a, bool bwd) {
+  const int64_t esz = a.io == Io::BF16 ? 2 : 4, word = 16 / esz, even = 4 / esz;
+  auto rows = [&](const HeadRows& r) {
+    return reinterpret_cast<uintptr_t>(r.p) % 4 == 0 && r.batch % even == 0 && r.step % even == 0 && r.head % even == 0;
+  };
+  return a.dk % word == 0 && a.dv % word == 0 && rows(a.q) && rows(a.k) && rows(a.v) && (!bwd || rows(a.dout));
+}
+
+// Whether a chunk's rows, `step` elements apart, lie within the 32-bit byte offsets of the kernels.
+inline bool linattn_reach(int64_t step, int64_t esz) { return step < (int64_t(1) << 30) / (64 * esz); }
+
 int launch_linattn_chunk_states(const LinattnArgs& a, void* stream);
 int launch_linattn_fwd(const LinattnArgs& a, void* stream);
 int launch_linattn_bwd(const LinattnArgs& a, void* stream);
