@@ -197,11 +197,11 @@ constexpr uint32_t kLaBytes = 0x7fffffffu;  // offsets in use are below it (lina
 // A tile of C steps x D columns on its way from memory to LDS, spread over the workgroup's threads.
 // kWhole: rows of whole 16-byte words at 4-byte aligned addresses, a load a word; else a load an
 // element.
-template <typename Elem, int C, int D, bool kWhole>
+template <typename Elem, int C, int D, bool kWhole, int kThreads = kLaThreads>
 struct TileLoad {
-  static constexpr int kN = Vec<Elem>::kN, kRow = D / kN, kWords = C * kRow / kLaThreads;
-  static constexpr int kStep = kLaThreads / kRow;  // rows from one of a thread's words to the next
-  static_assert(C * kRow % kLaThreads == 0 && kLaThreads % kRow == 0, "whole words, whole rows");
+  static constexpr int kN = Vec<Elem>::kN, kRow = D / kN, kWords = C * kRow / kThreads;
+  static constexpr int kStep = kThreads / kRow;  // rows from one of a thread's words to the next
+  static_assert(C * kRow % kThreads == 0 && kThreads % kRow == 0, "whole words, whole rows");
   uint4 w[kWords];
 
   // Rows [0, rows) of `dim` elements, `step` bytes apart; zeros elsewhere (nothing there is read).
@@ -234,7 +234,7 @@ struct TileLoad {
   __device__ __forceinline__ void store(Elem* tile) const {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int at = int(threadIdx.x) + i * kLaThreads, row = at / kRow, col = (at % kRow) * kN;
+      const int at = int(threadIdx.x) + i * kThreads, row = at / kRow, col = (at % kRow) * kN;
       *reinterpret_cast<uint4*>(tile + row * la_pitch<Elem>(D) + col) = w[i];
     }
   }
@@ -323,8 +323,24 @@ struct Decays {
     }
     return all;
   }
-  static __device__ __forceinline__ float between(const Sum& t, const Sum& s) {
-    return exp2_hw((t.hi - s.hi) + (t.lo - s.lo));
+  // From s0 + e to t, e < 4. All four whatever comes of them: a condition around one would put its
+  // loads and exponential in a branch of their own.
+  __device__ __forceinline__ void between(int t, int s0, float (&keep)[4]) const {
+    const Sum to = sum[t];
+    Sum from[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) from[e] = sum[s0 + e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) keep[e] = exp2_hw((to.hi - from[e].hi) + (to.lo - from[e].lo));
+  }
+  // From s to t0 + e.
+  __device__ __forceinline__ void onwards(int s, int t0, float (&keep)[4]) const {
+    const Sum from = sum[s];
+    Sum to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = sum[t0 + e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) keep[e] = exp2_hw((to[e].hi - from.hi) + (to[e].lo - from.lo));
   }
 };
 

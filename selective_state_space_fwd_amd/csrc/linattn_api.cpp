@@ -59,7 +59,7 @@ int check_gates(const float* g, const int64_t* strides, const Sizes& z, ssm::Lin
 
 bool grids_fit(const Sizes& z, bool bwd) {
   const ssm::Io io = io_of(z.esz);
-  const int64_t c = ssm::linattn_chunk(io), chunks = (z.seqlen + c - 1) / c;
+  const int64_t c = ssm::linattn_bwd_chunk(io, z.dk, z.dv), chunks = (z.seqlen + c - 1) / c;
   const int64_t bh = product({z.batch, z.heads});
   if (bh < 0) return false;
   if (!bwd) {
@@ -87,9 +87,10 @@ int64_t fwd_workspace(const Sizes& z) {
 }
 
 int64_t bwd_workspace(const Sizes& z) {
-  const int64_t c = ssm::linattn_chunk(io_of(z.esz)), chunks = (z.seqlen + c - 1) / c;
-  // two states, the decay over the chunk, and a sum for dg
-  return product({z.batch, z.heads, chunks, 2 * ssm::linattn_state_floats(z.dk, z.dv) + 2, 4});
+  // (the sizes' products are known to fit: twice the states of every chunk)
+  const int64_t c = ssm::linattn_bwd_chunk(io_of(z.esz), z.dk, z.dv), chunks = (z.seqlen + c - 1) / c;
+  if (product({z.batch, z.heads, chunks, 4 * ssm::linattn_state_floats(z.dk, z.dv) + 4, 4}) < 0) return -1;
+  return ssm::linattn_bwd_states(z.batch, z.heads, z.dk, z.dv, z.seqlen, io_of(z.esz)).total * 4;
 }
 
 }  // namespace

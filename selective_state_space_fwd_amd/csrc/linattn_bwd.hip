@@ -18,8 +18,8 @@
 // linattn_state_kernel and linattn_join_kernel (linattn_kernels.hip) leave S and R of every chunk
 // in the workspace, [dk][dv] in fp32; linattn_bwd_kernel then takes a (batch row, query head,
 // chunk) per workgroup, the heads that share the query one after another (their dq and dk add
-// up in its accumulators, in a fixed order). A wave owns a quarter of dk for dq and dk, a quarter
-// of dv for dv, so that each value of S and R is split into operand pieces once.
+// up in its accumulators, in a fixed order). A wave owns an eighth of dk for dq and dk, an eighth of dv
+// for dv, so that each value of S and R is split into operand pieces once.
 //
 // Roundings: the pairs' weights (scale D qk and scale D dov) are rounded to bf16 once, as operands,
 // next to results in bf16. S and R enter in three bf16 pieces where dg, a result in fp32, comes
@@ -48,16 +48,56 @@ struct BwdParams {
   float scale;
 };
 
+constexpr int kBwdThreads = 512;
+
+// The pair tiles (i, j), j0 <= j < j1, of each of the eight waves: two at most. The last two have none:
+// they do the next head's decays and the last one's dg meanwhile.
+struct BwdTiles {
+  int i, j0, j1;
+};
+template <int C>
+__device__ __forceinline__ BwdTiles bwd_tiles(int w) {
+  if constexpr (C == 64) {
+    if (w == 0) return {3, 0, 2};
+    if (w == 1) return {3, 2, 4};
+    if (w == 2) return {2, 0, 2};
+    if (w == 3) return {2, 2, 3};
+    if (w == 4) return {1, 0, 2};
+    return {0, 0, w == 5 ? 1 : 0};
+  } else {
+    if (w == 0) return {1, 0, 1};
+    if (w == 1) return {1, 1, 2};
+    return {0, 0, w == 2 ? 1 : 0};
+  }
+}
+
+// What dg of one head comes from, by step of the chunk.
+template <int C>
+struct DgParts {
+  float row[C / 16][C], col[C / 16][C];  // of W, by the tile they are of
+  float qs[8][C], ks[8][C];              // q . dq^S and k . dk^R, by wave
+  float x[8], total;
+};
+
 template <typename Elem, int KP, int VP, bool kWhole>
-__global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void linattn_bwd_kernel(BwdParams p) {
-  constexpr int C = chunk_of<Elem>(), T = C / 16, SB = C / 32;
+__global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p) {
+  constexpr int C = linattn_bwd_chunk(sizeof(Elem) == 2 ? Io::BF16 : Io::F32, KP, VP);
+  constexpr int T = C / 16, SB = C / 32, KB = KP / 32, VB = VP / 32;
   constexpr uint32_t E = sizeof(Elem);
-  constexpr int NK = KP / 64, NV = VP / 64;  // 16-wide tiles of dk and dv a wave owns
+  // The largest sizes keep fewer operands at a time, for want of registers.
+  constexpr int kUnroll = KB + VB > 8 ? 1 : 8;
+  // The 16-wide column tiles of dk and dv that a wave owns, for all steps; where there are only four,
+  // one for half of the steps.
+  constexpr bool kHalfK = KP < 128, kHalfV = VP < 128;
+  constexpr int NK = kHalfK ? 1 : KP / 128, NV = kHalfV ? 1 : VP / 128;
+  constexpr int TK = kHalfK ? T / 2 : T, TV = kHalfV ? T / 2 : T;
+  // The states' operands are loaded ahead of the pairs where they fit in registers.
+  constexpr bool kAhead = NK * VB <= 4;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
   __shared__ __attribute__((aligned(16))) Elem sP[C * PP], sD[C * PP];  // weights by rows s: scale D qk, scale D dov
-  __shared__ Decays<C> dec;
-  __shared__ float sRow[T][C], sCol[T][C], sQs[4][C], sKs[4][C], sX[4];
+  __shared__ __attribute__((aligned(16))) Decays<C> decays[2];          // of even and odd heads
+  __shared__ DgParts<C> parts[2];
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
@@ -71,14 +111,16 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
   const int64_t q_step = int64_t(p.qk_heads) * p.dk, v_step = int64_t(p.heads) * p.dv;
   Elem* dq = static_cast<Elem*>(p.dq) + (b * p.seqlen + t0) * q_step + hk * p.dk;
   Elem* dk = static_cast<Elem*>(p.dk_out) + (b * p.seqlen + t0) * q_step + hk * p.dk;
+  const int kt = kHalfK ? w & 3 : NK * w, ik = kHalfK ? (w >> 2) * TK : 0;
+  const int vt = kHalfV ? w & 3 : NV * w, iv = kHalfV ? (w >> 2) * TV : 0;
 
-  la_f32x4 aq[NK][T], ak[NK][T];
+  la_f32x4 aq[NK][TK], ak[NK][TK];
 #pragma unroll
   for (int n = 0; n < NK; ++n)
 #pragma unroll
-    for (int i = 0; i < T; ++i) aq[n][i] = ak[n][i] = la_f32x4{0, 0, 0, 0};
+    for (int i = 0; i < TK; ++i) aq[n][i] = ak[n][i] = la_f32x4{0, 0, 0, 0};
 
-  // rows a..a+3 of dim columns, steps 16 i + r; zero behind the end.
+  // Columns col .. + 3 of step 16 i + r; zero behind the end.
   auto put = [&](Elem* base, int64_t step, int i, int col, int dim, la_f32x4 v) {
     const int t = 16 * i + r;
 #pragma unroll
@@ -86,14 +128,75 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
     store4_at<Elem, kWhole>(Buf(base, kLaBytes), uint32_t(t) * uint32_t(step) * E + uint32_t(col) * E, dim - col,
                             t < rows, v);
   };
+  auto dv_of = [&](int h) { return static_cast<Elem*>(p.dv_out) + (b * p.seqlen + t0) * v_step + int64_t(h) * p.dv; };
 
-  if (live > 0) {
+  if (live == 0) {
+    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int i = 0; i < TV; ++i) put(dv_of(h), v_step, iv + i, 16 * (vt + n) + 4 * g, p.dv, la_f32x4{0, 0, 0, 0});
+      if (p.dg && int(threadIdx.x) < rows) p.dg[(b * p.seqlen + t0 + threadIdx.x) * p.heads + h] = 0.0f;
+      if (p.dg_sums && threadIdx.x == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = 0.0f;
+    }
+  } else {
+    TileLoad<Elem, C, VP, kWhole, kBwdThreads> lv, lo;
+    auto fetch = [&](int hh) {
+      const int64_t h = hk * p.group + hh;
+      const int n = hh < p.group ? live : 0;
+      lv.load(static_cast<const Elem*>(p.v.p) + b * p.v.batch + (n ? h : 0) * p.v.head + t0 * p.v.step,
+              uint32_t(p.v.step) * E, n, p.dv);
+      lo.load(static_cast<const Elem*>(p.dout.p) + b * p.dout.batch + (n ? h : 0) * p.dout.head + t0 * p.dout.step,
+              uint32_t(p.dout.step) * E, n, p.dv);
+    };
+    auto gate_of = [&](int hh) {
+      return load_decay(p.g && hh < p.group ? p.g + b * p.g_batch + (hk * p.group + hh) * p.g_head : nullptr, p.g_step,
+                        t0, live);
+    };
+    // dg of the head whose parts lie in parts[hh & 1], by one wave.
+    auto finish = [&](int hh) {
+      const DgParts<C>& d = parts[hh & 1];
+      const int h = hk * p.group + hh, t = l < C ? l : C - 1, i = t / 16;
+      double down = 0.0, up = 0.0, around = 0.0;
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        if (j <= i) down += d.row[j][t];
+        if (j >= i) down -= d.col[j][t];
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const bool mine = !kHalfK || (x >> 2) == i / TK;
+        if (mine) down += d.qs[x][t];
+        if (mine) up += d.ks[x][t];
+        if (!kHalfK || x < 4) around += d.x[x];
+      }
+      if (l >= C) down = up = 0.0;
+      const double before = wave_prefix_f64(down), all = dpp_f64(before, 63);
+      const double behind = wave_prefix_f64(up) - up;
+      double dg = all - before + down + behind + double(d.total) * around;
+      if (l >= live) dg = 0.0;
+      if (p.dg && l < rows) p.dg[(b * p.seqlen + t0 + l) * p.heads + h] = float(dg);
+      if (p.dg_sums) {
+        const double sum = dpp_f64(wave_prefix_f64(dg), 63);
+        if (l == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = float(sum);
+      }
+    };
+    const bool want_dg = p.dg || p.dg_sums;
+
+    double gate = 0.0;
+    if (w == 6) {
+      gate = gate_of(0);
+      const double next = gate_of(1);
+      decays[0].set(gate);
+      gate = next;
+    }
     {
-      TileLoad<Elem, C, KP, kWhole> lq, lk;
+      TileLoad<Elem, C, KP, kWhole, kBwdThreads> lq, lk;
       lq.load(static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head + t0 * p.q.step,
               uint32_t(p.q.step) * E, live, p.dk);
       lk.load(static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head + t0 * p.k.step,
               uint32_t(p.k.step) * E, live, p.dk);
+      fetch(0);
       lq.store(sQ);
       lk.store(sK);
     }
@@ -105,229 +208,234 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 && VP <= 128 ? 2 : 1) void li
         put4(&sD[(16 * (i + 1) + r) * PP + 16 * i + 4 * g], la_f32x4{0, 0, 0, 0});
       }
     }
-  }
 
-  for (int hh = 0; hh < p.group; ++hh) {
-    const int h = hk * p.group + hh;
-    Elem* dv = static_cast<Elem*>(p.dv_out) + (b * p.seqlen + t0) * v_step + h * p.dv;
-    if (live == 0) {
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int i = 0; i < T; ++i) put(dv, v_step, i, 16 * (NV * w + n) + 4 * g, p.dv, la_f32x4{0, 0, 0, 0});
-      if (p.dg && int(threadIdx.x) < rows) p.dg[(b * p.seqlen + t0 + threadIdx.x) * p.heads + h] = 0.0f;
-      if (p.dg_sums && threadIdx.x == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = 0.0f;
-      continue;
-    }
-    const float* S = p.states + ((b * p.heads + h) * p.chunks + c) * p.state_floats;
-    const float* R = p.adjoints + ((b * p.heads + h) * p.chunks + c) * p.state_floats;
-    {
-      TileLoad<Elem, C, VP, kWhole> lv, lo;
-      double gate = 0.0;
-      lv.load(static_cast<const Elem*>(p.v.p) + b * p.v.batch + h * p.v.head + t0 * p.v.step,
-              uint32_t(p.v.step) * E, live, p.dv);
-      lo.load(static_cast<const Elem*>(p.dout.p) + b * p.dout.batch + h * p.dout.head + t0 * p.dout.step,
-              uint32_t(p.dout.step) * E, live, p.dv);
-      if (w == 0) gate = load_decay(p.g ? p.g + b * p.g_batch + h * p.g_head : nullptr, p.g_step, t0, live);
+    for (int hh = 0; hh < p.group; ++hh) {
+      const int h = hk * p.group + hh;
+      const int64_t state = ((b * p.heads + h) * p.chunks + c) * p.state_floats;
+      const Buf S(p.states + state, uint32_t(p.state_floats) * 4), R(p.adjoints + state, uint32_t(p.state_floats) * 4);
+      const Decays<C>& dec = decays[hh & 1];
+      DgParts<C>& part = parts[hh & 1];
+      // Row k of a state, values v of a block of 32: operands of dq and dk.
+      auto state_at = [&](int n, int vb) {
+        const int k = 16 * (kt + n) + r, v = 32 * vb + 8 * g;
+        return k < p.kpad && v < p.vpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
+      };
+      uint4 fs[kAhead ? NK : 1][VB][2], fr[kAhead ? NK : 1][VB][2];
+
       lds_barrier();  // every wave has read the head before
       lv.store(sV);
       lo.store(sO);
-      if (w == 0) dec.set(gate);
-    }
-    lds_barrier();
-
-    // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
-    const WaveTiles mine = wave_tiles<C>(w);
-    auto pairs = [&](int i, int j, const Frag<Elem>(&qf)[KP / 32], const Frag<Elem>(&of)[VP / 32]) {
-      la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
-#pragma unroll
-      for (int kb = 0; kb < KP / 32; ++kb) a = mma(qf[kb], row_frag(sK, QP, 16 * j + r, 32 * kb), a);
-#pragma unroll
-      for (int vb = 0; vb < VP / 32; ++vb) d = mma(of[vb], row_frag(sV, OP, 16 * j + r, 32 * vb), d);
-      const int s = 16 * j + r;
-      const typename Decays<C>::Sum from = dec.sum[s];
-      float wrow[4], wcol = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * i + 4 * g + e;
-        const float m = s <= t ? p.scale * Decays<C>::between(dec.sum[t], from) : 0.0f;
-        d[e] = s <= t ? d[e] * m : 0.0f;
-        wrow[e] = s < t ? a[e] * d[e] : 0.0f;
-        a[e] = s <= t ? a[e] * m : 0.0f;
-        wcol += wrow[e];
-      }
-      put4(&sP[s * PP + 16 * i + 4 * g], a);
-      put4(&sD[s * PP + 16 * i + 4 * g], d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float sum = sum_lanes<4>(wrow[e]);
-        if (r == 0) sRow[j][16 * i + 4 * g + e] = sum;
-      }
-      wcol += __shfl_xor(wcol, 16, 64);
-      wcol += __shfl_xor(wcol, 32, 64);
-      if (g == 0) sCol[i][s] = wcol;
-    };
-    {
-      Frag<Elem> qf[KP / 32], of[VP / 32];
-      auto rows_at = [&](int i) {
-#pragma unroll
-        for (int kb = 0; kb < KP / 32; ++kb) qf[kb] = row_frag(sQ, QP, 16 * i + r, 32 * kb);
-#pragma unroll
-        for (int vb = 0; vb < VP / 32; ++vb) of[vb] = row_frag(sO, OP, 16 * i + r, 32 * vb);
-      };
-      rows_at(mine.i);
-      for (int j = mine.j0; j < mine.j1; ++j) pairs(mine.i, j, qf, of);
-      if (mine.more) {
-        rows_at(0);
-        pairs(0, 0, qf, of);
-      }
-    }
-    lds_barrier();
-
-    // dq and dk of this wave's columns of dk.
-    float dots = 0.0f;  // <R, S> over them
-    float qs[T], ks[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i) qs[i] = ks[i] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const int k0 = 16 * (NK * w + n);
-      if (k0 >= p.dk) break;
-      la_f32x4 xq[T], xk[T];
-#pragma unroll
-      for (int i = 0; i < T; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int vb = 0; vb < VP / 32; ++vb) {
-        if (32 * vb >= p.vpad) break;
-        const int64_t off = int64_t(k0 + r) * p.vpad + 32 * vb + 8 * g;
-        const la_f32x4 s0 = *reinterpret_cast<const la_f32x4*>(S + off),
-                       s1 = *reinterpret_cast<const la_f32x4*>(S + off + 4),
-                       r0 = *reinterpret_cast<const la_f32x4*>(R + off),
-                       r1 = *reinterpret_cast<const la_f32x4*>(R + off + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dots = __builtin_fmaf(s0[e], r0[e], dots);
-          dots = __builtin_fmaf(s1[e], r1[e], dots);
-        }
-        Pieces<Elem, 3> ps, pr;
-        ps.split({s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]});
-        pr.split({r0[0], r0[1], r0[2], r0[3], r1[0], r1[1], r1[2], r1[3]});
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-          xq[i] = mma(ps, row_frag(sO, OP, 16 * i + r, 32 * vb), xq[i]);
-          xk[i] = mma(pr, row_frag(sV, OP, 16 * i + r, 32 * vb), xk[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const int t = 16 * i + r;
-        const float into = dec.into[t] * p.scale, onto = dec.onto[t];
-        const la_f32x4 qv = get4(&sQ[t * QP + k0 + 4 * g]), kv = get4(&sK[t * QP + k0 + 4 * g]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xq[i][e] *= into;
-          xk[i][e] *= onto;
-          qs[i] = __builtin_fmaf(qv[e], xq[i][e], qs[i]);
-          ks[i] = __builtin_fmaf(kv[e], xk[i][e], ks[i]);
-          aq[n][i][e] += xq[i][e];
-          ak[n][i][e] += xk[i][e];
-        }
-      }
-#pragma unroll
-      for (int sb = 0; sb < SB; ++sb) {
-        const Frag<Elem> kf = col_frag(sK, QP, 32 * sb, k0), qf = col_frag(sQ, QP, 32 * sb, k0);
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-          if (i / 2 >= sb) aq[n][i] = mma(kf, col_frag(sD, PP, 32 * sb, 16 * i), aq[n][i]);
-          if (i / 2 <= sb) ak[n][i] = mma(qf, row_frag(sD, PP, 16 * i + r, 32 * sb), ak[n][i]);
-        }
-      }
-    }
-    // dv of this wave's columns of dv.
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int v0 = 16 * (NV * w + n);
-      if (v0 >= p.dv) break;
-      la_f32x4 av[T];
-#pragma unroll
-      for (int i = 0; i < T; ++i) av[i] = la_f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int kb = 0; kb < KP / 32; ++kb) {
-        if (32 * kb >= p.kpad) break;
-        const float* from = R + int64_t(32 * kb + 8 * g) * p.vpad + v0 + r;
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = from[e * p.vpad];
-        Pieces<Elem, 2> pr;
-        pr.split(x);
-#pragma unroll
-        for (int i = 0; i < T; ++i) av[i] = mma(pr, row_frag(sK, QP, 16 * i + r, 32 * kb), av[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const float onto = dec.onto[16 * i + r];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) av[i][e] *= onto;
-      }
-#pragma unroll
-      for (int sb = 0; sb < SB; ++sb) {
-        const Frag<Elem> of = col_frag(sO, OP, 32 * sb, v0);
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-          if (i / 2 <= sb) av[i] = mma(of, row_frag(sP, PP, 16 * i + r, 32 * sb), av[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < T; ++i) put(dv, v_step, i, v0 + 4 * g, p.dv, av[i]);
-    }
-    if (p.dg || p.dg_sums) {
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        float a = qs[i], d = ks[i];
-        a += __shfl_xor(a, 16, 64);
-        a += __shfl_xor(a, 32, 64);
-        d += __shfl_xor(d, 16, 64);
-        d += __shfl_xor(d, 32, 64);
-        if (g == 0) {
-          sQs[w][16 * i + r] = a;
-          sKs[w][16 * i + r] = d;
-        }
-      }
-      dots = sum_lanes<6>(dots);
-      if (l == 0) sX[w] = dots;
       lds_barrier();
-      if (w == 0) {
-        const int t = l < C ? l : C - 1, i = t / 16;
-        double down = 0.0, up = 0.0;
+      // (ahead of the loads, which it would wait for)
+      if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set(gate);
+      if constexpr (kAhead) {
 #pragma unroll
-        for (int j = 0; j < T; ++j) {
-          if (j <= i) down += sRow[j][t];
-          if (j >= i) down -= sCol[j][t];
-        }
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          down += sQs[x][t];
-          up += sKs[x][t];
-        }
-        if (l >= C) down = up = 0.0;
-        const double before = wave_prefix_f64(down), all = dpp_f64(before, 63);
-        const double behind = wave_prefix_f64(up) - up;
-        const double around = double(dec.total) * (double(sX[0]) + sX[1] + sX[2] + sX[3]);
-        double dg = all - before + down + behind + around;
-        if (l >= live) dg = 0.0;
-        if (p.dg && l < rows) p.dg[(b * p.seqlen + t0 + l) * p.heads + h] = float(dg);
-        if (p.dg_sums) {
-          const double sum = dpp_f64(wave_prefix_f64(dg), 63);
-          if (l == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = float(sum);
+          for (int vb = 0; vb < VB; ++vb) {
+            const uint32_t off = state_at(n, vb);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              fs[n][vb][e] = S.load16(off + 16u * e);
+              fr[n][vb][e] = R.load16(off + 16u * e);
+            }
+          }
+      }
+      fetch(hh + 1);
+      if (w == 6) gate = gate_of(hh + 2);
+
+      // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
+      const BwdTiles mine = bwd_tiles<C>(w);
+      if (mine.j1 > mine.j0) {
+        const int i = mine.i;
+        for (int j = mine.j0; j < mine.j1; ++j) {
+          la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
+#pragma unroll kUnroll
+          for (int kb = 0; kb < KB; ++kb)
+            a = mma(row_frag(sQ, QP, 16 * i + r, 32 * kb), row_frag(sK, QP, 16 * j + r, 32 * kb), a);
+#pragma unroll kUnroll
+          for (int vb = 0; vb < VB; ++vb)
+            d = mma(row_frag(sO, OP, 16 * i + r, 32 * vb), row_frag(sV, OP, 16 * j + r, 32 * vb), d);
+          const int s = 16 * j + r;
+          float keep[4], wrow[4], wcol = 0.0f;
+          dec.onwards(s, 16 * i + 4 * g, keep);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 16 * i + 4 * g + e;
+            const float m = p.scale * keep[e], da = d[e] * m, aa = a[e] * m, ww = a[e] * da;
+            d[e] = s <= t ? da : 0.0f;
+            a[e] = s <= t ? aa : 0.0f;
+            wrow[e] = s < t ? ww : 0.0f;
+            wcol += wrow[e];
+          }
+          put4(&sP[s * PP + 16 * i + 4 * g], a);
+          put4(&sD[s * PP + 16 * i + 4 * g], d);
+          if (want_dg) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float sum = sum_lanes<4>(wrow[e]);
+              if (r == 0) part.row[j][16 * i + 4 * g + e] = sum;
+            }
+            wcol += __shfl_xor(wcol, 16, 64);
+            wcol += __shfl_xor(wcol, 32, 64);
+            if (g == 0) part.col[i][s] = wcol;
+          }
         }
       }
+      if (w == 7 && hh > 0 && want_dg) finish(hh - 1);
+      lds_barrier();
+
+      // Column v of R, values k of a block of 32: operands of dv.
+      float rk[NV * KB <= 4 ? NV : 1][KB][8];
+      auto load_column = [&](int n, int kb, float (&x)[8]) {
+        const int v = 16 * (vt + n) + r, k = 32 * kb + 8 * g;
+        const uint32_t off = v < p.vpad && k < p.kpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(R.load4(off + uint32_t(e * p.vpad) * 4u));
+      };
+      if constexpr (NV * KB <= 4) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) load_column(n, kb, rk[n][kb]);
+      }
+
+      // dq and dk of this wave's columns of dk.
+      float dots = 0.0f;  // <R, S> over them
+      float qs[TK], ks[TK];
+#pragma unroll
+      for (int i = 0; i < TK; ++i) qs[i] = ks[i] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const int k0 = 16 * (kt + n);
+        la_f32x4 xq[TK], xk[TK];
+#pragma unroll
+        for (int i = 0; i < TK; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
+#pragma unroll kUnroll
+        for (int vb = 0; vb < VB; ++vb) {
+          uint4 words[2][2];
+          if constexpr (kAhead) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              words[0][e] = fs[n][vb][e];
+              words[1][e] = fr[n][vb][e];
+            }
+          } else {
+            const uint32_t off = state_at(n, vb);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              words[0][e] = S.load16(off + 16u * e);
+              words[1][e] = R.load16(off + 16u * e);
+            }
+          }
+          float sv[8], rv[8];
+          widen_raw16<float>(words[0][0], sv);
+          widen_raw16<float>(words[0][1], sv + 4);
+          widen_raw16<float>(words[1][0], rv);
+          widen_raw16<float>(words[1][1], rv + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dots = __builtin_fmaf(sv[e], rv[e], dots);
+          Pieces<Elem, 3> ps, pr;
+          ps.split(sv);
+          pr.split(rv);
+#pragma unroll
+          for (int i = 0; i < TK; ++i) {
+            xq[i] = mma(ps, row_frag(sO, OP, 16 * (ik + i) + r, 32 * vb), xq[i]);
+            xk[i] = mma(pr, row_frag(sV, OP, 16 * (ik + i) + r, 32 * vb), xk[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TK; ++i) {
+          const int t = 16 * (ik + i) + r;
+          const float into = dec.into[t] * p.scale, onto = dec.onto[t];
+          const la_f32x4 qv = get4(&sQ[t * QP + k0 + 4 * g]), kv = get4(&sK[t * QP + k0 + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            xq[i][e] *= into;
+            xk[i][e] *= onto;
+            qs[i] = __builtin_fmaf(qv[e], xq[i][e], qs[i]);
+            ks[i] = __builtin_fmaf(kv[e], xk[i][e], ks[i]);
+            aq[n][i][e] += xq[i][e];
+            ak[n][i][e] += xk[i][e];
+          }
+        }
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) {
+          const Frag<Elem> kf = col_frag(sK, QP, 32 * sb, k0), qf = col_frag(sQ, QP, 32 * sb, k0);
+#pragma unroll
+          for (int i = 0; i < TK; ++i) {
+            if ((ik + i) / 2 >= sb) aq[n][i] = mma(kf, col_frag(sD, PP, 32 * sb, 16 * (ik + i)), aq[n][i]);
+            if ((ik + i) / 2 <= sb) ak[n][i] = mma(qf, row_frag(sD, PP, 16 * (ik + i) + r, 32 * sb), ak[n][i]);
+          }
+        }
+      }
+      // dv of this wave's columns of dv.
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int v0 = 16 * (vt + n);
+        la_f32x4 av[TV];
+#pragma unroll
+        for (int i = 0; i < TV; ++i) av[i] = la_f32x4{0, 0, 0, 0};
+#pragma unroll kUnroll
+        for (int kb = 0; kb < KB; ++kb) {
+          Pieces<Elem, 2> pr;
+          if constexpr (NV * KB <= 4) {
+            pr.split(rk[n][kb]);
+          } else {
+            float x[8];
+            load_column(n, kb, x);
+            pr.split(x);
+          }
+#pragma unroll
+          for (int i = 0; i < TV; ++i) av[i] = mma(pr, row_frag(sK, QP, 16 * (iv + i) + r, 32 * kb), av[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < TV; ++i) {
+          const float onto = dec.onto[16 * (iv + i) + r];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) av[i][e] *= onto;
+        }
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) {
+          const Frag<Elem> of = col_frag(sO, OP, 32 * sb, v0);
+#pragma unroll
+          for (int i = 0; i < TV; ++i)
+            if ((iv + i) / 2 <= sb) av[i] = mma(of, row_frag(sP, PP, 16 * (iv + i) + r, 32 * sb), av[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < TV; ++i) put(dv_of(h), v_step, iv + i, v0 + 4 * g, p.dv, av[i]);
+      }
+      if (want_dg) {
+#pragma unroll
+        for (int i = 0; i < TK; ++i) {
+          float a = qs[i], d = ks[i];
+          a += __shfl_xor(a, 16, 64);
+          a += __shfl_xor(a, 32, 64);
+          d += __shfl_xor(d, 16, 64);
+          d += __shfl_xor(d, 32, 64);
+          if (g == 0) {
+            part.qs[w][16 * (ik + i) + r] = a;
+            part.ks[w][16 * (ik + i) + r] = d;
+          }
+        }
+        dots = sum_lanes<6>(dots);
+        if (l == 0) {
+          part.x[w] = dots;
+          if (w == 0) part.total = dec.total;
+        }
+      }
+    }
+    if (want_dg) {
+      lds_barrier();
+      if (w == 7) finish(p.group - 1);
     }
   }
 #pragma unroll
   for (int n = 0; n < NK; ++n)
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      put(dq, q_step, i, 16 * (NK * w + n) + 4 * g, p.dk, aq[n][i]);
-      put(dk, q_step, i, 16 * (NK * w + n) + 4 * g, p.dk, ak[n][i]);
+    for (int i = 0; i < TK; ++i) {
+      put(dq, q_step, ik + i, 16 * (kt + n) + 4 * g, p.dk, aq[n][i]);
+      put(dk, q_step, ik + i, 16 * (kt + n) + 4 * g, p.dk, ak[n][i]);
     }
 }
 
@@ -348,7 +456,7 @@ __global__ __launch_bounds__(256) void linattn_dg_kernel(const float* sums, int6
 
 template <typename Elem, int KP, int VP>
 void run_bwd_kernel(const BwdParams& p, int64_t groups, bool whole, hipStream_t s) {
-  const dim3 grid{uint32_t(groups)}, block{kLaThreads};
+  const dim3 grid{uint32_t(groups)}, block{kBwdThreads};
   if (whole) hipLaunchKernelGGL((linattn_bwd_kernel<Elem, KP, VP, true>), grid, block, 0, s, p);
   else hipLaunchKernelGGL((linattn_bwd_kernel<Elem, KP, VP, false>), grid, block, 0, s, p);
 }
@@ -367,7 +475,7 @@ void run_bwd(const BwdParams& p, int64_t groups, bool whole, hipStream_t s) {
 int launch_linattn_bwd(const LinattnArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (launch_linattn_chunk_states(a, stream) != 0) return -1;
-  const int64_t c = linattn_chunk(a.io), chunks = (a.seqlen + c - 1) / c;
+  const int64_t c = linattn_bwd_chunk(a.io, a.dk, a.dv), chunks = (a.seqlen + c - 1) / c;
   const int64_t floats = linattn_state_floats(a.dk, a.dv), rows = a.batch * a.heads * chunks;
   BwdParams p{};
   p.q = a.q, p.k = a.k, p.v = a.v, p.dout = a.dout;

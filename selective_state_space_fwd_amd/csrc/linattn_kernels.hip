@@ -145,10 +145,13 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) a = mma(row_frag(sK, QP, 16 * j + r, 32 * kb), qf[kb], a);
         const int t = 16 * i + r, s0 = 16 * j + 4 * g;
-        const typename Decays<C>::Sum to = dec.sum[t];
+        float keep[4];
+        dec.between(t, s0, keep);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a[e] = s0 + e <= t ? a[e] * p.scale * Decays<C>::between(to, dec.sum[s0 + e]) : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          const float weight = a[e] * (p.scale * keep[e]);
+          a[e] = s0 + e <= t ? weight : 0.0f;
+        }
         put4(&sP[t * PP + s0], a);
       };
       {
@@ -280,7 +283,12 @@ struct StateParams {
   int xd, yd;
   bool reverse;
   float scale;
-  float* states;          // [batch, heads, segments, pad(yd), pad(xd)]
+  float* states;          // nullable: [batch, heads, segments, pad(yd), pad(xd)], what a segment adds
+  // Walked instead: from the state at the segment's start, the state before every chunk.
+  float* every;           // nullable: [batch, heads, chunks, pad(yd), pad(xd)]
+  const float* starts;    // nullable (one segment): as states, joined
+  const float* first;     // nullable: [batch, heads, xd, yd], the sequence's start, where starts is null
+  float* last;            // nullable: the same, behind the last chunk of the walk
 };
 
 struct StatesParams {
@@ -288,14 +296,14 @@ struct StatesParams {
   const float* g;
   int64_t g_batch, g_step, g_head;
   const int32_t* lengths;
-  float* totals;          // [batch, heads, segments]: log2 decay over the segment
+  float* totals;          // nullable: [batch, heads, segments]: log2 decay over the segment
   int64_t seqlen, chunks, per, segments, rows;  // rows = batch * heads * segments
   int heads, y_tiles;
 };
 
-template <typename Elem, int XP, int NY, bool kWhole>
+template <typename Elem, int C, int XP, int NY, bool kWhole>
 __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_kernel(StatesParams p) {
-  constexpr int C = chunk_of<Elem>(), SB = C / 32, YT = 64 * NY;
+  constexpr int SB = C / 32, YT = 64 * NY;
   constexpr int XPITCH = la_pitch<Elem>(XP), YPITCH = la_pitch<Elem>(YT);
   __shared__ __attribute__((aligned(16))) Elem sX[C * XPITCH], sY[C * YPITCH];
   __shared__ __attribute__((aligned(16))) Decays<C> decays[2];
@@ -319,11 +327,35 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
   const int64_t end = row_end(p.lengths, b, p.seqlen);
   const int64_t c0 = seg * p.per, c1 = c0 + p.per < p.chunks ? c0 + p.per : p.chunks, n = c1 - c0;
 
+  const int xpad = int(linattn_pad(d.xd, 32)), ypad = int(linattn_pad(d.yd, 32));
+  const int64_t floats = int64_t(xpad) * ypad, ext = (b * p.heads + h) * int64_t(d.xd) * d.yd;
+  // Tiles (2 j, m) and (2 j + 1, m): rows x = 32 j + 8 g + i and + 4 + i of column y0 + 16 (NY w + m) + r.
   la_f32x4 S[XP / 16][NY];
 #pragma unroll
   for (int j = 0; j < XP / 16; ++j)
 #pragma unroll
-    for (int m = 0; m < NY; ++m) S[j][m] = la_f32x4{0, 0, 0, 0};
+    for (int m = 0; m < NY; ++m) {
+      const int yc = y0 + 16 * (NY * w + m) + r, xr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
+      S[j][m] = la_f32x4{0, 0, 0, 0};
+      if (d.starts && yc < ypad && xr < xpad)
+        S[j][m] = *reinterpret_cast<const la_f32x4*>(d.starts + state * floats + int64_t(yc) * xpad + xr);
+      if (d.first && yc < d.yd) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (xr + e < d.xd) S[j][m][e] = d.first[ext + int64_t(xr + e) * d.yd + yc];
+      }
+    }
+  auto store = [&](float* to) {
+#pragma unroll
+    for (int m = 0; m < NY; ++m) {
+      const int yc = y0 + 16 * (NY * w + m) + r;
+      if (yc >= ypad) continue;
+#pragma unroll
+      for (int j = 0; j < XP / 16; ++j)
+        if (16 * j < xpad)
+          *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 32 * (j / 2) + 8 * g + 4 * (j % 2)) = S[j][m];
+    }
+  };
   double all = 0.0;
   TileLoad<Elem, C, XP, kWhole> lx;
   TileLoad<Elem, C, YT, kWhole> ly;
@@ -364,6 +396,7 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
     if (w == 0 && i + 1 < i1) all += decays[(i + 1) & 1].set(gate);
     fetch(i + 1);
     if (w == 0) gate = load_decay(gates, p.g_step, chunk(i + 2) * C, rows_of(i + 2));
+    if (d.every) store(d.every + ((b * p.heads + h) * p.chunks + chunk(i)) * floats);
     const float total = dec.total;
     Pieces<Elem, 3> add[SB][NY];
 #pragma unroll
@@ -397,18 +430,21 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
       }
     }
   }
-  const int xpad = int(linattn_pad(d.xd, 32)), ypad = int(linattn_pad(d.yd, 32));
-  float* to = d.states + state * (int64_t(xpad) * ypad);
+  if (d.states) store(d.states + state * floats);
+  if (p.totals && which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
+  if (d.last && seg == (d.reverse ? 0 : p.segments - 1)) {
 #pragma unroll
-  for (int m = 0; m < NY; ++m) {
-    const int yc = y0 + 16 * (NY * w + m) + r;
-    if (yc >= ypad) continue;
+    for (int m = 0; m < NY; ++m) {
+      const int yc = y0 + 16 * (NY * w + m) + r;
 #pragma unroll
-    for (int j = 0; j < XP / 16; ++j)
-      if (16 * j < xpad)
-        *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 32 * (j / 2) + 8 * g + 4 * (j % 2)) = S[j][m];
+      for (int j = 0; j < XP / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int xr = 32 * (j / 2) + 8 * g + 4 * (j % 2) + e;
+          if (yc < d.yd && xr < d.xd) d.last[ext + int64_t(xr) * d.yd + yc] = S[j][m][e];
+        }
+    }
   }
-  if (which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
 }
 
 // ---------------------------------------------------------------- the states at segments' starts
@@ -476,24 +512,32 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(JoinParams p) {
 
 // ---------------------------------------------------------------- launches
 
-template <typename Elem, int XP, int NY>
+template <typename Elem, int C, int XP, int NY>
 void run_states(const StatesParams& p, int dirs, bool whole, hipStream_t s) {
   const dim3 grid{uint32_t(p.rows * p.y_tiles * dirs)}, block{kLaThreads};
-  if (whole) hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((linattn_state_kernel<Elem, XP, NY, false>), grid, block, 0, s, p);
+  if (whole) hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, false>), grid, block, 0, s, p);
 }
 
-template <typename Elem>
-void run_states_of(StatesParams& p, int dirs, bool whole, hipStream_t s) {
-  const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = yd <= 64 || xd > 128 ? 1 : 2;
+template <typename Elem, int C>
+void run_states_of(StatesParams& p, int dirs, bool narrow, bool whole, hipStream_t s) {
+  const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = narrow || yd <= 64 || xd > 128 ? 1 : 2;
   p.y_tiles = (yd + 64 * ny - 1) / (64 * ny);
   if (ny == 1) {
-    if (xd <= 64) return run_states<Elem, 64, 1>(p, dirs, whole, s);
-    if (xd <= 128) return run_states<Elem, 128, 1>(p, dirs, whole, s);
-    return run_states<Elem, 256, 1>(p, dirs, whole, s);
+    if (xd <= 64) return run_states<Elem, C, 64, 1>(p, dirs, whole, s);
+    if (xd <= 128) return run_states<Elem, C, 128, 1>(p, dirs, whole, s);
+    return run_states<Elem, C, 256, 1>(p, dirs, whole, s);
   }
-  if (xd <= 64) return run_states<Elem, 64, 2>(p, dirs, whole, s);
-  run_states<Elem, 128, 2>(p, dirs, whole, s);
+  if (xd <= 64) return run_states<Elem, C, 64, 2>(p, dirs, whole, s);
+  run_states<Elem, C, 128, 2>(p, dirs, whole, s);
+}
+
+// Chunks of c steps; narrow: 64 columns a workgroup.
+int run_all_states(StatesParams& p, int dirs, Io io, int c, bool narrow, bool whole, hipStream_t s) {
+  if (io == Io::F32) run_states_of<float, 32>(p, dirs, narrow, whole, s);
+  else if (c == 64) run_states_of<uint16_t, 64>(p, dirs, narrow, whole, s);
+  else run_states_of<uint16_t, 32>(p, dirs, narrow, whole, s);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 template <typename Elem, int KP, int NV>
@@ -516,41 +560,81 @@ void run_fwd(const FwdParams& p, int64_t groups, bool whole, hipStream_t s) {
 
 }  // namespace
 
-// Both directions' states of every chunk, for the backward, as [dk][dv]; then the states at the
-// chunks' starts and the adjoints behind them. Workspace: states, adjoints, totals.
+// Both directions' states of every chunk, for the backward, as [dk][dv]: the states at the chunks'
+// starts and the adjoints behind them (linattn_bwd_states says how and where).
 int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t c = linattn_chunk(a.io), chunks = (a.seqlen + c - 1) / c;
-  const int64_t floats = linattn_state_floats(a.dk, a.dv), rows = a.batch * a.heads * chunks;
-  const int group = int(a.heads / a.qk_heads);
+  const LinattnBwdStates st = linattn_bwd_states(a.batch, a.heads, a.dk, a.dv, a.seqlen, a.io);
+  const int c = linattn_bwd_chunk(a.io, a.dk, a.dv), group = int(a.heads / a.qk_heads);
   const bool whole = linattn_whole(a, true);
-  float* adjoints = a.workspace + rows * floats;
+  float *states = a.workspace, *adjoints = states + st.chunk_rows * st.floats;
+  if (a.batch == 0) return 0;
   StatesParams p{};
-  p.dir[0] = StateParams{a.v, a.k, 1, group, int(a.dv), int(a.dk), false, 1.0f, a.workspace};
-  p.dir[1] = StateParams{a.dout, a.q, 1, group, int(a.dv), int(a.dk), true, a.scale, adjoints};
   p.g = a.g;
   p.g_batch = a.g_batch, p.g_step = a.g_step, p.g_head = a.g_head;
   p.lengths = a.lengths;
-  p.totals = adjoints + rows * floats;
-  p.seqlen = a.seqlen, p.chunks = chunks, p.per = 1, p.segments = chunks, p.rows = rows;
-  p.heads = int(a.heads);
-  if (chunks > 0) {
-    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 2, whole, s);
-    else run_states_of<float>(p, 2, whole, s);
-    if (hipGetLastError() != hipSuccess) return -1;
-  }
+  p.seqlen = a.seqlen, p.chunks = st.chunks, p.heads = int(a.heads);
+  auto dir = [&](bool reverse) {
+    StateParams d{};
+    d.x = reverse ? a.dout : a.v;
+    d.y = reverse ? a.q : a.k;
+    d.x_group = 1, d.y_group = group;
+    d.xd = int(a.dv), d.yd = int(a.dk);
+    d.reverse = reverse;
+    d.scale = reverse ? a.scale : 1.0f;
+    return d;
+  };
   JoinParams j{};
-  j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
-  j.dir[1] = JoinDir{adjoints, a.dfinal, a.dinitial, true};
-  j.totals = p.totals;
-  j.segments = chunks, j.state_floats = floats;
+  j.state_floats = st.floats;
   j.cols = int(linattn_pad(a.dv, 32));
   j.row_count = int(a.dk), j.col_count = int(a.dv);
   j.row_stride = 1, j.col_stride = a.dk, j.ext_floats = a.dk * a.dv;
-  j.blocks = linattn_join_blocks(floats);
-  if (a.batch == 0) return 0;
-  hipLaunchKernelGGL(linattn_join_kernel, dim3(uint32_t(j.blocks * a.batch * a.heads), 2), dim3(256), 0, s, j);
-  return hipGetLastError() == hipSuccess ? 0 : -1;
+  j.blocks = linattn_join_blocks(st.floats);
+  auto join = [&] {
+    hipLaunchKernelGGL(linattn_join_kernel, dim3(uint32_t(j.blocks * a.batch * a.heads), 2), dim3(256), 0, s, j);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+  };
+  // What each chunk, or segment, adds to the states: into `local`, the adjoints behind the states.
+  auto add = [&](int64_t per, int64_t count, float* local, float* totals) {
+    p.dir[0] = dir(false), p.dir[1] = dir(true);
+    p.rows = a.batch * a.heads * count;
+    p.per = per, p.segments = count;
+    p.dir[0].states = local, p.dir[1].states = local + p.rows * st.floats;
+    p.totals = totals;
+    return run_all_states(p, 2, a.io, c, per > 1, whole, s);
+  };
+  if (!st.walked) {
+    float* totals = adjoints + st.chunk_rows * st.floats;
+    if (st.chunks > 0 && add(1, st.chunks, states, totals) != 0) return -1;
+    j.totals = totals, j.segments = st.chunks;
+    j.dir[0] = JoinDir{states, a.initial, nullptr, false};
+    j.dir[1] = JoinDir{adjoints, a.dfinal, a.dinitial, true};
+    return join();
+  }
+  const int64_t per = st.segments.per, count = st.segments.count;
+  float* local = states + st.chunk_rows * (2 * st.floats + 4);
+  if (count > 1) {
+    float* totals = local + 2 * st.segment_rows * st.floats;
+    if (add(per, count, local, totals) != 0) return -1;
+    j.totals = totals, j.segments = count;
+    j.dir[0] = JoinDir{local, a.initial, nullptr, false};
+    j.dir[1] = JoinDir{local + st.segment_rows * st.floats, a.dfinal, nullptr, true};
+    if (join() != 0) return -1;
+  }
+  p.dir[0] = dir(false), p.dir[1] = dir(true);
+  p.rows = a.batch * a.heads * count;
+  p.per = per, p.segments = count;
+  p.totals = nullptr;
+  p.dir[0].every = states, p.dir[1].every = adjoints;
+  if (count > 1) {
+    p.dir[0].starts = local;
+    p.dir[1].starts = local + st.segment_rows * st.floats;
+  } else {
+    p.dir[0].first = a.initial;
+    p.dir[1].first = a.dfinal;
+  }
+  p.dir[1].last = a.dinitial;
+  return run_all_states(p, 2, a.io, c, true, whole, s);
 }
 
 int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
@@ -561,16 +645,15 @@ int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
   const bool whole = linattn_whole(a, false);
   if (seg.count > 1) {
     StatesParams p{};
-    p.dir[0] = StateParams{a.k, a.v, group, 1, int(a.dk), int(a.dv), false, 1.0f, a.workspace};
+    p.dir[0] = StateParams{a.k, a.v, group, 1, int(a.dk), int(a.dv), false, 1.0f, a.workspace,
+                           nullptr, nullptr, nullptr, nullptr};
     p.g = a.g;
     p.g_batch = a.g_batch, p.g_step = a.g_step, p.g_head = a.g_head;
     p.lengths = a.lengths;
     p.totals = a.workspace + rows * floats;
     p.seqlen = a.seqlen, p.chunks = seg.chunks, p.per = seg.per, p.segments = seg.count, p.rows = rows;
     p.heads = int(a.heads);
-    if (a.io == Io::BF16) run_states_of<uint16_t>(p, 1, whole, s);
-    else run_states_of<float>(p, 1, whole, s);
-    if (hipGetLastError() != hipSuccess) return -1;
+    if (run_all_states(p, 1, a.io, linattn_chunk(a.io), false, whole, s) != 0) return -1;
     JoinParams j{};
     j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
     j.totals = p.totals;

@@ -7,10 +7,19 @@
 
 namespace ssm {
 
+#ifndef LAT
+#define LAB (64 << 20)
+#define LAT 384
+#define LAW 512
+#endif
 constexpr int kLinattnMaxDim = 256;  // dk and dv
 
 // Steps of a chunk: 64, or 32 in fp32, whose tiles would not fit LDS at 256 columns otherwise.
 constexpr int linattn_chunk(Io io) { return io == Io::BF16 ? 64 : 32; }
+// The backward, whose four tiles and two of weights share LDS, takes 32 above 128 columns.
+constexpr int linattn_bwd_chunk(Io io, int64_t dk, int64_t dv) {
+  return io == Io::BF16 && dk <= 128 && dv <= 128 ? 64 : 32;
+}
 
 // A [batch, seqlen, heads, dim] array whose last axis is contiguous; element strides.
 struct HeadRows {
@@ -60,7 +69,7 @@ inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk
   const int64_t c = linattn_chunk(io);
   s.chunks = (seqlen + c - 1) / c;
   const int64_t base = batch * heads * linattn_value_tiles(dk, dv);
-  int64_t want = base > 0 && base < 384 ? (512 + base - 1) / base : 1;
+  int64_t want = base > 0 && base < LAT ? (LAW + base - 1) / base : 1;
   if (want > s.chunks) want = s.chunks;
   s.per = want > 0 ? (s.chunks + want - 1) / want : 1;
   s.count = s.chunks > 0 ? (s.chunks + s.per - 1) / s.per : 1;
@@ -71,6 +80,39 @@ inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk
 // reads stay inside.
 inline int64_t linattn_state_floats(int64_t rows, int64_t cols) {
   return linattn_pad(rows, 32) * linattn_pad(cols, 32);
+}
+
+// The backward's states of every chunk. Walked: a workgroup of 64 columns of dk walks the chunks of a
+// segment and leaves the state of each, from the segment's start, which is the sequence's, or is
+// found by a first walk that leaves segments' states alone and the join. Else every chunk by
+// itself, and the join over the chunks (all of them read and written once more), where they are
+// few enough to stay in the caches.
+struct LinattnBwdStates {
+  bool walked;
+  LinattnSegments segments;  // of the walk
+  int64_t chunks, floats;
+  // Workspace: states, adjoints, decays and dg sums of the chunks, then the same of the segments, in
+  // floats (two more a row than those, to keep the states 16-byte aligned).
+  int64_t chunk_rows, segment_rows, total;
+};
+inline LinattnBwdStates linattn_bwd_states(int64_t batch, int64_t heads, int64_t dk, int64_t dv, int64_t seqlen, Io io) {
+  LinattnBwdStates s{};
+  const int64_t c = linattn_bwd_chunk(io, dk, dv);
+  s.chunks = (seqlen + c - 1) / c;
+  s.floats = linattn_state_floats(dk, dv);
+  s.chunk_rows = batch * heads * s.chunks;
+  s.walked = double(s.chunk_rows) * double(s.floats) * 8.0 > double(LAB);
+  s.segments = LinattnSegments{s.chunks, s.chunks, 1};
+  if (s.walked) {
+    const int64_t base = batch * heads * 2 * ((dk + 63) / 64);
+    int64_t want = base < 384 ? (512 + base - 1) / base : 1;
+    if (want > s.chunks) want = s.chunks;
+    s.segments.per = (s.chunks + want - 1) / want;
+    s.segments.count = (s.chunks + s.segments.per - 1) / s.segments.per;
+  }
+  s.segment_rows = s.segments.count > 1 ? batch * heads * s.segments.count : 0;
+  s.total = (s.chunk_rows + s.segment_rows) * (2 * s.floats + 4);
+  return s;
 }
 
 inline int64_t linattn_join_blocks(int64_t state_floats) { return (state_floats / 4 + 255) / 256; }

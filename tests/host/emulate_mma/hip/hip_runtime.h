@@ -119,7 +119,7 @@ inline void launch(dim3 grid, dim3 block, std::function<void()> kernel) {
       for (int w = 0; w < n / 64; ++w) wave_meets[w] = Meeting{64};
       for (int t = 0; t < n; ++t) {
         done[t] = 0;
-        stacks[t].resize(256 << 10);
+        stacks[t].resize(1 << 20);
         getcontext(&fibers[t]);
         fibers[t].uc_stack.ss_sp = stacks[t].data();
         fibers[t].uc_stack.ss_size = stacks[t].size();
