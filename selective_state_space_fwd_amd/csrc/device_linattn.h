@@ -310,10 +310,10 @@ struct Decays {
   float onto[C];  // from s to the chunk's end
   float total;    // over the chunk
 
-  // Lane t < C of one wave holds the step's log2 decay (0 behind the end). Returns the sum.
-  __device__ __forceinline__ double set(double step) {
+  // Lane t < C of one wave holds the step's log decay (0 behind the end). Returns the log2 sum.
+  __device__ __forceinline__ double set(float step) {
     const int l = threadIdx.x & 63;
-    const double cs = wave_prefix_f64(step), all = dpp_f64(cs, C - 1);
+    const double cs = wave_prefix_f64(log2_decay(step)), all = dpp_f64(cs, C - 1);
     if (l < C) {
       const float h = float(cs);
       sum[l] = Sum{h, float(cs - double(h))};
@@ -344,10 +344,12 @@ struct Decays {
   }
 };
 
-// The log2 decay of step t0 + lane, 0 at and past `rows` (nothing there is read).
-__device__ __forceinline__ double load_decay(const float* g, int64_t step, int64_t t0, int rows) {
+// The log decay of step t0 + lane, 0 at and past `rows` and without g (nothing there is read). A load
+// without a branch, by every wave: a later wait for an older load can then leave it in flight.
+__device__ __forceinline__ float load_decay(const float* g, int64_t step, int64_t t0, int rows, int64_t from = 0) {
   const int l = threadIdx.x & 63;
-  return g && l < rows ? log2_decay(g[(t0 + l) * step]) : 0.0;
+  const Buf b(g + t0 * step + from, kLaBytes);
+  return __uint_as_float(b.load4(g && l < rows ? uint32_t(l) * uint32_t(step) * 4u : kLaOob));
 }
 
 __device__ __forceinline__ int64_t row_end(const int32_t* lengths, int64_t b, int64_t seqlen) {

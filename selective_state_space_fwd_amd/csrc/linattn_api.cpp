@@ -77,7 +77,7 @@ bool grids_fit(const Sizes& z, bool bwd) {
 bool steps_fit(const Sizes& z, const ssm::LinattnArgs& a) {
   for (int64_t step : {a.q.step, a.k.step, a.v.step, a.dout.step, z.heads * z.dv, z.qk_heads * z.dk})
     if (!ssm::linattn_reach(step, z.esz)) return false;
-  return true;
+  return ssm::linattn_reach(a.g_step, 4);
 }
 
 int64_t fwd_workspace(const Sizes& z) {

@@ -150,8 +150,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
               uint32_t(p.dout.step) * E, n, p.dv);
     };
     auto gate_of = [&](int hh) {
-      return load_decay(p.g && hh < p.group ? p.g + b * p.g_batch + (hk * p.group + hh) * p.g_head : nullptr, p.g_step,
-                        t0, live);
+      return load_decay(p.g ? p.g + b * p.g_batch + int64_t(hk) * p.group * p.g_head : nullptr, p.g_step, t0,
+                        hh < p.group ? live : 0, int64_t(hh < p.group ? hh : 0) * p.g_head);
     };
     // dg of the head whose parts lie in parts[hh & 1], by one wave.
     auto finish = [&](int hh) {
@@ -183,12 +183,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
     };
     const bool want_dg = p.dg || p.dg_sums;
 
-    double gate = 0.0;
-    if (w == 6) {
-      gate = gate_of(0);
-      const double next = gate_of(1);
-      decays[0].set(gate);
-      gate = next;
+    float gate = gate_of(1);
+    {
+      const float first = gate_of(0);
+      if (w == 6) decays[0].set(first);
     }
     {
       TileLoad<Elem, C, KP, kWhole, kBwdThreads> lq, lk;
@@ -241,8 +239,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
             }
           }
       }
+      gate = gate_of(hh + 2);
       fetch(hh + 1);
-      if (w == 6) gate = gate_of(hh + 2);
 
       // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
       const BwdTiles mine = bwd_tiles<C>(w);

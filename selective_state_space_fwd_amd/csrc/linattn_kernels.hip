@@ -113,12 +113,10 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
     lv.load(v + t0 * p.v.step, uint32_t(p.v.step) * E, rows, v_left);
   };
   // The last wave, with the fewest tiles of pairs, forms each chunk's decays a chunk ahead.
-  double gate = 0.0;
-  if (w == 3) {
-    gate = load_decay(gates, p.g_step, c0 * C, rows_of(c0));
-    const double next = load_decay(gates, p.g_step, (c0 + 1) * C, rows_of(c0 + 1));
-    decays[c0 & 1].set(gate);
-    gate = next;
+  float gate = load_decay(gates, p.g_step, (c0 + 1) * C, rows_of(c0 + 1));
+  {
+    const float first = load_decay(gates, p.g_step, c0 * C, rows_of(c0));
+    if (w == 3) decays[c0 & 1].set(first);
   }
   fetch(c0);
   for (int64_t c = c0; c < c1; ++c) {
@@ -135,8 +133,8 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
       lds_barrier();
       // (ahead of the loads for the next chunk, which it would wait for)
       if (w == 3) decays[(c + 1) & 1].set(gate);
+      gate = load_decay(gates, p.g_step, (c + 2) * C, rows_of(c + 2));
       fetch(c + 1);
-      if (w == 3) gate = load_decay(gates, p.g_step, (c + 2) * C, rows_of(c + 2));
       // The weights of the pairs s <= t, with the decay between them: tile (i, j) as rows s of
       // columns t, stored by rows t.
       const WaveTiles mine = wave_tiles<C>(w);
@@ -283,9 +281,9 @@ struct StateParams {
   int xd, yd;
   bool reverse;
   float scale;
-  float* states;          // nullable: [batch, heads, segments, pad(yd), pad(xd)], what a segment adds
+  float* states;          // [batch, heads, segments, pad(yd), pad(xd)], what a segment adds
   // Walked instead: from the state at the segment's start, the state before every chunk.
-  float* every;           // nullable: [batch, heads, chunks, pad(yd), pad(xd)]
+  float* every;           // [batch, heads, chunks, pad(yd), pad(xd)]
   const float* starts;    // nullable (one segment): as states, joined
   const float* first;     // nullable: [batch, heads, xd, yd], the sequence's start, where starts is null
   float* last;            // nullable: the same, behind the last chunk of the walk
@@ -296,12 +294,13 @@ struct StatesParams {
   const float* g;
   int64_t g_batch, g_step, g_head;
   const int32_t* lengths;
-  float* totals;          // nullable: [batch, heads, segments]: log2 decay over the segment
+  float* totals;          // [batch, heads, segments]: log2 decay over the segment (not walked)
   int64_t seqlen, chunks, per, segments, rows;  // rows = batch * heads * segments
   int heads, y_tiles;
 };
 
-template <typename Elem, int C, int XP, int NY, bool kWhole>
+// kWalk: leave the state before every chunk.
+template <typename Elem, int C, int XP, int NY, bool kWhole, bool kWalk>
 __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_kernel(StatesParams p) {
   constexpr int SB = C / 32, YT = 64 * NY;
   constexpr int XPITCH = la_pitch<Elem>(XP), YPITCH = la_pitch<Elem>(YT);
@@ -337,28 +336,33 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
     for (int m = 0; m < NY; ++m) {
       const int yc = y0 + 16 * (NY * w + m) + r, xr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
       S[j][m] = la_f32x4{0, 0, 0, 0};
-      if (d.starts && yc < ypad && xr < xpad)
-        S[j][m] = *reinterpret_cast<const la_f32x4*>(d.starts + state * floats + int64_t(yc) * xpad + xr);
-      if (d.first && yc < d.yd) {
+      if constexpr (kWalk) {
+        if (d.starts && yc < ypad && xr < xpad)
+          S[j][m] = *reinterpret_cast<const la_f32x4*>(d.starts + state * floats + int64_t(yc) * xpad + xr);
+        if (d.first && yc < d.yd) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (xr + e < d.xd) S[j][m][e] = d.first[ext + int64_t(xr + e) * d.yd + yc];
+          for (int e = 0; e < 4; ++e)
+            if (xr + e < d.xd) S[j][m][e] = d.first[ext + int64_t(xr + e) * d.yd + yc];
+        }
       }
     }
-  auto store = [&](float* to) {
+  // (without branches, so that the loads of the next chunk can be waited for without these)
+  auto store = [&](float* base) {
+    const Buf to(base, uint32_t(floats) * 4);
 #pragma unroll
     for (int m = 0; m < NY; ++m) {
       const int yc = y0 + 16 * (NY * w + m) + r;
-      if (yc >= ypad) continue;
 #pragma unroll
-      for (int j = 0; j < XP / 16; ++j)
-        if (16 * j < xpad)
-          *reinterpret_cast<la_f32x4*>(to + int64_t(yc) * xpad + 32 * (j / 2) + 8 * g + 4 * (j % 2)) = S[j][m];
+      for (int j = 0; j < XP / 16; ++j) {
+        const int xr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
+        to.store16(__builtin_bit_cast(uint4, S[j][m]), yc < ypad && xr < xpad ? uint32_t(yc * xpad + xr) * 4u : kLaOob);
+      }
     }
   };
   double all = 0.0;
-  TileLoad<Elem, C, XP, kWhole> lx;
-  TileLoad<Elem, C, YT, kWhole> ly;
+  // Two chunks on their way at a time: a chunk takes less time than memory to answer.
+  TileLoad<Elem, C, XP, kWhole> lx[2];
+  TileLoad<Elem, C, YT, kWhole> ly[2];
   constexpr uint32_t E = sizeof(Elem);
   const int y_left = d.yd - y0 < YT ? d.yd - y0 : YT;
   auto chunk = [&](int64_t i) { return d.reverse ? c1 - 1 - i : c0 + i; };
@@ -366,11 +370,15 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
     const int64_t left = i < n ? end - chunk(i) * C : 0;
     return left < 0 ? 0 : left < C ? int(left) : C;
   };
-  auto fetch = [&](int64_t i) {
+  auto fetch = [&](int64_t i, int set) {
     const int64_t t0 = chunk(i) * C;
     const int rows = rows_of(i);
-    lx.load(x + (rows ? t0 : 0) * d.x.step, uint32_t(d.x.step) * E, rows, d.xd);
-    ly.load(y + (rows ? t0 : 0) * d.y.step, uint32_t(d.y.step) * E, rows, y_left);
+    lx[set].load(x + (rows ? t0 : 0) * d.x.step, uint32_t(d.x.step) * E, rows, d.xd);
+    ly[set].load(y + (rows ? t0 : 0) * d.y.step, uint32_t(d.y.step) * E, rows, y_left);
+  };
+  auto gate_of = [&](int64_t i) {
+    const int rows = rows_of(i);
+    return load_decay(gates, p.g_step, rows ? chunk(i) * C : 0, rows);
   };
   // Chunks behind the row's end leave the state as it is: the first of a reverse walk.
   int64_t i0 = 0, i1 = n;
@@ -378,25 +386,24 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
     while (i0 < n && rows_of(i0) == 0) ++i0;
   else
     while (i1 > 0 && rows_of(i1 - 1) == 0) --i1;
-  fetch(i0);
-  double gate = 0.0;
-  if (w == 0 && i0 < i1) {
-    gate = load_decay(gates, p.g_step, chunk(i0) * C, rows_of(i0));
-    const double next = load_decay(gates, p.g_step, chunk(i0 + 1) * C, rows_of(i0 + 1));
-    all = decays[i0 & 1].set(gate);
-    gate = next;
+  float gate = gate_of(i0 + 1);
+  {
+    const float first = gate_of(i0);
+    if (w == 0 && i0 < i1) all = decays[i0 & 1].set(first);
   }
-  for (int64_t i = i0; i < i1; ++i) {
+  fetch(i0, 0);
+  fetch(i0 + 1, 1);
+  auto step = [&](int64_t i, int set) {
     const Decays<C>& dec = decays[i & 1];
     lds_barrier();
-    lx.store(sX);
-    ly.store(sY);
+    lx[set].store(sX);
+    ly[set].store(sY);
     lds_barrier();
-    // (ahead of the loads for the next chunk, which it would wait for)
+    // (ahead of the loads for the chunk after the next, which it would wait for)
     if (w == 0 && i + 1 < i1) all += decays[(i + 1) & 1].set(gate);
-    fetch(i + 1);
-    if (w == 0) gate = load_decay(gates, p.g_step, chunk(i + 2) * C, rows_of(i + 2));
-    if (d.every) store(d.every + ((b * p.heads + h) * p.chunks + chunk(i)) * floats);
+    gate = gate_of(i + 2);
+    fetch(i + 2, set);
+    if constexpr (kWalk) store(d.every + ((b * p.heads + h) * p.chunks + chunk(i)) * floats);
     const float total = dec.total;
     Pieces<Elem, 3> add[SB][NY];
 #pragma unroll
@@ -429,10 +436,14 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
         for (int m = 0; m < NY; ++m) S[j][m] = mma(f, add[sb][m], S[j][m]);
       }
     }
+  };
+  for (int64_t i = i0; i < i1; i += 2) {
+    step(i, 0);
+    if (i + 1 < i1) step(i + 1, 1);
   }
-  if (d.states) store(d.states + state * floats);
-  if (p.totals && which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
-  if (d.last && seg == (d.reverse ? 0 : p.segments - 1)) {
+  if constexpr (!kWalk) store(d.states + state * floats);
+  if (!kWalk && which == 0 && yt == 0 && threadIdx.x == 0) p.totals[state] = float(all);
+  if (kWalk && d.last && seg == (d.reverse ? 0 : p.segments - 1)) {
 #pragma unroll
     for (int m = 0; m < NY; ++m) {
       const int yc = y0 + 16 * (NY * w + m) + r;
@@ -512,31 +523,36 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(JoinParams p) {
 
 // ---------------------------------------------------------------- launches
 
-template <typename Elem, int C, int XP, int NY>
+template <typename Elem, int C, int XP, int NY, bool kWalk>
 void run_states(const StatesParams& p, int dirs, bool whole, hipStream_t s) {
   const dim3 grid{uint32_t(p.rows * p.y_tiles * dirs)}, block{kLaThreads};
-  if (whole) hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, false>), grid, block, 0, s, p);
+  if (whole) hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, true, kWalk>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((linattn_state_kernel<Elem, C, XP, NY, false, kWalk>), grid, block, 0, s, p);
 }
 
-template <typename Elem, int C>
-void run_states_of(StatesParams& p, int dirs, bool narrow, bool whole, hipStream_t s) {
-  const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = narrow || yd <= 64 || xd > 128 ? 1 : 2;
+// 64 columns a workgroup where the state is walked (more workgroups) or has more than 128 rows (for want
+// of registers), else up to 128.
+template <typename Elem, int C, bool kWalk>
+void run_states_of(StatesParams& p, int dirs, bool whole, hipStream_t s) {
+  const int xd = p.dir[0].xd, yd = p.dir[0].yd, ny = kWalk || (p.per > 1 && dirs > 1) || yd <= 64 || xd > 128 ? 1 : 2;
   p.y_tiles = (yd + 64 * ny - 1) / (64 * ny);
   if (ny == 1) {
-    if (xd <= 64) return run_states<Elem, C, 64, 1>(p, dirs, whole, s);
-    if (xd <= 128) return run_states<Elem, C, 128, 1>(p, dirs, whole, s);
-    return run_states<Elem, C, 256, 1>(p, dirs, whole, s);
+    if (xd <= 64) return run_states<Elem, C, 64, 1, kWalk>(p, dirs, whole, s);
+    if (xd <= 128) return run_states<Elem, C, 128, 1, kWalk>(p, dirs, whole, s);
+    return run_states<Elem, C, 256, 1, kWalk>(p, dirs, whole, s);
   }
-  if (xd <= 64) return run_states<Elem, C, 64, 2>(p, dirs, whole, s);
-  run_states<Elem, C, 128, 2>(p, dirs, whole, s);
+  if constexpr (!kWalk) {
+    if (xd <= 64) return run_states<Elem, C, 64, 2, false>(p, dirs, whole, s);
+    run_states<Elem, C, 128, 2, false>(p, dirs, whole, s);
+  }
 }
 
-// Chunks of c steps; narrow: 64 columns a workgroup.
-int run_all_states(StatesParams& p, int dirs, Io io, int c, bool narrow, bool whole, hipStream_t s) {
-  if (io == Io::F32) run_states_of<float, 32>(p, dirs, narrow, whole, s);
-  else if (c == 64) run_states_of<uint16_t, 64>(p, dirs, narrow, whole, s);
-  else run_states_of<uint16_t, 32>(p, dirs, narrow, whole, s);
+// Chunks of c steps.
+template <bool kWalk>
+int run_all_states(StatesParams& p, int dirs, Io io, int c, bool whole, hipStream_t s) {
+  if (io == Io::F32) run_states_of<float, 32, kWalk>(p, dirs, whole, s);
+  else if (c == 64) run_states_of<uint16_t, 64, kWalk>(p, dirs, whole, s);
+  else run_states_of<uint16_t, 32, kWalk>(p, dirs, whole, s);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -601,7 +617,7 @@ int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
     p.per = per, p.segments = count;
     p.dir[0].states = local, p.dir[1].states = local + p.rows * st.floats;
     p.totals = totals;
-    return run_all_states(p, 2, a.io, c, per > 1, whole, s);
+    return run_all_states<false>(p, 2, a.io, c, whole, s);
   };
   if (!st.walked) {
     float* totals = adjoints + st.chunk_rows * st.floats;
@@ -634,7 +650,7 @@ int launch_linattn_chunk_states(const LinattnArgs& a, void* stream) {
     p.dir[1].first = a.dfinal;
   }
   p.dir[1].last = a.dinitial;
-  return run_all_states(p, 2, a.io, c, true, whole, s);
+  return run_all_states<true>(p, 2, a.io, c, whole, s);
 }
 
 int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
@@ -653,7 +669,7 @@ int launch_linattn_fwd(const LinattnArgs& a, void* stream) {
     p.totals = a.workspace + rows * floats;
     p.seqlen = a.seqlen, p.chunks = seg.chunks, p.per = seg.per, p.segments = seg.count, p.rows = rows;
     p.heads = int(a.heads);
-    if (run_all_states(p, 1, a.io, linattn_chunk(a.io), false, whole, s) != 0) return -1;
+    if (run_all_states<false>(p, 1, a.io, linattn_chunk(a.io), whole, s) != 0) return -1;
     JoinParams j{};
     j.dir[0] = JoinDir{a.workspace, a.initial, nullptr, false};
     j.totals = p.totals;
