@@ -63,6 +63,7 @@ template <typename Elem, int N>
 struct Pieces;
 template <int N>
 struct Pieces<uint16_t, N> {
+  static constexpr int kCount = N;
   Frag<uint16_t> f[N];
   __device__ __forceinline__ void split(const float (&x)[8]) {
     float rest[8];
@@ -83,6 +84,7 @@ struct Pieces<uint16_t, N> {
 };
 template <int N>
 struct Pieces<float, N> {
+  static constexpr int kCount = 1;
   Frag<float> f;
   __device__ __forceinline__ void split(const float (&x)[8]) {
 #pragma unroll
@@ -90,25 +92,14 @@ struct Pieces<float, N> {
   }
 };
 
+// Piece p of kCount.
 template <int N>
-__device__ __forceinline__ la_f32x4 mma(const Pieces<uint16_t, N>& a, const Frag<uint16_t>& b, la_f32x4 c) {
-#pragma unroll
-  for (int p = N - 1; p >= 0; --p) c = mma(a.f[p], b, c);  // the small ones first
-  return c;
+__device__ __forceinline__ const Frag<uint16_t>& piece(const Pieces<uint16_t, N>& a, int p) {
+  return a.f[p];
 }
 template <int N>
-__device__ __forceinline__ la_f32x4 mma(const Pieces<float, N>& a, const Frag<float>& b, la_f32x4 c) {
-  return mma(a.f, b, c);
-}
-template <int N>
-__device__ __forceinline__ la_f32x4 mma(const Frag<uint16_t>& a, const Pieces<uint16_t, N>& b, la_f32x4 c) {
-#pragma unroll
-  for (int p = N - 1; p >= 0; --p) c = mma(a, b.f[p], c);
-  return c;
-}
-template <int N>
-__device__ __forceinline__ la_f32x4 mma(const Frag<float>& a, const Pieces<float, N>& b, la_f32x4 c) {
-  return mma(a, b.f, c);
+__device__ __forceinline__ const Frag<float>& piece(const Pieces<float, N>& a, int) {
+  return a.f;
 }
 
 __device__ __forceinline__ void widen_frag(const Frag<uint16_t>& f, float (&v)[8]) {

@@ -91,8 +91,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   constexpr bool kHalfK = KP < 128, kHalfV = VP < 128;
   constexpr int NK = kHalfK ? 1 : KP / 128, NV = kHalfV ? 1 : VP / 128;
   constexpr int TK = kHalfK ? T / 2 : T, TV = kHalfV ? T / 2 : T;
-  // The states' operands are loaded ahead of the pairs where they fit in registers.
-  constexpr bool kAhead = NK * VB <= 4;
+  // The states' operands are loaded ahead of the pairs where registers are left for them (b4 8 heads of
+  // 128 for 32 of 64, 2048 steps: 147 us against 155); 128 x 128 keeps them out of its way (16384
+  // steps of 16 heads: 385 against 441, with spills).
+  constexpr bool kAhead = NK * VB <= 2;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
   __shared__ __attribute__((aligned(16))) Elem sP[C * PP], sD[C * PP];  // weights by rows s: scale D qk, scale D dov
@@ -291,12 +293,6 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(R.load4(off + uint32_t(e * p.vpad) * 4u));
       };
-      if constexpr (NV * KB <= 4) {
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) load_column(n, kb, rk[n][kb]);
-      }
 
       // dq and dk of this wave's columns of dk.
       float dots = 0.0f;  // <R, S> over them
@@ -338,9 +334,21 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           pr.split(rv);
 #pragma unroll
           for (int i = 0; i < TK; ++i) {
-            xq[i] = mma(ps, row_frag(sO, OP, 16 * (ik + i) + r, 32 * vb), xq[i]);
-            xk[i] = mma(pr, row_frag(sV, OP, 16 * (ik + i) + r, 32 * vb), xk[i]);
+            const Frag<Elem> fo = row_frag(sO, OP, 16 * (ik + i) + r, 32 * vb),
+                             fv = row_frag(sV, OP, 16 * (ik + i) + r, 32 * vb);
+#pragma unroll
+            for (int e = ps.kCount - 1; e >= 0; --e) {  // the small ones first, the two sums in turn
+              xq[i] = mma(piece(ps, e), fo, xq[i]);
+              xk[i] = mma(piece(pr, e), fv, xk[i]);
+            }
           }
+        }
+        // (by now the states' registers are free again)
+        if (NV * KB <= 4 && n == NK - 1) {
+#pragma unroll
+          for (int m = 0; m < NV; ++m)
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) load_column(m, kb, rk[NV * KB <= 4 ? m : 0][kb]);
         }
 #pragma unroll
         for (int i = 0; i < TK; ++i) {
@@ -385,7 +393,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
             pr.split(x);
           }
 #pragma unroll
-          for (int i = 0; i < TV; ++i) av[i] = mma(pr, row_frag(sK, QP, 16 * (iv + i) + r, 32 * kb), av[i]);
+          for (int i = 0; i < TV; ++i) {
+            const Frag<Elem> fk = row_frag(sK, QP, 16 * (iv + i) + r, 32 * kb);
+#pragma unroll
+            for (int e = pr.kCount - 1; e >= 0; --e) av[i] = mma(piece(pr, e), fk, av[i]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < TV; ++i) {

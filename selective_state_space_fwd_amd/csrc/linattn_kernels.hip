@@ -168,46 +168,59 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
       for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int n = 0; n < NV; ++n) vf[sb][n] = col_frag(sV, VP, 32 * sb, 16 * (NV * w + n));
-      Pieces<Elem, 2> sp[KB][NV];
+      // Results as rows v of columns t: through the state first. Products of different sums follow each
+      // other, so that none waits for the one before.
+      la_f32x4 o[T][NV];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) o[i][n] = la_f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        Frag<Elem> f[T];
+#pragma unroll
+        for (int i = 0; i < T; ++i) f[i] = row_frag(sQ, QP, 16 * i + r, 32 * kb);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
           const la_f32x4 x = S[2 * kb][n], y = S[2 * kb + 1][n];
-          sp[kb][n].split({x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+          Pieces<Elem, 2> sp;
+          sp.split({x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+#pragma unroll
+          for (int e = sp.kCount - 1; e >= 0; --e)
+#pragma unroll
+            for (int i = 0; i < T; ++i) o[i][n] = mma(piece(sp, e), f[i], o[i][n]);
         }
-      lds_barrier();
-      // Results as rows v of columns t.
+      }
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-        la_f32x4 o[NV];
-#pragma unroll
-        for (int n = 0; n < NV; ++n) o[n] = la_f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const Frag<Elem> f = row_frag(sQ, QP, 16 * i + r, 32 * kb);
-#pragma unroll
-          for (int n = 0; n < NV; ++n) o[n] = mma(sp[kb][n], f, o[n]);
-        }
-        const int t = 16 * i + r;
-        const float into = dec.into[t] * p.scale;
+        const float into = dec.into[16 * i + r] * p.scale;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= into;
+          for (int e = 0; e < 4; ++e) o[i][n][e] *= into;
+      }
+      lds_barrier();
+      // Then the pairs.
 #pragma unroll
-        for (int sb = 0; sb <= i / 2; ++sb) {
-          const Frag<Elem> f = row_frag(sP, PP, 16 * i + r, 32 * sb);
+      for (int sb = 0; sb < SB; ++sb) {
+        Frag<Elem> f[T];
 #pragma unroll
-          for (int n = 0; n < NV; ++n) o[n] = mma(vf[sb][n], f, o[n]);
-        }
+        for (int i = 2 * sb; i < T; ++i) f[i] = row_frag(sP, PP, 16 * i + r, 32 * sb);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int i = 2 * sb; i < T; ++i) o[i][n] = mma(vf[sb][n], f[i], o[i][n]);
+      }
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const int t = 16 * i + r;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
           const int vr = vcol + 16 * n + 4 * g;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] = t < live ? o[n][e] : 0.0f;
+          for (int e = 0; e < 4; ++e) o[i][n][e] = t < live ? o[i][n][e] : 0.0f;
           store4_at<Elem, kWhole>(to, uint32_t(t) * uint32_t(out_step) * E + uint32_t(vr) * E, p.dv - vr, t < rows,
-                                  o[n]);
+                                  o[i][n]);
         }
       }
       // The state at the chunk's end.
@@ -228,18 +241,25 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
         }
       }
 #pragma unroll
-      for (int j = 0; j < KP / 16; ++j) {
+      for (int j = 0; j < KP / 16; ++j)
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) S[j][n][e] *= total;
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-          const Frag<Elem> f = col_frag_paired(sK, QP, 32 * sb, 32 * (j / 2), j % 2);
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-          for (int n = 0; n < NV; ++n) S[j][n] = mma(f, add[sb][n], S[j][n]);
+        for (int j4 = 0; j4 < KP / 16; j4 += 4) {
+          Frag<Elem> f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = col_frag_paired(sK, QP, 32 * sb, 32 * ((j4 + j) / 2), j % 2);
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = add[sb][n].kCount - 1; e >= 0; --e)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) S[j4 + j][n] = mma(f[j], piece(add[sb][n], e), S[j4 + j][n]);
         }
-      }
     } else {
       // Behind the row's end: zeros, and the state stays.
 #pragma unroll
@@ -328,13 +348,13 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
 
   const int xpad = int(linattn_pad(d.xd, 32)), ypad = int(linattn_pad(d.yd, 32));
   const int64_t floats = int64_t(xpad) * ypad, ext = (b * p.heads + h) * int64_t(d.xd) * d.yd;
-  // Tiles (2 j, m) and (2 j + 1, m): rows x = 32 j + 8 g + i and + 4 + i of column y0 + 16 (NY w + m) + r.
+  // Tile (j, m): rows x = 16 j + 4 g + i of column y = y0 + 16 (NY w + m) + r.
   la_f32x4 S[XP / 16][NY];
 #pragma unroll
   for (int j = 0; j < XP / 16; ++j)
 #pragma unroll
     for (int m = 0; m < NY; ++m) {
-      const int yc = y0 + 16 * (NY * w + m) + r, xr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
+      const int yc = y0 + 16 * (NY * w + m) + r, xr = 16 * j + 4 * g;
       S[j][m] = la_f32x4{0, 0, 0, 0};
       if constexpr (kWalk) {
         if (d.starts && yc < ypad && xr < xpad)
@@ -354,7 +374,7 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
       const int yc = y0 + 16 * (NY * w + m) + r;
 #pragma unroll
       for (int j = 0; j < XP / 16; ++j) {
-        const int xr = 32 * (j / 2) + 8 * g + 4 * (j % 2);
+        const int xr = 16 * j + 4 * g;
         to.store16(__builtin_bit_cast(uint4, S[j][m]), yc < ypad && xr < xpad ? uint32_t(yc * xpad + xr) * 4u : kLaOob);
       }
     }
@@ -424,18 +444,25 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
       }
     }
 #pragma unroll
-    for (int j = 0; j < XP / 16; ++j) {
+    for (int j = 0; j < XP / 16; ++j)
 #pragma unroll
       for (int m = 0; m < NY; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][m][e] *= total;
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) {
-        const Frag<Elem> f = col_frag_paired(sX, XPITCH, 32 * sb, 32 * (j / 2), j % 2);
+    for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-        for (int m = 0; m < NY; ++m) S[j][m] = mma(f, add[sb][m], S[j][m]);
+      for (int j4 = 0; j4 < XP / 16; j4 += 4) {
+        Frag<Elem> f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = col_frag(sX, XPITCH, 32 * sb, 16 * (j4 + j));
+#pragma unroll
+        for (int m = 0; m < NY; ++m)
+#pragma unroll
+          for (int e = add[sb][m].kCount - 1; e >= 0; --e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[j4 + j][m] = mma(f[j], piece(add[sb][m], e), S[j4 + j][m]);
       }
-    }
   };
   for (int64_t i = i0; i < i1; i += 2) {
     step(i, 0);
@@ -451,7 +478,7 @@ __global__ __launch_bounds__(kLaThreads, XP <= 128 ? 2 : 1) void linattn_state_k
       for (int j = 0; j < XP / 16; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int xr = 32 * (j / 2) + 8 * g + 4 * (j % 2) + e;
+          const int xr = 16 * j + 4 * g + e;
           if (yc < d.yd && xr < d.xd) d.last[ext + int64_t(xr) * d.yd + yc] = S[j][m][e];
         }
     }

@@ -7,11 +7,6 @@
 
 namespace ssm {
 
-#ifndef LAT
-#define LAB (64 << 20)
-#define LAT 384
-#define LAW 512
-#endif
 constexpr int kLinattnMaxDim = 256;  // dk and dv
 
 // Steps of a chunk: 64, or 32 in fp32, whose tiles would not fit LDS at 256 columns otherwise.
@@ -56,6 +51,12 @@ constexpr int64_t linattn_value_tiles(int64_t dk, int64_t dv) {
 }
 constexpr int64_t linattn_pad(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+// Workgroups that fill the device, two for each CU; with a good part of that, more would cost the
+// segments' states without making it faster. b4, 32 heads of 128 x 64, 2048 steps: 88 us in 512
+// workgroups, 98 in 768, 93 in 1024; b1, 16 heads of 128 x 128, 65536 steps: 491, 602 and 561.
+constexpr int64_t kLinattnFew = 384;
+constexpr int64_t kLinattnGroups = 512;
+
 // How the forward cuts a sequence into segments that run side by side, each from a state that
 // two small launches before it find.
 struct LinattnSegments {
@@ -69,7 +70,7 @@ inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk
   const int64_t c = linattn_chunk(io);
   s.chunks = (seqlen + c - 1) / c;
   const int64_t base = batch * heads * linattn_value_tiles(dk, dv);
-  int64_t want = base > 0 && base < LAT ? (LAW + base - 1) / base : 1;
+  int64_t want = base > 0 && base < kLinattnFew ? (kLinattnGroups + base - 1) / base : 1;
   if (want > s.chunks) want = s.chunks;
   s.per = want > 0 ? (s.chunks + want - 1) / want : 1;
   s.count = s.chunks > 0 ? (s.chunks + s.per - 1) / s.per : 1;
@@ -86,7 +87,10 @@ inline int64_t linattn_state_floats(int64_t rows, int64_t cols) {
 // segment and leaves the state of each, from the segment's start, which is the sequence's, or is
 // found by a first walk that leaves segments' states alone and the join. Else every chunk by
 // itself, and the join over the chunks (all of them read and written once more), where they are
-// few enough to stay in the caches.
+// few enough to stay in the caches. b4, 32 heads of 128 x 64, 2048 steps (268 MB): 126 us walked, 196
+// joined; b1, 16 heads of 128 x 128, 16384 steps (537 MB): 316 and 396; b3, 4 heads of 64 x 100, 517
+// steps in fp32 (17 MB): 36 and 24.
+constexpr int64_t kLinattnCached = int64_t(64) << 20;
 struct LinattnBwdStates {
   bool walked;
   LinattnSegments segments;  // of the walk
@@ -101,11 +105,11 @@ inline LinattnBwdStates linattn_bwd_states(int64_t batch, int64_t heads, int64_t
   s.chunks = (seqlen + c - 1) / c;
   s.floats = linattn_state_floats(dk, dv);
   s.chunk_rows = batch * heads * s.chunks;
-  s.walked = double(s.chunk_rows) * double(s.floats) * 8.0 > double(LAB);
+  s.walked = double(s.chunk_rows) * double(s.floats) * 8.0 > double(kLinattnCached);
   s.segments = LinattnSegments{s.chunks, s.chunks, 1};
   if (s.walked) {
     const int64_t base = batch * heads * 2 * ((dk + 63) / 64);
-    int64_t want = base < 384 ? (512 + base - 1) / base : 1;
+    int64_t want = base < kLinattnFew ? (kLinattnGroups + base - 1) / base : 1;
     if (want > s.chunks) want = s.chunks;
     s.segments.per = (s.chunks + want - 1) / want;
     s.segments.count = (s.chunks + s.segments.per - 1) / s.segments.per;
