@@ -14,6 +14,7 @@ import subprocess
 import sys
 import tempfile
 import warnings
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -68,7 +69,22 @@ def _compile(cmd, sources, target, verbose):
 
 
 def _link(sources, target, verbose, extra=()):
-    return _compile([hipcc(), *compile_flags(), *extra], sources, target, verbose)
+    """The library of these sources, each compiled by itself, several at a time."""
+    cmd = [hipcc(), *compile_flags(), *extra]
+    jobs = int(os.environ.get("MAX_JOBS") or min(8, os.cpu_count() or 1))
+    with tempfile.TemporaryDirectory(prefix=os.path.basename(target) + ".", suffix=".tmp", dir=PKG) as folder:
+        def compile_one(source):
+            obj = os.path.join(folder, os.path.basename(source) + ".o")
+            if verbose:
+                print(" ".join([*cmd, "-c", source]), flush=True)
+            r = subprocess.run([*cmd, "-c", source, "-o", obj], cwd=PKG, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"{cmd[0]} failed on {source} ({r.returncode}):\n{r.stderr}")
+            return obj
+
+        with ThreadPoolExecutor(max_workers=max(jobs, 1)) as pool:
+            objects = list(pool.map(compile_one, sources))
+        return _compile(cmd, objects, target, verbose)
 
 
 def _binding_lacks():
