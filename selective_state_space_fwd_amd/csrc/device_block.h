@@ -140,6 +140,11 @@ __device__ __forceinline__ void store_stream(void* p, const Dwords<4>& d) {
   store16_stream(p, make_uint4(d.w[0], d.w[1], d.w[2], d.w[3]));
 }
 
+__device__ __forceinline__ void store_stream(void* p, const Dwords<2>& d) {
+  typedef uint32_t Pair __attribute__((ext_vector_type(2), aligned(2)));
+  __builtin_nontemporal_store(Pair{d.w[0], d.w[1]}, reinterpret_cast<Pair*>(p));
+}
+
 // Value c (a constant after unrolling) of storage dwords, and all of them rounded.
 template <typename Elem, int N>
 __device__ __forceinline__ float few_elem(const Dwords<N>& d, int c) {

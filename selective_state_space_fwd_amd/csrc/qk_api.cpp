@@ -34,11 +34,14 @@ int check_sizes(uint32_t flags, int64_t batch, int64_t seqlen, int64_t q_heads, 
   z->table_bytes = product({table_rows, rot / 2, 4});
   const int64_t steps = product({batch, seqlen, 4}), rows = product({batch, seqlen, q_heads + k_heads});
   if (z->q_bytes < 0 || z->k_bytes < 0 || z->table_bytes < 0 || steps < 0 || rows < 0) return SSM_ERR_UNSUPPORTED;
-  const int lg = ssm::qk_lanes_log2(dim, rot), per = ssm::qk_rows(batch, seqlen, q_heads + k_heads, lg);
+  const int lg = ssm::qk_lanes_log2(dim, rot);
+  // The backward's items, no fewer than the forward's.
+  const bool many = ssm::qk_many(batch, seqlen, q_heads + k_heads, lg);
+  const int per = many ? ssm::qk_most_rows(true, int(z->esz)) : 1;
   const int64_t q_items = ssm::qk_items(batch, seqlen, q_heads, per), k_items = ssm::qk_items(batch, seqlen, k_heads, per);
   if (seqlen > kInt32Max || q_items > ssm::kQkMostItems || k_items > ssm::kQkMostItems) return SSM_ERR_UNSUPPORTED;
   const int64_t q_groups = ssm::qk_groups(q_items, lg), k_groups = ssm::qk_groups(k_items, lg);
-  z->workspace = (ssm::qk_partials(q_groups) + ssm::qk_partials(k_groups)) * dim * 4;
+  z->workspace = (ssm::qk_partials(q_groups, k_groups) + ssm::qk_partials(k_groups, q_groups)) * dim * 4;
   return ssm::grid_fits(q_groups + k_groups, 64 * ssm::kQkWaves) ? SSM_OK : SSM_ERR_UNSUPPORTED;
 }
 

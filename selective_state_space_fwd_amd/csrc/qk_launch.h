@@ -34,12 +34,20 @@ inline int qk_lanes_log2(int64_t dim, int64_t rot) {
   return lg;
 }
 
-// Heads of one step that a row's lanes take one after another, all loads first: they share the
-// angles. One where the call is small, for more waves.
-constexpr int kQkMostRows = 4;
-inline int qk_rows(int64_t batch, int64_t seqlen, int64_t heads, int lg) {
-  return ((batch * seqlen * heads) >> (6 - lg)) / kQkMostRows >= 4096 ? kQkMostRows : 1;
+// Large calls, by the waves that hold one head a group of lanes: several heads a group, and results
+// stored past L2. 32 + 8 heads of 128 in bf16, few | many, us (forward, gradient): 256 steps 5.3 10.4 |
+// 6.7 10.5; 1024 steps (10240 waves) 8.1 15.2 | 8.1 13.6; 2048 steps 11.4 20.9 | 9.1 18.1; 8192 steps
+// 41.7 64.4 | 34.9 51.7. fp32: 1024 steps 11.0 17.5 | 9.6 17.0; 8192 steps 62.5 84.3 | 57.9 82.0.
+constexpr int64_t kQkManyWaves = 10240;
+inline bool qk_many(int64_t batch, int64_t seqlen, int64_t heads, int lg) {
+  return (batch * seqlen * heads) >> (6 - lg) >= kQkManyWaves;
 }
+
+// Heads of one step that a group of lanes takes together in a large call, all loads first: they share
+// the angles. (bf16, 8192 steps of 32 + 8 heads of 128: forward 4 heads 44.0 us, 2 heads 45.0;
+// gradient, its loads an item ahead, 4 heads 76.5 (spills), 2 heads 68.5, 1 head 75.2. fp32's two
+// heads spill.)
+constexpr int qk_most_rows(bool bwd, int bytes) { return bwd ? (bytes == 2 ? 2 : 1) : 4; }
 
 // What one group of lanes takes: `rows` heads of one side (q or k) at one step; and the workgroups
 // of a side.
@@ -53,9 +61,15 @@ inline int64_t qk_groups(int64_t items, int lg) {
 // Items are numbered in 32 bits.
 constexpr int64_t kQkMostItems = (int64_t(1) << 31) - 1;
 
-// Workgroups of a side in the backward, each with one row of partial weight gradients.
-constexpr int64_t kQkMostPartials = 2048;
-inline int64_t qk_partials(int64_t groups) { return groups < kQkMostPartials ? groups : kQkMostPartials; }
+// Workgroups of a side in the backward, each with one row of partial weight gradients: no more than
+// the chip holds at once, four a compute unit, shared between the sides by their items, each loading
+// its next item while it works on this one. (bf16, 8192 steps of 32 + 8 heads of 128, five a compute
+// unit: 1280 workgroups 71.1 us, 2560 78.6; four: 1024 68.5.)
+constexpr int64_t kQkMostPartials = 1024;
+inline int64_t qk_partials(int64_t groups, int64_t other) {
+  const int64_t all = groups + other;
+  return all <= kQkMostPartials ? groups : groups == 0 ? 0 : (kQkMostPartials * groups + all - 1) / all;
+}
 
 int launch_qk_fwd(const QkArgs& a, void* stream);
 int launch_qk_bwd(const QkArgs& a, void* stream);
