@@ -96,6 +96,19 @@ def test_qk(shape, io):
     check_side("k", k64, kw, gk64, out[1], d, ref, shape[5], io)
 
 
+# Calls of many heads, whose counts leave the last of a group's heads and the last round of items short.
+LARGE = [
+    (3, 1501, 7, 3, 96, 48, True, True, True), (2, 6503, 5, 2, 33, 10, False, True, True),
+    (1, 2050, 9, 2, 256, 256, False, False, True), (2, 2049, 13, 1, 128, 64, False, True, False),
+]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", LARGE, ids=["b{}L{}q{}k{}d{}r{}".format(*s[:6]) for s in LARGE])
+def test_qk_large(shape, io):
+    test_qk(shape, io)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_strides(io):
     announce(f"qk_norm strides {io}")
