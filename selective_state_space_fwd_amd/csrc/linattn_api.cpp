@@ -232,7 +232,7 @@ int ssm_linattn_step(const void* q, const int64_t* q_strides, const void* k, con
   if (nslots < 0 || (!slots && nslots < batch)) return SSM_ERR_INVALID_ARG;
   const int64_t cache = product({nslots, heads, dk, dv, 4});
   if (nslots > kInt32Max || cache < 0 ||
-      !ssm::grid_fits(ssm::linattn_step_form(batch, heads, dk, dv).groups, 64 * ssm::kLinattnStepWaves))
+      !ssm::grid_fits(ssm::linattn_step_form(heads, dk, dv).groups, 64 * ssm::kLinattnStepWaves))
     return SSM_ERR_UNSUPPORTED;
   ssm::LinattnStepArgs a{};
   ssm::HeadRows gates;

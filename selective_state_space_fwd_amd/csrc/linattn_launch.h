@@ -44,18 +44,25 @@ struct LinattnArgs {
 };
 
 // Columns of dv that a workgroup of the forward takes: its waves keep the state of dk x that many
-// in registers, with room for the operands next to it.
+// in registers, with room for the operands next to it. (dk = dv = 128: 128 at a time 435 us for b1, 16 heads,
+// 65536 steps and 216 for b4, 32 heads, 4096 steps; 64 at a time 504 and 245.)
 constexpr int linattn_value_tile(int64_t dk, int64_t dv) { return dv <= 64 || dk > 128 ? 64 : 128; }
 constexpr int64_t linattn_value_tiles(int64_t dk, int64_t dv) {
   return (dv + linattn_value_tile(dk, dv) - 1) / linattn_value_tile(dk, dv);
 }
 constexpr int64_t linattn_pad(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Workgroups that fill the device, two for each CU; with a good part of that, more would cost the
-// segments' states without making it faster. b4, 32 heads of 128 x 64, 2048 steps: 88 us in 512
-// workgroups, 98 in 768, 93 in 1024; b1, 16 heads of 128 x 128, 65536 steps: 491, 602 and 561.
-constexpr int64_t kLinattnFew = 384;
+// Into how many segments the sequences are cut where batch rows and heads are `base` workgroups: at
+// most as many as leave all workgroups resident, two for each CU; and three at least, since the
+// segments' states are a second pass over half of what the forward reads. Forward, 2048 steps of heads of
+// 128 x 64, us in one segment | cut: base 128 114 | 80 in four (92 in three, 98 in six); 160 114 | 96 in three,
+// 110 in four (640 workgroups); 192 113 | 131 in two; 256 115 | 138. The backward's walks, gradient in all:
+// base 128 (4096 steps) 200 | 160 in four; 192 241 | 265 in two; 256 (2048 steps) 139 | 163.
 constexpr int64_t kLinattnGroups = 512;
+inline int64_t linattn_cuts(int64_t base, int64_t chunks) {
+  const int64_t want = base > 0 ? kLinattnGroups / base : 1;
+  return want < 3 ? 1 : want < chunks ? want : chunks;
+}
 
 // How the forward cuts a sequence into segments that run side by side, each from a state that
 // two small launches before it find.
@@ -70,9 +77,8 @@ inline LinattnSegments linattn_segments(int64_t batch, int64_t heads, int64_t dk
   const int64_t c = linattn_chunk(io);
   s.chunks = (seqlen + c - 1) / c;
   const int64_t base = batch * heads * linattn_value_tiles(dk, dv);
-  int64_t want = base > 0 && base < kLinattnFew ? (kLinattnGroups + base - 1) / base : 1;
-  if (want > s.chunks) want = s.chunks;
-  s.per = want > 0 ? (s.chunks + want - 1) / want : 1;
+  const int64_t want = linattn_cuts(base, s.chunks);
+  s.per = s.chunks > 0 ? (s.chunks + want - 1) / want : 1;
   s.count = s.chunks > 0 ? (s.chunks + s.per - 1) / s.per : 1;
   return s;
 }
@@ -109,8 +115,7 @@ inline LinattnBwdStates linattn_bwd_states(int64_t batch, int64_t heads, int64_t
   s.segments = LinattnSegments{s.chunks, s.chunks, 1};
   if (s.walked) {
     const int64_t base = batch * heads * 2 * ((dk + 63) / 64);
-    int64_t want = base < kLinattnFew ? (kLinattnGroups + base - 1) / base : 1;
-    if (want > s.chunks) want = s.chunks;
+    const int64_t want = linattn_cuts(base, s.chunks);
     s.segments.per = (s.chunks + want - 1) / want;
     s.segments.count = (s.chunks + s.segments.per - 1) / s.segments.per;
   }
@@ -141,23 +146,22 @@ int launch_linattn_bwd(const LinattnArgs& a, void* stream);
 
 constexpr int kLinattnStepWaves = 4;
 
-// Rows of the state per lane, of 2^lg lanes a row (no more than a lane for each row's v): many
-// where the call fills the device, so that a lane has as many loads in flight; few else.
+// Rows of the state per lane, of 2^lg lanes a row (no more than a lane for each row's v): eight, for as
+// many loads in flight, or four where eight would give a workgroup more rows than the head has. 32 heads of
+// 128 x 64 (eight): 67 MB moved 12.7 us, 14.2 with four; 24 heads of 64 x 64 (four): 50 MB 10.2 us, 13.3 with
+// eight. Two or sixteen were slower at both.
 constexpr int linattn_step_most_rows(int lg) { return lg >= 3 ? 8 : 1 << lg; }
-constexpr int linattn_step_few_rows(int lg) { return lg >= 1 ? 2 : 1; }
+constexpr int linattn_step_less_rows(int lg) { return lg >= 3 ? 4 : 1 << lg; }
 
 struct LinattnStepForm {
   int rows;
-  bool past_caches;         // the states are too many for the GPU's caches to keep
   int64_t tiles, groups;    // workgroups of a head, and of a batch row
 };
-inline LinattnStepForm linattn_step_form(int64_t batch, int64_t heads, int64_t dk, int64_t dv) {
-  const int lg = step_lanes_log2(dk), most = linattn_step_most_rows(lg), per = 64 >> lg;
-  const bool many = batch * heads * dv / (most * per) >= 8192;
+inline LinattnStepForm linattn_step_form(int64_t heads, int64_t dk, int64_t dv) {
+  const int lg = step_lanes_log2(dk), most = linattn_step_most_rows(lg), per = kLinattnStepWaves * (64 >> lg);
   LinattnStepForm f{};
-  f.rows = many ? most : linattn_step_few_rows(lg);
-  f.past_caches = many && batch * heads * dk * dv * 4 >= (int64_t(1) << 27);
-  const int64_t tile = int64_t(kLinattnStepWaves) * f.rows * per;
+  f.rows = most * per <= dv ? most : linattn_step_less_rows(lg);
+  const int64_t tile = int64_t(f.rows) * per;
   f.tiles = (dv + tile - 1) / tile;
   f.groups = f.tiles * heads;
   return f;

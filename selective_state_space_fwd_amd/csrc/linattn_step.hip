@@ -5,7 +5,12 @@
 // The fp32 state is all of the traffic, read and written once, so the layout is the state's: a lane
 // holds four consecutive k (16 bytes) of R rows v, the lanes of a row are consecutive and a power
 // of two in number. q, k and the decay are the head's, the same for its rows; a row's v is loaded
-// by one lane each and dealt out, and its result goes back the same way.
+// by one lane each and dealt out, and its result goes back the same way. A state is not read again
+// before the next token, so it goes past L2 both ways: 32 heads of 128 x 64, b32 (67 MB moved) 18.9 ->
+// 12.7 us, b64 32.7 -> 24.6, b128 57 -> 50, and no slower where one cache of 17 MB stays in the caches.
+//
+// Memory binds it: b512, 32 heads of 128 x 64 (1080 MB) 188 us, 5.7 TB/s (a copy's rate is 5.1); b8, 16 heads
+// of 128 x 128 (17 MB) 5.9 us, where a launch is most of it.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -31,11 +36,9 @@ struct LinattnStepParams {
 
 typedef float quad_t __attribute__((ext_vector_type(4), aligned(4)));
 
-template <bool kStream>
 __device__ __forceinline__ void load_state(const float* p, int n, float (&v)[4]) {
   if (n >= 4) {
-    const quad_t q = kStream ? __builtin_nontemporal_load(reinterpret_cast<const quad_t*>(p))
-                             : *reinterpret_cast<const quad_t*>(p);
+    const quad_t q = __builtin_nontemporal_load(reinterpret_cast<const quad_t*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = q[i];
   } else {
@@ -44,7 +47,7 @@ __device__ __forceinline__ void load_state(const float* p, int n, float (&v)[4])
 }
 
 // LG: log2 of the lanes of a row. R: rows a lane, at most as many as lanes of a row.
-template <typename Elem, int LG, int R, bool kStream>
+template <typename Elem, int LG, int R>
 __global__ __launch_bounds__(64 * kWaves) void linattn_step_kernel(LinattnStepParams p) {
   constexpr int RPA = 64 >> LG;  // rows per access of a wave
   static_assert(R * RPA <= 64, "a lane for each row's v");
@@ -71,7 +74,7 @@ __global__ __launch_bounds__(64 * kWaves) void linattn_step_kernel(LinattnStepPa
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int v = v0 + i * RPA + (lane >> LG);
-    load_state<kStream>(state + int64_t(v) * p.dk, v < p.dv ? nk : 0, s[i]);
+    load_state(state + int64_t(v) * p.dk, v < p.dv ? nk : 0, s[i]);
   }
   float q[4], k[4], v = 0.0f, g = 0.0f;
   auto load_token = [&] {
@@ -117,24 +120,18 @@ __global__ __launch_bounds__(64 * kWaves) void linattn_step_kernel(LinattnStepPa
   for (int i = 0; i < R; ++i) {
     const int vr = v0 + i * RPA + (lane >> LG);
     float* to = state + int64_t(vr) * p.dk;
-    const int n = vr < p.dv ? nk : 0;
-    if (kStream)
-      store_run_stream<float, 4>(to, n, s[i]);
-    else
-      store_run<float, 4>(to, n, s[i]);
+    store_run_stream<float, 4>(to, vr < p.dv ? nk : 0, s[i]);
   }
 }
 
 template <typename Elem, int LG>
 void run_lg(const LinattnStepParams& p, const LinattnStepForm& f, hipStream_t s) {
-  constexpr int most = linattn_step_most_rows(LG), few = linattn_step_few_rows(LG);
+  constexpr int most = linattn_step_most_rows(LG), less = linattn_step_less_rows(LG);
   const dim3 grid(unsigned(f.groups), unsigned(p.batch)), block(64 * kWaves);
-  if (f.past_caches)
-    hipLaunchKernelGGL((linattn_step_kernel<Elem, LG, most, true>), grid, block, 0, s, p);
-  else if (f.rows == most)
-    hipLaunchKernelGGL((linattn_step_kernel<Elem, LG, most, false>), grid, block, 0, s, p);
+  if (f.rows == most)
+    hipLaunchKernelGGL((linattn_step_kernel<Elem, LG, most>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((linattn_step_kernel<Elem, LG, few, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((linattn_step_kernel<Elem, LG, less>), grid, block, 0, s, p);
 }
 
 template <typename Elem>
@@ -153,7 +150,7 @@ void run(const LinattnStepParams& p, const LinattnStepForm& f, hipStream_t s) {
 }  // namespace
 
 int launch_linattn_step(const LinattnStepArgs& a, void* stream) {
-  const LinattnStepForm f = linattn_step_form(a.batch, a.heads, a.dk, a.dv);
+  const LinattnStepForm f = linattn_step_form(a.heads, a.dk, a.dv);
   LinattnStepParams p{};
   p.q = a.q, p.k = a.k, p.v = a.v;
   p.g = a.g, p.g_batch = a.g_batch, p.g_head = a.g_head;

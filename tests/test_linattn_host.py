@@ -171,7 +171,7 @@ int main() {
       bad += w.segments.count > 1 && w.segment_rows != b * h * w.segments.count;
       bad += w.total < (w.chunk_rows + w.segment_rows) * (2 * w.floats + 2);
     }
-    const LinattnStepForm f = linattn_step_form(b, h, k, v);
+    const LinattnStepForm f = linattn_step_form(h, k, v);
     bad += f.tiles * kLinattnStepWaves * f.rows * (64 >> step_lanes_log2(k)) < v || f.rows * (64 >> step_lanes_log2(k)) > 64;
   }
   for (int64_t d = 1; d <= 256; ++d) for (int64_t r = 0; r <= d; r += 2) {
