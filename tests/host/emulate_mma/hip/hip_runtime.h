@@ -5,6 +5,7 @@
 // returned.
 #pragma once
 #include <math.h>
+#include <setjmp.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -54,7 +55,13 @@ struct Meeting {  // of `alive` lanes
   int alive = 0, here = 0;
   long turn = 0;
 };
-inline ucontext_t scheduler;
+// A fiber starts by its context and is switched to by jumps, which make no system call.
+struct Jump {
+  jmp_buf at;
+  bool set;
+};
+inline Jump scheduler;
+inline std::vector<Jump> jumps;
 inline std::vector<ucontext_t> fibers;
 inline std::vector<char> done;
 inline std::vector<std::vector<char>> stacks;
@@ -64,7 +71,15 @@ inline char slot[1024][32];
 inline dim3 thread_idx, block_idx, grid_dim, block_dim;
 inline std::function<void()> body;
 
-inline void yield() { swapcontext(&fibers[now], &scheduler); }
+inline void yield() {
+  jumps[now].set = true;
+  if (!_setjmp(jumps[now].at)) _longjmp(scheduler.at, 1);
+}
+inline void resume(int t) {
+  if (_setjmp(scheduler.at)) return;
+  if (jumps[t].set) _longjmp(jumps[t].at, 1);
+  setcontext(&fibers[t]);
+}
 inline void close(Meeting& m) {
   m.here = 0;
   ++m.turn;
@@ -108,6 +123,7 @@ inline void launch(dim3 grid, dim3 block, std::function<void()> kernel) {
   body = std::move(kernel);
   const int n = int(block.x);
   fibers.resize(n);
+  jumps.resize(n);
   done.resize(n);
   stacks.resize(n);
   grid_dim = grid;
@@ -119,11 +135,12 @@ inline void launch(dim3 grid, dim3 block, std::function<void()> kernel) {
       for (int w = 0; w < n / 64; ++w) wave_meets[w] = Meeting{64};
       for (int t = 0; t < n; ++t) {
         done[t] = 0;
+        jumps[t].set = false;
         stacks[t].resize(1 << 20);
         getcontext(&fibers[t]);
         fibers[t].uc_stack.ss_sp = stacks[t].data();
         fibers[t].uc_stack.ss_size = stacks[t].size();
-        fibers[t].uc_link = &scheduler;
+        fibers[t].uc_link = nullptr;
         makecontext(&fibers[t], fiber, 0);
       }
       for (int left = n; left > 0;)
@@ -131,7 +148,7 @@ inline void launch(dim3 grid, dim3 block, std::function<void()> kernel) {
           if (done[t]) continue;
           now = t;
           thread_idx = dim3(unsigned(t));
-          swapcontext(&scheduler, &fibers[t]);
+          resume(t);
           if (done[t]) --left;
         }
     }

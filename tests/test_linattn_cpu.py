@@ -55,6 +55,8 @@ def build(folder, rules={}):
 @pytest.mark.parametrize("rules", [{}, LARGE], ids=["small", "large"])
 def test_linattn_cpu(tmp_path, rules):
     exe = build(str(tmp_path), rules)
-    r = subprocess.run([exe], capture_output=True, text=True, timeout=900)
-    print(r.stdout[-6000:])
-    assert r.returncode == 0 and "linattn ok" in r.stdout, f"{r.returncode}\n{r.stdout[-3000:]}"
+    runs = [subprocess.Popen([exe, side], stdout=subprocess.PIPE, text=True) for side in ("front", "back")]
+    for r in runs:
+        out, _ = r.communicate(timeout=900)
+        print(out[-6000:])
+        assert r.returncode == 0 and "linattn ok" in out, f"{r.returncode}\n{out[-3000:]}"
