@@ -24,6 +24,13 @@
 // Roundings: the pairs' weights (scale D qk and scale D dov) are rounded to bf16 once, as operands,
 // next to results in bf16. S and R enter in three bf16 pieces where dg, a result in fp32, comes
 // of the product, and in two in dv.
+//
+// Measured, bf16, this kernel | the walk that leaves S and R: b4, 8 heads of 128 for 32 of 64, 2048 steps
+// 155 | 129 us, reading 370 MB and writing 70 | 106 and 268; b1, 16 heads of 128 x 128, 16384 steps 328 | 200 (and 105
+// for a first walk that finds its segments' starts). The two pass S and R through memory, 8 bytes a value
+// each way; recomputing them in this kernel (several chunks a workgroup) was slower, 168 against 147, for want of
+// registers. What bounds it: no unit is full (matrix cores 15%, LDS 30%, VALU 36% of its cycles, memory at half of
+// a copy's rate); registers hold a CU to one workgroup, whose loads, pairs, states and stores follow one another.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -92,9 +99,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   constexpr int NK = kHalfK ? 1 : KP / 128, NV = kHalfV ? 1 : VP / 128;
   constexpr int TK = kHalfK ? T / 2 : T, TV = kHalfV ? T / 2 : T;
   // The states' operands are loaded ahead of the pairs where registers are left for them (b4 8 heads of
-  // 128 for 32 of 64, 2048 steps: 147 us against 155); 128 x 128 keeps them out of its way (16384
-  // steps of 16 heads: 385 against 441, with spills).
+  // 128 for 32 of 64, 2048 steps: 147 us against 155); 128 x 128 has none to spare.
   constexpr bool kAhead = NK * VB <= 2;
+  // Where they are not, two blocks of them at a time in bf16: b1, 16 heads of 128 x 128, 16384 steps, the whole
+  // gradient: 584 us; all four, with 80 bytes a lane spilled, 660. (fp32, without spills: all, 623 against 635.)
+  constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
   __shared__ __attribute__((aligned(16))) Elem sP[C * PP], sD[C * PP];  // weights by rows s: scale D qk, scale D dov
@@ -305,7 +314,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
         la_f32x4 xq[TK], xk[TK];
 #pragma unroll
         for (int i = 0; i < TK; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
-#pragma unroll kUnroll
+#pragma unroll kStateUnroll
         for (int vb = 0; vb < VB; ++vb) {
           uint4 words[2][2];
           if constexpr (kAhead) {
