@@ -57,11 +57,15 @@ constexpr int64_t linattn_pad(int64_t n, int64_t to) { return (n + to - 1) / to 
 // segments' states are a second pass over half of what the forward reads. Forward, 2048 steps of heads of
 // 128 x 64, us in one segment | cut: base 128 114 | 80 in four (92 in three, 98 in six); 160 114 | 96 in three,
 // 110 in four (640 workgroups); 192 113 | 131 in two; 256 115 | 138. The backward's walks, gradient in all:
-// base 128 (4096 steps) 200 | 160 in four; 192 241 | 265 in two; 256 (2048 steps) 139 | 163.
+// base 128 (4096 steps) 200 | 160 in four; 192 241 | 265 in two; 256 (2048 steps) 139 | 163. And only sequences of
+// more than five chunks, whose walk takes as long as the two launches more. bf16, 16 heads of 128 x 128 and
+// 64 of 128 x 64: 256 steps 24.0 18.3 | 26.3 28.8; 384 steps 32.5 24.9 | 29.4 30.9; 512 steps 41.6 31.3 | 31.0 32.8;
+// fp32: 128 steps 31.7 21.5 | 29.3 28.6; 192 steps 43.9 29.2 | 31.4 33.4.
 constexpr int64_t kLinattnGroups = 512;
+constexpr int64_t kLinattnWhole = 5;
 inline int64_t linattn_cuts(int64_t base, int64_t chunks) {
   const int64_t want = base > 0 ? kLinattnGroups / base : 1;
-  return want < 3 ? 1 : want < chunks ? want : chunks;
+  return want < 3 || chunks <= kLinattnWhole ? 1 : want < chunks ? want : chunks;
 }
 
 // How the forward cuts a sequence into segments that run side by side, each from a state that

@@ -16,9 +16,9 @@ KERNELS = ("linattn_kernels.hip", "linattn_bwd.hip", "linattn_step.hip", "qk_ker
 
 
 HOST = ("linattn_api.cpp", "qk_api.cpp")
-# Launch rules that send these small cases down the ways of large calls: states left by a walk, several
-# heads a lane group, workgroups that stay for many items.
-LARGE = {"kLinattnCached": 0, "kQkManyWaves": 1, "kQkMostPartials": 3}
+# Launch rules that send these small cases down the ways of large calls: states left by a walk, segments
+# of few chunks, several heads a lane group, workgroups that stay for many items.
+LARGE = {"kLinattnCached": 0, "kLinattnWhole": 1, "kQkManyWaves": 1, "kQkMostPartials": 3}
 
 
 def build(folder, rules={}):
