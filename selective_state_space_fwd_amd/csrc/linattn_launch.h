@@ -97,9 +97,11 @@ inline int64_t linattn_state_floats(int64_t rows, int64_t cols) {
 // segment and leaves the state of each, from the segment's start, which is the sequence's, or is
 // found by a first walk that leaves segments' states alone and the join. Else every chunk by
 // itself, and the join over the chunks (all of them read and written once more), where they are
-// few enough to stay in the caches. b4, 32 heads of 128 x 64, 2048 steps (268 MB): 126 us walked, 196
-// joined; b1, 16 heads of 128 x 128, 16384 steps (537 MB): 316 and 396; b3, 4 heads of 64 x 100, 517
-// steps in fp32 (17 MB): 36 and 24.
+// few enough to stay in the caches and a walk would be cut. b4, 32 heads of 128 x 64, 2048 steps
+// (268 MB): 126 us walked, 196 joined; b1, 16 heads of 128 x 128, 16384 steps (537 MB): 316 and 396; b3, 4
+// heads of 64 x 100, 517 steps in fp32 (17 MB): 36 and 24. The whole gradient, us, walked | joined: b2, 32 heads
+// of 128 x 64 (256 workgroups, not cut), 128 steps 28.0 | 33.6, 512 steps 54.3 | 62.4, fp32 86.9 | 106.9; 16 heads
+// of 128 x 128, 192 steps 33.9 | 35.1, 256 steps 38.4 | 37.1, 512 steps (cut) 51.0 | 42.9.
 constexpr int64_t kLinattnCached = int64_t(64) << 20;
 struct LinattnBwdStates {
   bool walked;
@@ -115,10 +117,11 @@ inline LinattnBwdStates linattn_bwd_states(int64_t batch, int64_t heads, int64_t
   s.chunks = (seqlen + c - 1) / c;
   s.floats = linattn_state_floats(dk, dv);
   s.chunk_rows = batch * heads * s.chunks;
-  s.walked = double(s.chunk_rows) * double(s.floats) * 8.0 > double(kLinattnCached);
+  const int64_t base = batch * heads * 2 * ((dk + 63) / 64);
+  s.walked = s.chunk_rows > 0 && (double(s.chunk_rows) * double(s.floats) * 8.0 > double(kLinattnCached) ||
+                                  linattn_cuts(base, s.chunks) == 1);
   s.segments = LinattnSegments{s.chunks, s.chunks, 1};
   if (s.walked) {
-    const int64_t base = batch * heads * 2 * ((dk + 63) / 64);
     const int64_t want = linattn_cuts(base, s.chunks);
     s.segments.per = (s.chunks + want - 1) / want;
     s.segments.count = (s.chunks + s.segments.per - 1) / s.segments.per;
