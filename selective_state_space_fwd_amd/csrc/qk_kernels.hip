@@ -13,9 +13,10 @@
 // first, with the angles and weights loaded once; the gradient's workgroups stay for many items, the
 // next one's loads on their way, and leave one row of weight gradients each.
 //
-// Measured, b4 2048 steps of 32 + 8 heads of 128 in bf16, inputs not in cache: forward 38.4 us for 168.8 MB
-// (4.4 TB/s; a copy reaches 5.1), gradient with its weights' sum 65.4 us for 252.7 MB (3.9 TB/s).
-// b8 one token: 5 to 6 us, what a launch costs.
+// Measured, b4 2048 steps of 32 + 8 heads of 128 in bf16, inputs not in cache: forward 33.4 us for 168.8 MB
+// (5.1 TB/s, a copy's rate; the values are held as they came until all heads' loads are out, 38 us widened at
+// once), gradient with its weights' sum 65.4 us for 252.7 MB (3.9 TB/s). b8 one token: 5 to 6 us, what a launch
+// costs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -54,7 +55,7 @@ struct QkParams {
 // The two runs of a lane: values [a, a + na) and [b, b + nb), and its first angle.
 struct Runs {
   int a, b, na, nb, angle;
-  bool turns;
+  bool turns, joined;      // joined: eight neighbours, all there
 };
 
 __device__ __forceinline__ int clamp4(int n) { return n < 0 ? 0 : n > 4 ? 4 : n; }
@@ -74,6 +75,7 @@ __device__ __forceinline__ Runs runs_of(int unit, const QkParams& p) {
     u.na = clamp4(n);
     u.nb = clamp4(n - 4);
   }
+  u.joined = u.b == u.a + 4 && u.nb == 4;
   return u;
 }
 
@@ -107,6 +109,12 @@ __device__ __forceinline__ Dwords<int(sizeof(Elem))> load_raw4(const Elem* p, in
 }
 
 template <typename Elem>
+__device__ __forceinline__ RawRuns<Elem> load_raw(const Elem* p, const Runs& u) {
+  if (sizeof(Elem) == 2 && u.joined) return *reinterpret_cast<const RawRuns<Elem>*>(p + u.a);
+  return RawRuns<Elem>{load_raw4<Elem>(p + u.a, u.na), load_raw4<Elem>(p + u.b, u.nb)};
+}
+
+template <typename Elem>
 __device__ __forceinline__ void widen_runs(const RawRuns<Elem>& d, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -115,23 +123,34 @@ __device__ __forceinline__ void widen_runs(const RawRuns<Elem>& d, float (&v)[8]
   }
 }
 
-// Four values (n of them), past L2 with kStream.
-template <typename Elem, bool kStream>
-__device__ __forceinline__ void store4(Elem* p, int n, const float (&v)[4]) {
-  if (kStream && n >= 4) {
-    Dwords<int(sizeof(Elem))> d;
-    pack_few<Elem, 4>(v, d);
+// C values (n of them), past L2 with `stream`.
+template <typename Elem, int C>
+__device__ __forceinline__ void store_run_of(Elem* p, int n, const float (&v)[C], bool stream) {
+  if (stream && n >= C) {
+    Dwords<C * int(sizeof(Elem)) / 4> d;
+    pack_few<Elem, C>(v, d);
     store_stream(p, d);
   } else {
-    store_few<Elem, 4>(p, n, v);
+    store_few<Elem, C>(p, n, v);
   }
 }
 
-template <typename Elem, bool kStream>
-__device__ __forceinline__ void store_runs(Elem* p, const Runs& u, const float (&v)[8]) {
+template <typename Elem>
+__device__ __forceinline__ void store_runs(Elem* p, const Runs& u, const float (&v)[8], bool stream) {
+  if constexpr (sizeof(Elem) == 2) {
+    if (u.joined) return store_run_of<Elem, 8>(p + u.a, 8, v, stream);
+  }
   const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-  store4<Elem, kStream>(p + u.a, u.na, a);
-  store4<Elem, kStream>(p + u.b, u.nb, b);
+  store_run_of<Elem, 4>(p + u.a, u.na, a, stream);
+  store_run_of<Elem, 4>(p + u.b, u.nb, b, stream);
+}
+
+// Whether a store of the row's lanes fills lines; parts of lines go through L2, which joins them (8192 steps of
+// 32 + 8 heads, past L2 | through it: fp32 heads of 128, neighbouring pairs 96.9 | 65.1 us; bf16 heads of 16 22.2 |
+// 10.6; whole lines, bf16 heads of 128: 33.4 | 44).
+template <typename Elem>
+__device__ __forceinline__ bool fills_lines(const Runs& u, const QkParams& p) {
+  return u.joined ? sizeof(Elem) == 2 : p.rot / 2 * int(sizeof(Elem)) >= 128;
 }
 
 // The four pairs turned by (c, s); by (c, -s) for the way back.
@@ -198,11 +217,12 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkParams p) {
   Item x = item_of(group * kPer + (threadIdx.x >> LG), d, p.seqlen, R);
   if (!x.live) return;
   const Runs u = runs_of(lane, p);
+  const bool stream = kMany && fills_lines<Elem>(u, p);
   const Elem* from = static_cast<const Elem*>(d.x) + x.b * d.batch + x.t * d.step + x.head0 * d.head;
   const int rows = d.heads - x.head0 < R ? d.heads - x.head0 : R;
-  float v[R][8];
+  RawRuns<Elem> raw[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) load_runs<Elem>(from + (i < rows ? i : 0) * d.head, u, v[i]);
+  for (int i = 0; i < R; ++i) raw[i] = load_raw<Elem>(from + (i < rows ? i : 0) * d.head, u);
   float c[4], s[4], w[8];
   load_angles(p, x, u, c, s);
 #pragma unroll
@@ -211,16 +231,18 @@ __global__ __launch_bounds__(kThreads) void qk_fwd_kernel(QkParams p) {
   Elem* to = static_cast<Elem*>(d.out) + ((int64_t(x.b) * p.seqlen + x.t) * d.heads + x.head0) * p.dim;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
+    float v[8];
+    widen_runs<Elem>(raw[i], v);
     float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(v[i][e], v[i][e], sum);
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
     const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum_lanes<LG>(sum), p.inv_dim, p.eps));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * w[e];
-    turn(v[i], c, s, p.interleaved != 0);
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
+    turn(v, c, s, p.interleaved != 0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = x.at_table ? v[i][e] : 0.0f;
-    if (i < rows) store_runs<Elem, kMany>(to + i * p.dim, u, v[i]);
+    for (int e = 0; e < 8; ++e) v[e] = x.at_table ? v[e] : 0.0f;
+    if (i < rows) store_runs<Elem>(to + i * p.dim, u, v, stream);
   }
 }
 
@@ -233,6 +255,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_bwd_kernel(QkParams p, uint32_
   const QkSide& d = p.side[side];
   const uint32_t group = blockIdx.x - (side ? p.q_groups : 0), step = (side ? groups - p.q_groups : p.q_groups) * kPer;
   const Runs u = runs_of(lane, p);
+  const bool stream = kMany && fills_lines<Elem>(u, p);
   float w[8], dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -301,7 +324,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_bwd_kernel(QkParams p, uint32_
         const float o = r * (y[e] - v[e] * mean);
         v[e] = x.at_table ? o : 0.0f;
       }
-      if (i < rows) store_runs<Elem, kMany>(to + i * p.dim, u, v);
+      if (i < rows) store_runs<Elem>(to + i * p.dim, u, v, stream);
     }
   }
   if (!d.partials) return;
@@ -314,10 +337,12 @@ __global__ __launch_bounds__(kThreads, 4) void qk_bwd_kernel(QkParams p, uint32_
     float a[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) a[e] = 0.0f;
+    // (a few at a time: all at once would be the kernel's most registers)
+#pragma unroll 4
     for (uint32_t i = 0; i < kPer; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[e] += part[i][lane * 8 + e];
-    store_runs<float, false>(d.partials + int64_t(group) * p.dim, u, a);
+    store_runs<float>(d.partials + int64_t(group) * p.dim, u, a, false);
   }
 }
 
