@@ -19,9 +19,9 @@
 // (16 bits): in one its error would add to that of the weights. What is added to the state enters
 // in three pieces, all 24 bits, since the state is a result in fp32.
 //
-// Measured, bf16: b4, 8 heads of 128 for 32 of 64, 2048 steps 80.6 us in all, 51 the forward, 29 the segments'
+// Measured, bf16: b4, 8 heads of 128 for 32 of 64, 2048 steps 80.4 us in all, 51 the forward, 29 the segments'
 // states, 7 the join (must move 106 MB, 21 us at a copy's rate; the three launches move 226); b1, 16 heads of
-// 128 x 128, 65536 steps 423, of which 323, 166 and 14 where each runs alone (must move 1076 MB, 210 us; they move 1750,
+// 128 x 128, 65536 steps 433, of which 323, 166 and 14 where each runs alone (must move 1076 MB, 210 us; they move 1750,
 // 4.1 TB/s). The long one is near memory's rate on what a second pass over k and v costs; the short one waits: a
 // chunk's products, decays and stores follow one another, and registers hold it to two workgroups a CU.
 #include <hip/hip_runtime.h>

@@ -35,16 +35,17 @@ inline int qk_lanes_log2(int64_t dim, int64_t rot) {
 }
 
 // Large calls, by the waves that hold one head a group of lanes: several heads a group, and results
-// stored past L2. 32 + 8 heads of 128 in bf16, few | many, us (forward, gradient): 256 steps 5.3 10.4 |
-// 6.7 10.5; 1024 steps (10240 waves) 8.1 15.2 | 8.1 13.6; 2048 steps 11.4 20.9 | 9.1 18.1; 8192 steps
-// 41.7 64.4 | 34.9 51.7. fp32: 1024 steps 11.0 17.5 | 9.6 17.0; 8192 steps 62.5 84.3 | 57.9 82.0.
+// stored past L2. 32 + 8 heads of 128 in bf16, few | many, us (forward, gradient): 512 steps 5.2 12.1 |
+// 5.5 10.5; 1024 steps (10240 waves) 7.9 15.2 | 6.5 13.7; 2048 steps 11.3 21.2 | 8.6 18.3; 8192 steps
+// 38.9 64.5 | 32.1 53.0. fp32: 1024 steps 11.0 17.4 | 9.7 16.9; 8192 steps 62.7 84.3 | 57.8 81.5. Below, where both
+// are near a launch, the results stay in L2 for what reads them next.
 constexpr int64_t kQkManyWaves = 10240;
 inline bool qk_many(int64_t batch, int64_t seqlen, int64_t heads, int lg) {
   return (batch * seqlen * heads) >> (6 - lg) >= kQkManyWaves;
 }
 
 // Heads of one step that a group of lanes takes together in a large call, all loads first: they share
-// the angles. (bf16, 8192 steps of 32 + 8 heads of 128: forward 4 heads 44.0 us, 2 heads 45.0;
+// the angles. (bf16, 8192 steps of 32 + 8 heads of 128: forward 4 heads 32.1 us, 2 heads 33.7;
 // gradient, its loads an item ahead, 4 heads 76.5 (spills), 2 heads 68.5, 1 head 75.2. fp32's two
 // heads spill.)
 constexpr int qk_most_rows(bool bwd, int bytes) { return bwd ? (bytes == 2 ? 2 : 1) : 4; }
