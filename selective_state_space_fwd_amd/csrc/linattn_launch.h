@@ -133,13 +133,17 @@ inline LinattnBwdStates linattn_bwd_states(int64_t batch, int64_t heads, int64_t
 
 inline int64_t linattn_join_blocks(int64_t state_floats) { return (state_floats / 4 + 255) / 256; }
 
-// Rows of whole 16-byte words at 4-byte aligned addresses: a load a word.
+// Rows of whole 16-byte words at 4-byte aligned addresses, those of the results too: a load a word and a store for four
+// values, which a buffer makes in dwords; else each value by itself. (Results are contiguous, so that their rows
+// are where their first value is.)
 inline bool linattn_whole(const LinattnArgs& a, bool bwd) {
   const int64_t esz = a.io == Io::BF16 ? 2 : 4, word = 16 / esz, even = 4 / esz;
+  auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; };
   auto rows = [&](const HeadRows& r) {
-    return reinterpret_cast<uintptr_t>(r.p) % 4 == 0 && r.batch % even == 0 && r.step % even == 0 && r.head % even == 0;
+    return at(r.p) && r.batch % even == 0 && r.step % even == 0 && r.head % even == 0;
   };
-  return a.dk % word == 0 && a.dv % word == 0 && rows(a.q) && rows(a.k) && rows(a.v) && (!bwd || rows(a.dout));
+  const bool results = bwd ? at(a.dq) && at(a.dk_) && at(a.dv_) : at(a.out);
+  return a.dk % word == 0 && a.dv % word == 0 && rows(a.q) && rows(a.k) && rows(a.v) && (!bwd || rows(a.dout)) && results;
 }
 
 // Whether a chunk's rows, `step` elements apart, lie within the 32-bit byte offsets of the kernels.
