@@ -282,6 +282,38 @@ __device__ __forceinline__ double wave_prefix_f64(double v) {
   return v + (row >= 1 ? a : 0.0) + (row >= 2 ? b : 0.0) + (row >= 3 ? c : 0.0);
 }
 
+// Sums of floats over some of a wave's lanes. They only add: what a lane does not sum leaves no trace in
+// it, however large, infinite or NaN.
+template <int kCtrl>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane_of) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane_of));
+}
+// Over the lanes of a row of 16: up to and with this one, and from it on.
+__device__ __forceinline__ float row_prefix(float v) {
+  v = dpp_add<0x111>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112>(v);
+  v = dpp_add<0x114>(v);
+  return dpp_add<0x118>(v);
+}
+__device__ __forceinline__ float row_suffix(float v) {
+  return dpp_move<0x140>(row_prefix(dpp_move<0x140>(v)));  // row_mirror
+}
+// Over the lanes of a wave: before this one, and from it on.
+__device__ __forceinline__ float wave_before(float v) {
+  v = row_prefix(v);
+  const float a = lane_value(v, 15), b = lane_value(v, 31), c = lane_value(v, 47);
+  const int row = int(threadIdx.x & 63) >> 4;
+  return dpp_move<0x111>(v) + (row >= 1 ? a : 0.0f) + (row >= 2 ? b : 0.0f) + (row >= 3 ? c : 0.0f);
+}
+__device__ __forceinline__ float wave_from(float v) {
+  v = row_suffix(v);
+  const float a = lane_value(v, 16), b = lane_value(v, 32), c = lane_value(v, 48);
+  const int row = int(threadIdx.x & 63) >> 4;
+  return v + (row <= 2 ? c : 0.0f) + (row <= 1 ? b : 0.0f) + (row <= 0 ? a : 0.0f);
+}
 // The log decay of a step in units of log 2. Below -1e4 it is -1e4, whose exponential is zero all
 // the same, so that a reset (-inf) leaves finite sums; NaN stays.
 __device__ __forceinline__ double log2_decay(float g) {

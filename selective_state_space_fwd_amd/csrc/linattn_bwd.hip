@@ -10,10 +10,11 @@
 //   dg_t = sum_{i>=t>j} W_ij + sum_{i>=t} q_i . dq_i^S + sum_{j<t} k_j . dk_j^R + exp(cs_end) <R, S>
 //
 // where W_ij = scale D_ij (q_i . k_j)(do_i . v_j), and dq^S, dk^R are the parts through S and R:
-// the pairs of steps, of the chunk and around it, between which the decay g_t lies. dg so needs
-// no difference of sums over the sequence, whose rounding errors would stay where the decays
-// have made dg small; W's rectangles are suffix sums of its row sums less its column sums, over
-// one chunk, in 64 bits.
+// the pairs of steps, of the chunk and around it, between which the decay g_t lies. dg so only adds
+// terms that the decay scales: no difference of sums, over the sequence or the chunk, whose rounding
+// errors would stay where a decay has made dg small. W's rectangle (rows from t on, columns before t) is made of the
+// tiles that lie in it, of row sums of the tiles beside t's block, column sums of those below it, and
+// of a rectangle of the block's own tile.
 //
 // linattn_state_kernel and linattn_join_kernel (linattn_kernels.hip) leave S and R of every chunk
 // in the workspace, [dk][dv] in fp32; linattn_bwd_kernel then takes a (batch row, query head,
@@ -81,8 +82,9 @@ __device__ __forceinline__ BwdTiles bwd_tiles(int w) {
 // What dg of one head comes from, by step of the chunk.
 template <int C>
 struct DgParts {
-  float row[C / 16][C], col[C / 16][C];  // of W, by the tile they are of
-  float qs[8][C], ks[8][C];              // q . dq^S and k . dk^R, by wave
+  float row[C / 16][C];      // of W: row sums of the tiles (i, j), j < i, by j; the tile (i, i)'s rectangles
+  float col[C / 16][C];      // column sums of the tiles (i, j), j < i, by i
+  float qs[8][C], ks[8][C];  // q . dq^S and k . dk^R, by wave
   float x[8], total;
 };
 
@@ -168,25 +170,50 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
     auto finish = [&](int hh) {
       const DgParts<C>& d = parts[hh & 1];
       const int h = hk * p.group + hh, t = l < C ? l : C - 1, i = t / 16;
-      double down = 0.0, up = 0.0, around = 0.0;
+      const bool on = l < C;
+      // W's rectangle: in the block's own tile; of the tiles (i, j) the rows from t on, and those (x, j), j < i < x, which
+      // lie in it whole; of the tiles (x, i) the columns before t.
+      // (Everything is loaded first, whatever comes of it, so that the loads are one wait.)
+      float row[T], col[T], qs[8], ks[8], x[8];
 #pragma unroll
       for (int j = 0; j < T; ++j) {
-        if (j <= i) down += d.row[j][t];
-        if (j >= i) down -= d.col[j][t];
+        row[j] = d.row[j][t];
+        col[j] = d.col[j][t];
       }
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const bool mine = !kHalfK || (x >> 2) == i / TK;
-        if (mine) down += d.qs[x][t];
-        if (mine) up += d.ks[x][t];
-        if (!kHalfK || x < 4) around += d.x[x];
+      for (int j = 0; j < 8; ++j) {
+        qs[j] = d.qs[j][t];
+        ks[j] = d.ks[j][t];
+        x[j] = d.x[j];
       }
-      if (l >= C) down = up = 0.0;
-      const double before = wave_prefix_f64(down), all = dpp_f64(before, 63);
-      const double behind = wave_prefix_f64(up) - up;
-      double dg = all - before + down + behind + double(d.total) * around;
-      if (l >= live) dg = 0.0;
-      if (p.dg && l < rows) p.dg[(b * p.seqlen + t0 + l) * p.heads + h] = float(dg);
+      float rect = 0.0f, cols = 0.0f;
+#pragma unroll
+      for (int j = 0; j < T; ++j) rect = on && j == i ? row[j] : rect;
+#pragma unroll
+      for (int j = 0; j + 1 < T; ++j) {
+        const float rows_on = row_suffix(on && i > j ? row[j] : 0.0f);
+        rect += rows_on;
+#pragma unroll
+        for (int y = j + 2; y < T; ++y) {
+          const float tile = lane_value(rows_on, 16 * y);
+          rect += on && i > j && i < y ? tile : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 1; j < T; ++j) cols += on && j > i ? col[j] : 0.0f;
+      rect += dpp_move<0x111>(row_prefix(cols));
+      float down = 0.0f, up = 0.0f;
+      double around = 0.0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool mine = on && (!kHalfK || (j >> 2) == i / TK);
+        down += mine ? qs[j] : 0.0f;
+        up += mine ? ks[j] : 0.0f;
+        if (!kHalfK || j < 4) around += x[j];
+      }
+      float dg = float(double(rect) + wave_from(down) + wave_before(up) + double(d.total) * around);
+      if (l >= live) dg = 0.0f;
+      if (p.dg && l < rows) p.dg[(b * p.seqlen + t0 + l) * p.heads + h] = dg;
       if (p.dg_sums) {
         const double sum = dpp_f64(wave_prefix_f64(dg), 63);
         if (l == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = float(sum);
@@ -279,7 +306,18 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           }
           put4(&sP[s * PP + 16 * i + 4 * g], a);
           put4(&sD[s * PP + 16 * i + 4 * g], d);
-          if (want_dg) {
+          if (want_dg && i == j) {
+            // Rows from column s's own step on, columns before it.
+            float rect = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float before = row_prefix(dpp_move<0x111>(wrow[e]));  // (row_shr 1)
+              rect += 4 * g + e >= r ? before : 0.0f;
+            }
+            rect += __shfl_xor(rect, 16, 64);
+            rect += __shfl_xor(rect, 32, 64);
+            if (g == 0) part.row[i][s] = rect;
+          } else if (want_dg) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float sum = sum_lanes<4>(wrow[e]);
