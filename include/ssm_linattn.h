@@ -31,6 +31,9 @@
  * 64-bit; with bf16 storage the weights of the pairs of a chunk are rounded to bf16 once as operands
  * of the matrix cores, and the states enter as two or three bf16 pieces.
  *
+ * A NaN or infinity of a step is in the results of that step and later ones, as the recurrence takes it, and in none
+ * before. (Where the recurrence gives an infinity, a result may be NaN.)
+ *
  * Results and workspace must overlap no other argument. Calls are asynchronous on `stream`, use
  * no atomics (bitwise reproducible) and allocate nothing; every check happens before any HIP call.
  * Calls that share a workspace must not overlap in time. Return SSM_OK, SSM_ERR_INVALID_ARG (also a

@@ -180,6 +180,48 @@ __device__ __forceinline__ la_f32x4 get4(const uint16_t* p) {
 }
 __device__ __forceinline__ la_f32x4 get4(const float* p) { return *reinterpret_cast<const la_f32x4*>(p); }
 
+// Whether any value of the operands given is infinite or NaN: a pair of steps that a chunk's product leaves out
+// by a weight of 0 would put 0 x infinity, NaN, into results that the value has no part in. Of every value the exponent
+// alone, plus one, carries into the sign's place where it is all ones.
+struct NotFinite {
+  uint32_t seen = 0, signs = 0;
+  __device__ __forceinline__ void add(const Frag<uint16_t>& f) {
+    for (uint32_t w : {f.w.x, f.w.y, f.w.z, f.w.w}) seen |= (w & 0x7f807f80u) + 0x00800080u;
+    signs = 0x80008000u;
+  }
+  __device__ __forceinline__ void add(const Frag<float>& f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) seen |= (__float_as_uint(f.v[i]) & 0x7f800000u) + 0x00800000u;
+    signs = 0x80000000u;
+  }
+  // In any lane of the wave.
+  __device__ __forceinline__ bool any() const { return __ballot((seen & signs) != 0) != 0; }
+};
+
+// x, such that nothing formed of it is formed ahead of a loop around it (where it would hold registers).
+__device__ __forceinline__ int not_ahead(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+__device__ __forceinline__ float widen_one(uint16_t v) { return bf16_lo(v); }
+__device__ __forceinline__ float widen_one(float v) { return v; }
+
+// acc += the sum over steps [from, to) of weight (at w + step * w_step) times four values (at x + step * x_step), those
+// steps alone: what a product over whole blocks of steps gives where every value is finite.
+template <typename Elem>
+__device__ __forceinline__ la_f32x4 steps_alone(const Elem* w, int w_step, const Elem* x, int x_step, int from, int to,
+                                                la_f32x4 acc) {
+#pragma unroll 1
+  for (int s = from; s < to; ++s) {
+    const float weight = widen_one(w[s * w_step]);
+    const la_f32x4 v = get4(x + s * x_step);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(weight, v[e], acc[e]);
+  }
+  return acc;
+}
+
 // A byte offset past every buffer: loads there read 0, stores are dropped. Loads and stores go
 // through buffer resources with it in the place of a branch, so that nothing but their use waits.
 constexpr uint32_t kLaOob = 0x80000000u;

@@ -19,6 +19,10 @@
 // (16 bits): in one its error would add to that of the weights. What is added to the state enters
 // in three pieces, all 24 bits, since the state is a result in fp32.
 //
+// Values that are not finite: a NaN or infinity is in the results of its own and later steps and in none before, as in
+// the recurrence, although a chunk's product passes over all pairs of its steps. (The check of a chunk's values
+// costs the whole-row forms between -3% and +1%: b8, 32 heads of 128 x 64 113.4 -> 109.8 us, fp32 b4 178.8 -> 180.1.)
+//
 // Measured, bf16: b4, 8 heads of 128 for 32 of 64, 2048 steps 80.4 us in all, 51 the forward, 29 the segments'
 // states, 7 the join (must move 106 MB, 21 us at a copy's rate; the three launches move 226); b1, 16 heads of
 // 128 x 128, 65536 steps 433, of which 323, 166 and 14 where each runs alone (must move 1076 MB, 210 us; they move 1750,
@@ -124,7 +128,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
     const float first = load_decay(gates, p.g_step, c0 * C, rows_of(c0));
     if (w == 3) decays[c0 & 1].set(first);
   }
-  fetch(c0);
+  if constexpr (kWhole) fetch(c0);
   for (int64_t c = c0; c < c1; ++c) {
     const int64_t t0 = c * C;
     const Buf to(out + t0 * out_step, kLaBytes);
@@ -132,6 +136,9 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
     const int live = end <= t0 ? 0 : end - t0 < C ? int(end - t0) : C;  // that hold steps
     if (live > 0) {
       const Decays<C>& dec = decays[c & 1];
+      // (Rows by elements take twice the registers on their way, and are loaded when their chunk begins: ahead of it they
+      // made the kernel spill. b2, 16 heads of 100 x 100, 2048 steps in bf16 97.7 us, ahead 116.)
+      if constexpr (!kWhole) fetch(c);
       lds_barrier();  // every wave has read the chunk before
       lq.store(sQ);
       lk.store(sK);
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
       // (ahead of the loads for the next chunk, which it would wait for)
       if (w == 3) decays[(c + 1) & 1].set(gate);
       gate = load_decay(gates, p.g_step, (c + 2) * C, rows_of(c + 2));
-      fetch(c + 1);
+      if constexpr (kWhole) fetch(c + 1);
       // The weights of the pairs s <= t, with the decay between them: tile (i, j) as rows s of
       // columns t, stored by rows t.
       const WaveTiles mine = wave_tiles<C>(w);
@@ -206,16 +213,33 @@ __global__ __launch_bounds__(kLaThreads, KP <= 128 ? 2 : 1) void linattn_fwd_ker
           for (int e = 0; e < 4; ++e) o[i][n][e] *= into;
       }
       lds_barrier();
-      // Then the pairs.
+      // Then the pairs. The weights of those above the diagonal are zeros, which a value that is not finite would turn to
+      // NaN: a wave that has one in its columns sums the pairs below one by one.
+      NotFinite odd;
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) {
-        Frag<Elem> f[T];
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-        for (int i = 2 * sb; i < T; ++i) f[i] = row_frag(sP, PP, 16 * i + r, 32 * sb);
+        for (int n = 0; n < NV; ++n) odd.add(vf[sb][n]);
+      if (__builtin_expect(!odd.any(), 1)) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int sb = 0; sb < SB; ++sb) {
+          Frag<Elem> f[T];
 #pragma unroll
-          for (int i = 2 * sb; i < T; ++i) o[i][n] = mma(vf[sb][n], f[i], o[i][n]);
+          for (int i = 2 * sb; i < T; ++i) f[i] = row_frag(sP, PP, 16 * i + r, 32 * sb);
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int i = 2 * sb; i < T; ++i) o[i][n] = mma(vf[sb][n], f[i], o[i][n]);
+        }
+      } else {
+        const int r1 = not_ahead(r), g1 = not_ahead(g);
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const int t = 16 * i + r1;
+            o[i][n] = steps_alone(sP + t * PP, 1, sV + 16 * (NV * w + n) + 4 * g1, VP, 0, t + 1, o[i][n]);
+          }
       }
 #pragma unroll
       for (int i = 0; i < T; ++i) {

@@ -1,0 +1,39 @@
+"""Values that are not finite in linear attention, the kernels in a CPU build: they reach what the recurrence
+takes them to, and no step before them."""
+import numpy as np
+import pytest
+
+from linattn_emulated import CLANG, build, rounded
+from linattn_values import BAD, check_forward
+from test_linattn_cpu import LARGE
+
+pytestmark = pytest.mark.skipif(CLANG is None, reason="clang++ not available")
+
+
+@pytest.fixture(scope="module", params=[{}, LARGE], ids=["small", "large"])
+def kernels(request, tmp_path_factory):
+    return build(str(tmp_path_factory.mktemp("linattn")), request.param)
+
+
+def inputs(io, L, hk, h, dk, dv, seed):
+    rng = np.random.default_rng(seed)
+    draw = lambda *s: rounded(rng.standard_normal(s), io)
+    state = lambda: rounded(rng.standard_normal((1, h, dv, dk)), "f32")
+    args = dict(q=draw(1, L, hk, dk), k=draw(1, L, hk, dk), v=draw(1, L, h, dv),
+                g=rounded(-0.1 * rng.random((1, L, h)), "f32"), initial_state=state())
+    return args, draw(1, L, h, dv), state()
+
+
+PLACES = [("v", (0, 45, 1, 5)), ("v", (0, 64, 0, 17)), ("v", (0, 0, 1, 0)), ("v", (0, 89, 0, 35)),
+          ("k", (0, 45, 0, 3)), ("q", (0, 45, 0, 19)), ("g", (0, 50, 1)), ("initial_state", (0, 1, 7, 9))]
+
+
+# (-inf in g is a reset.)
+CASES = [(what, index, bad) for what, index in PLACES for bad in BAD if (what, bad) != ("g", "-inf")]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("what,index,bad", CASES)
+def test_forward(kernels, io, what, index, bad):
+    args, _, _ = inputs(io, 90, 1, 2, 20, 36, 3)
+    check_forward(lambda **a: kernels.forward(io, **a), io, args, what, index, BAD[bad])
