@@ -31,8 +31,8 @@
  * 64-bit; with bf16 storage the weights of the pairs of a chunk are rounded to bf16 once as operands
  * of the matrix cores, and the states enter as two or three bf16 pieces.
  *
- * A NaN or infinity of a step is in the results of that step and later ones, as the recurrence takes it, and in none
- * before. (Where the recurrence gives an infinity, a result may be NaN.)
+ * A NaN or infinity is in the results that the recurrence and its adjoint take it to, and in no other: of the forward,
+ * those of its own and later steps. (Where the recurrence gives an infinity, a result may be NaN.)
  *
  * Results and workspace must overlap no other argument. Calls are asynchronous on `stream`, use
  * no atomics (bitwise reproducible) and allocate nothing; every check happens before any HIP call.

@@ -35,6 +35,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_linattn.h"
 #include "linattn_launch.h"
 
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   constexpr int T = C / 16, SB = C / 32, KB = KP / 32, VB = VP / 32;
   constexpr uint32_t E = sizeof(Elem);
   // The largest sizes keep fewer operands at a time, for want of registers.
-  constexpr int kUnroll = KB + VB > 8 ? 1 : 8;
+  static constexpr int kUnroll = KB + VB > 8 ? 1 : 8;
   // The 16-wide column tiles of dk and dv that a wave owns, for all steps; where there are only four,
   // one for half of the steps.
   constexpr bool kHalfK = KP < 128, kHalfV = VP < 128;
@@ -105,12 +107,13 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   constexpr bool kAhead = NK * VB <= 2;
   // Where they are not, two blocks of them at a time in bf16: b1, 16 heads of 128 x 128, 16384 steps, the whole
   // gradient: 584 us; all four, with 80 bytes a lane spilled, 660. (fp32, without spills: all, 623 against 635.)
-  constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
+  static constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
   __shared__ __attribute__((aligned(16))) Elem sP[C * PP], sD[C * PP];  // weights by rows s: scale D qk, scale D dov
   __shared__ __attribute__((aligned(16))) Decays<C> decays[2];          // of even and odd heads
   __shared__ DgParts<C> parts[2];
+  __shared__ int again;
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
@@ -171,9 +174,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
       const DgParts<C>& d = parts[hh & 1];
       const int h = hk * p.group + hh, t = l < C ? l : C - 1, i = t / 16;
       const bool on = l < C;
-      // W's rectangle: in the block's own tile; of the tiles (i, j) the rows from t on, and those (x, j), j < i < x, which
-      // lie in it whole; of the tiles (x, i) the columns before t.
-      // (Everything is loaded first, whatever comes of it, so that the loads are one wait.)
+      // W's rectangle: in the block's own tile; of the tiles (i, j) the rows from t on, and those (y, j), j < i < y,
+      // which lie in it whole; of the tiles (y, i) the columns before t. (Everything is loaded first, whatever comes of
+      // it, so that the loads are one wait.)
       float row[T], col[T], qs[8], ks[8], x[8];
 #pragma unroll
       for (int j = 0; j < T; ++j) {
@@ -219,13 +222,15 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
         if (l == 0) p.dg_sums[(b * p.chunks + c) * p.heads + h] = float(sum);
       }
     };
-    const bool want_dg = p.dg || p.dg_sums;
-
-    float gate = gate_of(1);
-    {
+    const bool any_dg = p.dg || p.dg_sums;
+    NotFinite odd;  // of this thread's values of q, k and dout
+    float gate = 0.0f;
+    auto begin = [&] {
+      gate = gate_of(1);
       const float first = gate_of(0);
       if (w == 6) decays[0].set(first);
-    }
+    };
+    begin();
     {
       TileLoad<Elem, C, KP, kWhole, kBwdThreads> lq, lk;
       lq.load(static_cast<const Elem*>(p.q.p) + b * p.q.batch + hk * p.q.head + t0 * p.q.step,
@@ -233,6 +238,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
       lk.load(static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head + t0 * p.k.step,
               uint32_t(p.k.step) * E, live, p.dk);
       fetch(0);
+      lq.look(odd);
+      lk.look(odd);
       lq.store(sQ);
       lk.store(sK);
     }
@@ -244,247 +251,284 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
         put4(&sD[(16 * (i + 1) + r) * PP + 16 * i + 4 * g], la_f32x4{0, 0, 0, 0});
       }
     }
+    if (threadIdx.x == 0) again = 0;
 
-    for (int hh = 0; hh < p.group; ++hh) {
-      const int h = hk * p.group + hh;
-      const int64_t state = ((b * p.heads + h) * p.chunks + c) * p.state_floats;
-      const Buf S(p.states + state, uint32_t(p.state_floats) * 4), R(p.adjoints + state, uint32_t(p.state_floats) * 4);
-      const Decays<C>& dec = decays[hh & 1];
-      DgParts<C>& part = parts[hh & 1];
-      // Row k of a state, values v of a block of 32: operands of dq and dk.
-      auto state_at = [&](int n, int vb) {
-        const int k = 16 * (kt + n) + r, v = 32 * vb + 8 * g;
-        return k < p.kpad && v < p.vpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
-      };
-      uint4 fs[kAhead ? NK : 1][VB][2], fr[kAhead ? NK : 1][VB][2];
+    // All heads. alone: dq, dk and dv only, the pairs of steps one by one.
+    auto heads = [&](auto one_by_one, int r, int g) {
+      constexpr bool alone = decltype(one_by_one)::value;
+      const bool want_dg = !alone && any_dg;
+      for (int hh = 0; hh < p.group; ++hh) {
+        const int h = hk * p.group + hh;
+        const int64_t state = ((b * p.heads + h) * p.chunks + c) * p.state_floats;
+        const Buf S(p.states + state, uint32_t(p.state_floats) * 4), R(p.adjoints + state, uint32_t(p.state_floats) * 4);
+        const Decays<C>& dec = decays[hh & 1];
+        DgParts<C>& part = parts[hh & 1];
+        // Row k of a state, values v of a block of 32: operands of dq and dk.
+        auto state_at = [&](int n, int vb) {
+          const int k = 16 * (kt + n) + r, v = 32 * vb + 8 * g;
+          return k < p.kpad && v < p.vpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
+        };
+        uint4 fs[kAhead ? NK : 1][VB][2], fr[kAhead ? NK : 1][VB][2];
 
-      lds_barrier();  // every wave has read the head before
-      lv.store(sV);
-      lo.store(sO);
-      lds_barrier();
-      // (ahead of the loads, which it would wait for)
-      if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set(gate);
-      if constexpr (kAhead) {
+        lds_barrier();  // every wave has read the head before
+        if constexpr (!alone) lo.look(odd);
+        lv.store(sV);
+        lo.store(sO);
+        lds_barrier();
+        // (ahead of the loads, which it would wait for)
+        if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set(gate);
+        if constexpr (kAhead && !alone) {
 #pragma unroll
-        for (int n = 0; n < NK; ++n)
+          for (int n = 0; n < NK; ++n)
 #pragma unroll
-          for (int vb = 0; vb < VB; ++vb) {
-            const uint32_t off = state_at(n, vb);
+            for (int vb = 0; vb < VB; ++vb) {
+              const uint32_t off = state_at(n, vb);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              fs[n][vb][e] = S.load16(off + 16u * e);
-              fr[n][vb][e] = R.load16(off + 16u * e);
+              for (int e = 0; e < 2; ++e) {
+                fs[n][vb][e] = S.load16(off + 16u * e);
+                fr[n][vb][e] = R.load16(off + 16u * e);
+              }
             }
-          }
-      }
-      gate = gate_of(hh + 2);
-      fetch(hh + 1);
+        }
+        gate = gate_of(hh + 2);
+        fetch(hh + 1);
 
-      // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
-      const BwdTiles mine = bwd_tiles<C>(w);
-      if (mine.j1 > mine.j0) {
-        const int i = mine.i;
-        for (int j = mine.j0; j < mine.j1; ++j) {
-          la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
+        // The pairs: tile (i, j) as rows t of columns s, stored by rows s.
+        const BwdTiles mine = bwd_tiles<C>(w);
+        if (mine.j1 > mine.j0) {
+          const int i = mine.i;
+          for (int j = mine.j0; j < mine.j1; ++j) {
+            la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
 #pragma unroll kUnroll
-          for (int kb = 0; kb < KB; ++kb)
-            a = mma(row_frag(sQ, QP, 16 * i + r, 32 * kb), row_frag(sK, QP, 16 * j + r, 32 * kb), a);
+            for (int kb = 0; kb < KB; ++kb)
+              a = mma(row_frag(sQ, QP, 16 * i + r, 32 * kb), row_frag(sK, QP, 16 * j + r, 32 * kb), a);
 #pragma unroll kUnroll
-          for (int vb = 0; vb < VB; ++vb)
-            d = mma(row_frag(sO, OP, 16 * i + r, 32 * vb), row_frag(sV, OP, 16 * j + r, 32 * vb), d);
-          const int s = 16 * j + r;
-          float keep[4], wrow[4], wcol = 0.0f;
-          dec.onwards(s, 16 * i + 4 * g, keep);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = 16 * i + 4 * g + e;
-            const float m = p.scale * keep[e], da = d[e] * m, aa = a[e] * m, ww = a[e] * da;
-            d[e] = s <= t ? da : 0.0f;
-            a[e] = s <= t ? aa : 0.0f;
-            wrow[e] = s < t ? ww : 0.0f;
-            wcol += wrow[e];
-          }
-          put4(&sP[s * PP + 16 * i + 4 * g], a);
-          put4(&sD[s * PP + 16 * i + 4 * g], d);
-          if (want_dg && i == j) {
-            // Rows from column s's own step on, columns before it.
-            float rect = 0.0f;
+            for (int vb = 0; vb < VB; ++vb)
+              d = mma(row_frag(sO, OP, 16 * i + r, 32 * vb), row_frag(sV, OP, 16 * j + r, 32 * vb), d);
+            const int s = 16 * j + r;
+            float keep[4], wrow[4], wcol = 0.0f;
+            dec.onwards(s, 16 * i + 4 * g, keep);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float before = row_prefix(dpp_move<0x111>(wrow[e]));  // (row_shr 1)
-              rect += 4 * g + e >= r ? before : 0.0f;
+              const int t = 16 * i + 4 * g + e;
+              const float m = p.scale * keep[e], da = d[e] * m, aa = a[e] * m, ww = a[e] * da;
+              d[e] = s <= t ? da : 0.0f;
+              a[e] = s <= t ? aa : 0.0f;
+              wrow[e] = s < t ? ww : 0.0f;
+              wcol += wrow[e];
             }
-            rect += __shfl_xor(rect, 16, 64);
-            rect += __shfl_xor(rect, 32, 64);
-            if (g == 0) part.row[i][s] = rect;
-          } else if (want_dg) {
+            put4(&sP[s * PP + 16 * i + 4 * g], a);
+            put4(&sD[s * PP + 16 * i + 4 * g], d);
+            if (want_dg && i == j) {
+              // Rows from column s's own step on, columns before it.
+              float rect = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float sum = sum_lanes<4>(wrow[e]);
-              if (r == 0) part.row[j][16 * i + 4 * g + e] = sum;
+              for (int e = 0; e < 4; ++e) {
+                const float before = row_prefix(dpp_move<0x111>(wrow[e]));  // (row_shr 1)
+                rect += 4 * g + e >= r ? before : 0.0f;
+              }
+              rect += __shfl_xor(rect, 16, 64);
+              rect += __shfl_xor(rect, 32, 64);
+              if (g == 0) part.row[i][s] = rect;
+            } else if (want_dg) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float sum = sum_lanes<4>(wrow[e]);
+                if (r == 0) part.row[j][16 * i + 4 * g + e] = sum;
+              }
+              wcol += __shfl_xor(wcol, 16, 64);
+              wcol += __shfl_xor(wcol, 32, 64);
+              if (g == 0) part.col[i][s] = wcol;
             }
-            wcol += __shfl_xor(wcol, 16, 64);
-            wcol += __shfl_xor(wcol, 32, 64);
-            if (g == 0) part.col[i][s] = wcol;
           }
         }
-      }
-      if (w == 7 && hh > 0 && want_dg) finish(hh - 1);
-      lds_barrier();
+        if (w == 7 && hh > 0 && want_dg) finish(hh - 1);
+        lds_barrier();
 
-      // Column v of R, values k of a block of 32: operands of dv.
-      float rk[NV * KB <= 4 ? NV : 1][KB][8];
-      auto load_column = [&](int n, int kb, float (&x)[8]) {
-        const int v = 16 * (vt + n) + r, k = 32 * kb + 8 * g;
-        const uint32_t off = v < p.vpad && k < p.kpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
+        // Column v of R, values k of a block of 32: operands of dv.
+        float rk[NV * KB <= 4 ? NV : 1][KB][8];
+        auto load_column = [&](int n, int kb, float (&x)[8]) {
+          const int v = 16 * (vt + n) + r, k = 32 * kb + 8 * g;
+          const uint32_t off = v < p.vpad && k < p.kpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(R.load4(off + uint32_t(e * p.vpad) * 4u));
-      };
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(R.load4(off + uint32_t(e * p.vpad) * 4u));
+        };
 
-      // dq and dk of this wave's columns of dk.
-      float dots = 0.0f;  // <R, S> over them
-      float qs[TK], ks[TK];
+        // dq and dk of this wave's columns of dk.
+        float dots = 0.0f;  // <R, S> over them
+        float qs[TK], ks[TK];
 #pragma unroll
-      for (int i = 0; i < TK; ++i) qs[i] = ks[i] = 0.0f;
+        for (int i = 0; i < TK; ++i) qs[i] = ks[i] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NK; ++n) {
-        const int k0 = 16 * (kt + n);
-        la_f32x4 xq[TK], xk[TK];
+        for (int n = 0; n < NK; ++n) {
+          const int k0 = 16 * (kt + n);
+          la_f32x4 xq[TK], xk[TK];
 #pragma unroll
-        for (int i = 0; i < TK; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
+          for (int i = 0; i < TK; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
 #pragma unroll kStateUnroll
-        for (int vb = 0; vb < VB; ++vb) {
-          uint4 words[2][2];
-          if constexpr (kAhead) {
+          for (int vb = 0; vb < VB; ++vb) {
+            uint4 words[2][2];
+            if constexpr (kAhead && !alone) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              words[0][e] = fs[n][vb][e];
-              words[1][e] = fr[n][vb][e];
+              for (int e = 0; e < 2; ++e) {
+                words[0][e] = fs[n][vb][e];
+                words[1][e] = fr[n][vb][e];
+              }
+            } else {
+              const uint32_t off = state_at(n, vb);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                words[0][e] = S.load16(off + 16u * e);
+                words[1][e] = R.load16(off + 16u * e);
+              }
             }
-          } else {
-            const uint32_t off = state_at(n, vb);
+            float sv[8], rv[8];
+            widen_raw16<float>(words[0][0], sv);
+            widen_raw16<float>(words[0][1], sv + 4);
+            widen_raw16<float>(words[1][0], rv);
+            widen_raw16<float>(words[1][1], rv + 4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              words[0][e] = S.load16(off + 16u * e);
-              words[1][e] = R.load16(off + 16u * e);
+            for (int e = 0; e < 8; ++e) dots = __builtin_fmaf(sv[e], rv[e], dots);
+            Pieces<Elem, 3> ps, pr;
+            ps.split(sv);
+            pr.split(rv);
+#pragma unroll
+            for (int i = 0; i < TK; ++i) {
+              const Frag<Elem> fo = row_frag(sO, OP, 16 * (ik + i) + r, 32 * vb),
+                               fv = row_frag(sV, OP, 16 * (ik + i) + r, 32 * vb);
+#pragma unroll
+              for (int e = ps.kCount - 1; e >= 0; --e) {  // the small ones first, the two sums in turn
+                xq[i] = mma(piece(ps, e), fo, xq[i]);
+                xk[i] = mma(piece(pr, e), fv, xk[i]);
+              }
             }
           }
-          float sv[8], rv[8];
-          widen_raw16<float>(words[0][0], sv);
-          widen_raw16<float>(words[0][1], sv + 4);
-          widen_raw16<float>(words[1][0], rv);
-          widen_raw16<float>(words[1][1], rv + 4);
+          // (by now the states' registers are free again)
+          if (NV * KB <= 4 && n == NK - 1) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dots = __builtin_fmaf(sv[e], rv[e], dots);
-          Pieces<Elem, 3> ps, pr;
-          ps.split(sv);
-          pr.split(rv);
+            for (int m = 0; m < NV; ++m)
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb) load_column(m, kb, rk[NV * KB <= 4 ? m : 0][kb]);
+          }
 #pragma unroll
           for (int i = 0; i < TK; ++i) {
-            const Frag<Elem> fo = row_frag(sO, OP, 16 * (ik + i) + r, 32 * vb),
-                             fv = row_frag(sV, OP, 16 * (ik + i) + r, 32 * vb);
+            const int t = 16 * (ik + i) + r;
+            const float into = dec.into[t] * p.scale, onto = dec.onto[t];
+            const la_f32x4 qv = get4(&sQ[t * QP + k0 + 4 * g]), kv = get4(&sK[t * QP + k0 + 4 * g]);
 #pragma unroll
-            for (int e = ps.kCount - 1; e >= 0; --e) {  // the small ones first, the two sums in turn
-              xq[i] = mma(piece(ps, e), fo, xq[i]);
-              xk[i] = mma(piece(pr, e), fv, xk[i]);
+            for (int e = 0; e < 4; ++e) {
+              xq[i][e] *= into;
+              xk[i][e] *= onto;
+              qs[i] = __builtin_fmaf(qv[e], xq[i][e], qs[i]);
+              ks[i] = __builtin_fmaf(kv[e], xk[i][e], ks[i]);
+              aq[n][i][e] += xq[i][e];
+              ak[n][i][e] += xk[i][e];
+            }
+          }
+#pragma unroll
+          for (int sb = 0; sb < SB; ++sb) {
+            const Frag<Elem> kf = col_frag(sK, QP, 32 * sb, k0), qf = col_frag(sQ, QP, 32 * sb, k0);
+            if constexpr (!alone) {
+#pragma unroll
+              for (int i = 0; i < TK; ++i) {
+                if ((ik + i) / 2 >= sb) aq[n][i] = mma(kf, col_frag(sD, PP, 32 * sb, 16 * (ik + i)), aq[n][i]);
+                if ((ik + i) / 2 <= sb) ak[n][i] = mma(qf, row_frag(sD, PP, 16 * (ik + i) + r, 32 * sb), ak[n][i]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < TK; ++i) {
+                const int s = 16 * (ik + i) + r, b0 = 32 * sb, b1 = b0 + 32, col = k0 + 4 * g;
+                aq[n][i] = steps_alone(sD + s, PP, sK + col, QP, b0, s < b1 ? s + 1 : b1, aq[n][i]);
+                ak[n][i] = steps_alone(sD + s * PP, 1, sQ + col, QP, s > b0 ? s : b0, b1, ak[n][i]);
+              }
             }
           }
         }
-        // (by now the states' registers are free again)
-        if (NV * KB <= 4 && n == NK - 1) {
+        // dv of this wave's columns of dv.
 #pragma unroll
-          for (int m = 0; m < NV; ++m)
+        for (int n = 0; n < NV; ++n) {
+          const int v0 = 16 * (vt + n);
+          la_f32x4 av[TV];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) load_column(m, kb, rk[NV * KB <= 4 ? m : 0][kb]);
-        }
-#pragma unroll
-        for (int i = 0; i < TK; ++i) {
-          const int t = 16 * (ik + i) + r;
-          const float into = dec.into[t] * p.scale, onto = dec.onto[t];
-          const la_f32x4 qv = get4(&sQ[t * QP + k0 + 4 * g]), kv = get4(&sK[t * QP + k0 + 4 * g]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            xq[i][e] *= into;
-            xk[i][e] *= onto;
-            qs[i] = __builtin_fmaf(qv[e], xq[i][e], qs[i]);
-            ks[i] = __builtin_fmaf(kv[e], xk[i][e], ks[i]);
-            aq[n][i][e] += xq[i][e];
-            ak[n][i][e] += xk[i][e];
-          }
-        }
-#pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-          const Frag<Elem> kf = col_frag(sK, QP, 32 * sb, k0), qf = col_frag(sQ, QP, 32 * sb, k0);
-#pragma unroll
-          for (int i = 0; i < TK; ++i) {
-            if ((ik + i) / 2 >= sb) aq[n][i] = mma(kf, col_frag(sD, PP, 32 * sb, 16 * (ik + i)), aq[n][i]);
-            if ((ik + i) / 2 <= sb) ak[n][i] = mma(qf, row_frag(sD, PP, 16 * (ik + i) + r, 32 * sb), ak[n][i]);
-          }
-        }
-      }
-      // dv of this wave's columns of dv.
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const int v0 = 16 * (vt + n);
-        la_f32x4 av[TV];
-#pragma unroll
-        for (int i = 0; i < TV; ++i) av[i] = la_f32x4{0, 0, 0, 0};
+          for (int i = 0; i < TV; ++i) av[i] = la_f32x4{0, 0, 0, 0};
 #pragma unroll kUnroll
-        for (int kb = 0; kb < KB; ++kb) {
-          Pieces<Elem, 2> pr;
-          if constexpr (NV * KB <= 4) {
-            pr.split(rk[n][kb]);
-          } else {
-            float x[8];
-            load_column(n, kb, x);
-            pr.split(x);
+          for (int kb = 0; kb < KB; ++kb) {
+            Pieces<Elem, 2> pr;
+            if constexpr (NV * KB <= 4) {
+              pr.split(rk[n][kb]);
+            } else {
+              float x[8];
+              load_column(n, kb, x);
+              pr.split(x);
+            }
+#pragma unroll
+            for (int i = 0; i < TV; ++i) {
+              const Frag<Elem> fk = row_frag(sK, QP, 16 * (iv + i) + r, 32 * kb);
+#pragma unroll
+              for (int e = pr.kCount - 1; e >= 0; --e) av[i] = mma(piece(pr, e), fk, av[i]);
+            }
           }
 #pragma unroll
           for (int i = 0; i < TV; ++i) {
-            const Frag<Elem> fk = row_frag(sK, QP, 16 * (iv + i) + r, 32 * kb);
+            const float onto = dec.onto[16 * (iv + i) + r];
 #pragma unroll
-            for (int e = pr.kCount - 1; e >= 0; --e) av[i] = mma(piece(pr, e), fk, av[i]);
+            for (int e = 0; e < 4; ++e) av[i][e] *= onto;
+          }
+#pragma unroll
+          for (int sb = 0; sb < SB; ++sb) {
+            const Frag<Elem> of = col_frag(sO, OP, 32 * sb, v0);
+            if constexpr (!alone) {
+#pragma unroll
+              for (int i = 0; i < TV; ++i)
+                if ((iv + i) / 2 <= sb) av[i] = mma(of, row_frag(sP, PP, 16 * (iv + i) + r, 32 * sb), av[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < TV; ++i) {
+                const int s = 16 * (iv + i) + r, b0 = 32 * sb, b1 = b0 + 32;
+                av[i] = steps_alone(sP + s * PP, 1, sO + v0 + 4 * g, OP, s > b0 ? s : b0, b1, av[i]);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < TV; ++i) put(dv_of(h), v_step, iv + i, v0 + 4 * g, p.dv, av[i]);
+        }
+        if (want_dg) {
+#pragma unroll
+          for (int i = 0; i < TK; ++i) {
+            float a = qs[i], d = ks[i];
+            a += __shfl_xor(a, 16, 64);
+            a += __shfl_xor(a, 32, 64);
+            d += __shfl_xor(d, 16, 64);
+            d += __shfl_xor(d, 32, 64);
+            if (g == 0) {
+              part.qs[w][16 * (ik + i) + r] = a;
+              part.ks[w][16 * (ik + i) + r] = d;
+            }
+          }
+          dots = sum_lanes<6>(dots);
+          if (l == 0) {
+            part.x[w] = dots;
+            if (w == 0) part.total = dec.total;
           }
         }
-#pragma unroll
-        for (int i = 0; i < TV; ++i) {
-          const float onto = dec.onto[16 * (iv + i) + r];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) av[i][e] *= onto;
-        }
-#pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-          const Frag<Elem> of = col_frag(sO, OP, 32 * sb, v0);
-#pragma unroll
-          for (int i = 0; i < TV; ++i)
-            if ((iv + i) / 2 <= sb) av[i] = mma(of, row_frag(sP, PP, 16 * (iv + i) + r, 32 * sb), av[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < TV; ++i) put(dv_of(h), v_step, iv + i, v0 + 4 * g, p.dv, av[i]);
       }
-      if (want_dg) {
+    };
+    heads(std::false_type{}, r, g);
+    // The weights of the pairs above the diagonal are zeros, which a value of q, k or dout that is not finite turns to
+    // NaN in steps that it has no part in: a workgroup that met one forms dq, dk and dv again. (Afterwards, since a
+    // branch around the products took the registers of the loads on their way. b4, 8 heads of 128 for 32 of 64, 2048
+    // steps, the whole gradient: 262.8 us, 260.4 without this, 495 with the branch.)
+    if (odd.any() && l == 0) again = 1;
+    lds_barrier();
+    if (any_dg && w == 7) finish(p.group - 1);
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(again), 0)) {
 #pragma unroll
-        for (int i = 0; i < TK; ++i) {
-          float a = qs[i], d = ks[i];
-          a += __shfl_xor(a, 16, 64);
-          a += __shfl_xor(a, 32, 64);
-          d += __shfl_xor(d, 16, 64);
-          d += __shfl_xor(d, 32, 64);
-          if (g == 0) {
-            part.qs[w][16 * (ik + i) + r] = a;
-            part.ks[w][16 * (ik + i) + r] = d;
-          }
-        }
-        dots = sum_lanes<6>(dots);
-        if (l == 0) {
-          part.x[w] = dots;
-          if (w == 0) part.total = dec.total;
-        }
-      }
-    }
-    if (want_dg) {
-      lds_barrier();
-      if (w == 7) finish(p.group - 1);
+      for (int n = 0; n < NK; ++n)
+#pragma unroll
+        for (int i = 0; i < TK; ++i) aq[n][i] = ak[n][i] = la_f32x4{0, 0, 0, 0};
+      begin();
+      fetch(0);
+      heads(std::true_type{}, not_ahead(r), not_ahead(g));
     }
   }
 #pragma unroll

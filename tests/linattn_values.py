@@ -41,3 +41,23 @@ def check_forward(call, io, args, what, index, bad, lengths=None):
     assert not np.isfinite(ref[0]).all() and np.isfinite(ref[0]).any()
     only_where(got[0], ref[0], ab[0], io, n, f"out, {what} {bad}")
     only_where(got[1], ref[1], ab[1], "f32", n, f"final state, {what} {bad}")
+
+
+def check_backward(call, io, args, dout, dfinal, what, index, bad, lengths=None):
+    """As check_forward; `what` may be dout or dfinal too. call(dout=..., dfinal=..., ...) gives the gradients, dg of
+    each step."""
+    dk, dv, L = args["q"].shape[3], args["v"].shape[3], args["q"].shape[1]
+    n = roundings(dk, dv, L)
+    dirty = dict(args, dout=dout, dfinal=dfinal)
+    clean = dict(dirty)
+    dirty[what], clean[what] = place(dirty[what], index, bad)
+    with np.errstate(all="ignore"):
+        ref = ol.linattn_bwd_ref(**dirty, lengths=lengths)
+        ab = ol.linattn_bwd_ref(**{k: x if k == "g" or x is None else np.abs(x) for k, x in clean.items()},
+                                lengths=lengths)
+        got = call(**dirty, lengths=lengths)
+    assert any(not np.isfinite(x).all() for x in ref.values()) and any(np.isfinite(x).any() for x in ref.values())
+    for name in ("dq", "dk", "dv"):
+        only_where(got[name], ref[name], ab[name], io, n, f"{name}, {what} {bad}")
+    only_where(got["dinitial"], ref["dinitial"], ab["dinitial"], "f32", n, f"dinitial, {what} {bad}")
+    only_where(got["dg"], ref["dg"], ab["dg"], "f32", 2 * n, f"dg, {what} {bad}")

@@ -7,7 +7,7 @@ import pytest
 import selective_state_space_fwd_amd as ssm
 from block_util import dtype
 from gpu_util import announce, host, torch
-from linattn_values import BAD, check_forward
+from linattn_values import BAD, check_backward, check_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +54,27 @@ def test_forward(shape, io):
             index = tuple(index)
             announce(f"linattn {shape} {io} {bad} in {what} at {index}")
             check_forward(forward(io), io, args, what, index, BAD[bad])
+
+
+def backward(io):
+    def call(q, k, v, dout, g, initial_state, dfinal, lengths=None):
+        d = ssm.linattn_backward(device(q, io), device(k, io), device(v, io), device(dout, io), device(g),
+                                 initial_state=device(initial_state), dfinal=device(dfinal))
+        return {n: host(x) for n, x in d.items()}
+    return call
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients(shape, io):
+    args, dout, dfinal = inputs(io, shape, 74)
+    rng = np.random.default_rng(75)
+    arrays = dict(args, dout=dout, dfinal=dfinal)
+    for bad in BAD:
+        for what in ("v", "k", "k", "q", "q", "dout", "dout", "initial_state", "dfinal"):
+            index = tuple(int(rng.integers(n)) for n in arrays[what].shape)
+            announce(f"linattn_backward {shape} {io} {bad} in {what} at {index}")
+            check_backward(backward(io), io, args, dout, dfinal, what, index, BAD[bad])
 
 
 def test_uninitialised_padding():

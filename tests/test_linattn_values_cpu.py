@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from linattn_emulated import CLANG, build, rounded
-from linattn_values import BAD, check_forward
+from linattn_values import BAD, check_backward, check_forward
 from test_linattn_cpu import LARGE
 
 pytestmark = pytest.mark.skipif(CLANG is None, reason="clang++ not available")
@@ -37,3 +37,23 @@ CASES = [(what, index, bad) for what, index in PLACES for bad in BAD if (what, b
 def test_forward(kernels, io, what, index, bad):
     args, _, _ = inputs(io, 90, 1, 2, 20, 36, 3)
     check_forward(lambda **a: kernels.forward(io, **a), io, args, what, index, BAD[bad])
+
+
+GRADIENT_PLACES = PLACES[:6] + [("k", (0, 64, 0, 0)), ("q", (0, 20, 0, 8)), ("dout", (0, 45, 1, 5)), ("dout", (0, 63, 0, 35)),
+                                ("initial_state", (0, 1, 7, 9)), ("dfinal", (0, 0, 3, 4))]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("what,index", GRADIENT_PLACES)
+def test_gradients(kernels, io, what, index, bad):
+    args, dout, dfinal = inputs(io, 90, 1, 2, 20, 36, 4)
+    check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, what, index, BAD[bad])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("what,index", [("k", (0, 20, 0, 3)), ("dout", (0, 40, 0, 100)), ("q", (0, 50, 0, 1)),
+                                        ("v", (0, 9, 1, 64))])
+def test_gradients_of_large_heads(kernels, io, what, index):
+    args, dout, dfinal = inputs(io, 66, 1, 2, 72, 130, 5)
+    check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, what, index, np.nan)
