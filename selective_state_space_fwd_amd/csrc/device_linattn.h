@@ -366,7 +366,7 @@ __device__ __forceinline__ float wave_from(float v) {
   return v + (row <= 2 ? c : 0.0f) + (row <= 1 ? b : 0.0f) + (row <= 0 ? a : 0.0f);
 }
 // The log decay of a step in units of log 2. Below -1e4 it is -1e4, whose exponential is zero all
-// the same, so that a reset (-inf) leaves finite sums; NaN stays.
+// the same, so that a reset (-inf) leaves finite sums.
 __device__ __forceinline__ double log2_decay(float g) {
   const float x = g < -1e4f ? -1e4f : g;
   return double(x) * 1.4426950408889634074;
@@ -396,6 +396,24 @@ struct Decays {
       if (l == 0) total = exp2_hw(float(all));
     }
     return all;
+  }
+  // As set, for the gradient, where a NaN or infinite decay must not be between steps that both lie behind it (in the
+  // forward, and in the states, it is in all that is behind it anyway): it is kept out of the sums, and is NaN in
+  // `into`, `onto` and `total`, of which each result that such a decay is in has one.
+  __device__ __forceinline__ void set_apart(float step) {
+    if (__builtin_expect(set(step) < 1e30, 1)) return;
+    const int l = threadIdx.x & 63;
+    const bool counts = step <= 1e4f;
+    const unsigned long long odd = __ballot(!counts), from = odd & ((2ull << l) - 1), behind = odd >> l >> 1;
+    const double cs = wave_prefix_f64(counts ? log2_decay(step) : 0.0), all = dpp_f64(cs, C - 1);
+    const float nan = __builtin_nanf("");
+    if (l < C) {
+      const float h = float(cs);
+      sum[l] = Sum{h, float(cs - double(h))};
+      into[l] = from ? nan : exp2_hw(h);
+      onto[l] = behind ? nan : exp2_hw(float(all - cs));
+      if (l == 0) total = nan;
+    }
   }
   // From s0 + e to t, e < 4. All four whatever comes of them: a condition around one would put its
   // loads and exponential in a branch of their own.

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
     auto begin = [&] {
       gate = gate_of(1);
       const float first = gate_of(0);
-      if (w == 6) decays[0].set(first);
+      if (w == 6) decays[0].set_apart(first);
     };
     begin();
     {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
         lo.store(sO);
         lds_barrier();
         // (ahead of the loads, which it would wait for)
-        if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set(gate);
+        if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set_apart(gate);
         if constexpr (kAhead && !alone) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)

@@ -77,6 +77,19 @@ def test_gradients(shape, io):
             check_backward(backward(io), io, args, dout, dfinal, what, index, BAD[bad])
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_gradients_of_decays(shape, io):
+    args, dout, dfinal = inputs(io, shape, 76)
+    rng = np.random.default_rng(77)
+    args["g"][0, shape[0] // 2] = -np.inf  # (a reset does not hide it)
+    for bad in ("nan", "inf"):
+        for _ in range(2):
+            index = tuple(int(rng.integers(n)) for n in args["g"].shape)
+            announce(f"linattn_backward {shape} {io} {bad} in g at {index}")
+            check_backward(backward(io), io, args, dout, dfinal, "g", index, BAD[bad])
+
+
 def test_uninitialised_padding():
     """A prompt padded behind its end with whatever memory holds, the caller cutting the results: the rows before
     are those of the prompt alone."""

@@ -57,3 +57,15 @@ def test_gradients(kernels, io, what, index, bad):
 def test_gradients_of_large_heads(kernels, io, what, index):
     args, dout, dfinal = inputs(io, 66, 1, 2, 72, 130, 5)
     check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, what, index, np.nan)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("index", [(0, 0, 0), (0, 33, 1), (0, 50, 1), (0, 63, 0), (0, 64, 1), (0, 89, 0)])
+def test_gradients_of_decays(kernels, io, bad, index):
+    """A decay that is not finite is in dq from its step on, in dk and dv before it, in every dg of its head and in
+    dinitial, but in no dk and dv from its step on and in no dq before."""
+    args, dout, dfinal = inputs(io, 90, 1, 2, 20, 36, 6)
+    args["g"][0, 70, index[2]] = -np.inf  # a reset after or before it does not hide it
+    check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, "g", index, BAD[bad])
+    check_forward(lambda **a: kernels.forward(io, **a), io, args, "g", index, BAD[bad])
