@@ -31,16 +31,17 @@
  * 64-bit; with bf16 storage the weights of the pairs of a chunk are rounded to bf16 once as operands
  * of the matrix cores, and the states enter as two or three bf16 pieces.
  *
- * A NaN or infinity is in the results that the recurrence and its adjoint take it to, and in no other: of the forward,
- * those of its own and later steps. (Where the recurrence gives an infinity, a result may be NaN.)
+ * A NaN or infinity is in the results that the recurrence and its adjoint take it to, and in no
+ * other: of the forward, those of its own and later steps. Where the recurrence gives an infinity, a
+ * result may be NaN: with bf16 storage an infinite v, or a state above 3.39e38, gives NaN.
  *
  * Results and workspace must overlap no other argument. Calls are asynchronous on `stream`, use
  * no atomics (bitwise reproducible) and allocate nothing; every check happens before any HIP call.
  * Calls that share a workspace must not overlap in time. Return SSM_OK, SSM_ERR_INVALID_ARG (also a
  * workspace too small, heads no multiple of qk_heads), SSM_ERR_UNSUPPORTED (dk or dv outside [1, 256],
  * batch above 65535, steps of an array 16 MiB apart or more, sizes past int64 or a grid of 2^32 - 1
- * work-items, a storage type other than fp32/bf16), SSM_ERR_MISALIGNED (a pointer not aligned to its element size, a workspace not to 256
- * bytes) or SSM_ERR_HIP.
+ * work-items, a storage type other than fp32/bf16), SSM_ERR_MISALIGNED (a pointer not aligned to its
+ * element size, a workspace not to 256 bytes) or SSM_ERR_HIP.
  */
 #ifndef SSM_LINATTN_H
 #define SSM_LINATTN_H

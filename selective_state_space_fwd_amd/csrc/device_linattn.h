@@ -58,7 +58,9 @@ __device__ __forceinline__ la_f32x4 mma(const Frag<float>& a, const Frag<float>&
 
 // Eight fp32 values as an operand next to storage type Elem: N bf16 pieces, each the rounding of
 // what the ones before leave (8 bits of the significand each, so three hold all 24), or the
-// values themselves in fp32.
+// values themselves in fp32. What an infinity leaves is NaN, so that an infinite state or value (above bf16's
+// largest, 3.39e38, too) gives NaN where fp32 storage may give an infinity: a number in that place would be
+// a v_max_f32 more for each value, 1 to 3% of the calls (b8, 32 heads of 128 x 64: 109.2 us, 112.8 with it).
 template <typename Elem, int N>
 struct Pieces;
 template <int N>

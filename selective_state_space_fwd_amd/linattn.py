@@ -191,9 +191,11 @@ def linattn(q, k, v, g=None, scale: Optional[float] = None, initial_state=None, 
     g: log decays, [batch, seqlen, heads] or one for each head [heads], float32 (None: no decay);
     scale: 1 / sqrt(dk) by default; initial_state: [batch, heads, dv, dk] float32 (None: zero);
     lengths: [batch] int32, the steps of each row (clamped to [0, seqlen]; behind them out is 0, the
-    state stays and nothing is read). Returns (out [batch, seqlen, heads, dv] contiguous in v's
-    dtype, final_state as initial_state). workspace: a uint8 device tensor of at least
-    ssm_linattn_fwd_workspace_bytes(...) bytes, allocated here when None."""
+    state stays and nothing is read). A NaN or infinity is in the results of its own and later steps
+    alone (where the recurrence gives an infinity, a result may be NaN). Returns (out [batch,
+    seqlen, heads, dv] contiguous in v's dtype, final_state as initial_state). workspace: a uint8
+    device tensor of at least ssm_linattn_fwd_workspace_bytes(...) bytes, allocated here when
+    None."""
     r = _native().linattn(q, k, v, g, scale, initial_state, lengths, out, final_state,
                           return_final_state, workspace)
     if r is not None:
