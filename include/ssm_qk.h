@@ -16,7 +16,8 @@
  *   q_weight, k_weight : [dim] fp32 or NULL
  *   cos, sin  : [table_rows, rot / 2] fp32, contiguous (NULL where rot is 0)
  *   positions : [batch, seqlen] int32, or NULL: step t is at position t. A step whose position
- *               lies outside [0, table_rows) (-1, say: padding) gives zeros, and no gradient.
+ *               lies outside [0, table_rows) (-1, say: padding) gives zeros, and no gradient;
+ *               where rot is 0 there is no table, and only positions below 0 are outside.
  *   q_out, k_out, dq, dk : contiguous, storage type;  dq_weight, dk_weight : [dim] fp32
  * Arithmetic is fp32; results are rounded once. mean(x^2) has to be finite in fp32.
  *

@@ -46,7 +46,7 @@ struct QkParams {
   const float *cos, *sin;
   const int32_t* positions;
   float eps, inv_dim;
-  int64_t table_rows;
+  uint32_t places;           // positions from here on, and those below 0, are padding
   uint32_t seqlen;
   int dim, rot, turning;     // turning: lanes of a row that hold pairs
   int interleaved;
@@ -192,8 +192,8 @@ __device__ __forceinline__ Item item_of(uint32_t at, const QkSide& d, uint32_t s
 }
 
 __device__ __forceinline__ void load_angles(const QkParams& p, Item& x, const Runs& u, float (&c)[4], float (&s)[4]) {
-  const int64_t pos = p.positions ? p.positions[int64_t(x.b) * p.seqlen + x.t] : x.t;
-  x.at_table = p.rot == 0 || (pos >= 0 && pos < p.table_rows);
+  const uint32_t pos = p.positions ? uint32_t(p.positions[int64_t(x.b) * p.seqlen + x.t]) : x.t;
+  x.at_table = pos < p.places;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     c[i] = 1.0f;
@@ -201,8 +201,8 @@ __device__ __forceinline__ void load_angles(const QkParams& p, Item& x, const Ru
   }
   if (u.turns && x.at_table) {
     const int half = p.rot / 2, n = half - u.angle;
-    load_few<float, 4>(p.cos + pos * half + u.angle, n, c);
-    load_few<float, 4>(p.sin + pos * half + u.angle, n, s);
+    load_few<float, 4>(p.cos + int64_t(pos) * half + u.angle, n, c);
+    load_few<float, 4>(p.sin + int64_t(pos) * half + u.angle, n, s);
   }
 }
 
@@ -411,7 +411,10 @@ int launch(const QkArgs& a, bool bwd, void* stream) {
   p.q_groups = uint32_t(q_groups);
   p.cos = a.cos, p.sin = a.sin, p.positions = a.positions;
   p.eps = a.eps, p.inv_dim = 1.0f / float(a.dim);
-  p.seqlen = uint32_t(a.seqlen), p.table_rows = a.table_rows;
+  p.seqlen = uint32_t(a.seqlen);
+  // (without a rotation there is no table, and every position that is not below 0 has a place)
+  constexpr int64_t kMost = int64_t(1) << 31;
+  p.places = uint32_t(a.rot == 0 || a.table_rows > kMost ? kMost : a.table_rows);
   p.dim = int(a.dim), p.rot = int(a.rot), p.turning = int((a.rot / 2 + 3) / 4);
   p.interleaved = a.interleaved;
   if (groups > 0) {

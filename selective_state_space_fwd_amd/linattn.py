@@ -345,8 +345,9 @@ def qk_norm(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=No
     q: [batch, seqlen, q_heads, dim], k: [batch, seqlen, k_heads, dim] float32 or bfloat16 (dim at
     most 256); q_weight, k_weight: [dim] float32 (None: ones); cos, sin: [positions, pairs]
     float32, the angles' (None: no rotation); positions: [batch, seqlen] int32 (None: step t is
-    at position t); a step whose position lies outside the table gives zeros. Pairs are (i, i +
-    pairs), or, interleaved, (2 i, 2 i + 1). Returns (q_out, k_out), contiguous, in q's dtype."""
+    at position t); a step whose position lies outside the table, or without one below 0, is padding
+    and gives zeros. Pairs are (i, i + pairs), or, interleaved, (2 i, 2 i + 1). Returns (q_out,
+    k_out), contiguous, in q's dtype."""
     r = _native().qk_norm(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, q_out,
                           k_out)
     if r is not None:

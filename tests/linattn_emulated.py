@@ -126,3 +126,26 @@ class Emulated:
             dv, None)
         assert status == ssm.SSM_OK
         return {name: None if x is None else widened(x) for name, x in d.items()}
+
+    def qk(self, io, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, eps=1e-6):
+        """(q_out, k_out, dq, dk, dq_weight, dk_weight); cos and sin may be None."""
+        b, L, hq, d = q.shape
+        hk, rows, rot = k.shape[2], 0 if cos is None else len(cos), 0 if cos is None else 2 * cos.shape[1]
+        flags = ssm.SSM_IO_F32 if io == "f32" else ssm.SSM_IO_BF16
+        f32 = lambda x: None if x is None else np.ascontiguousarray(x, np.float32)
+        q, k, dq_out, dk_out = (stored(x, io) for x in (q, k, dq_out, dk_out))
+        shared = [f32(x) for x in (q_weight, k_weight, cos, sin)]
+        shared.append(None if positions is None else np.ascontiguousarray(positions, np.int32))
+        sizes = (b, L, hq, hk, d, rot, rows)
+        qo, ko, dq, dk = empty(q.shape, io), empty(k.shape, io), empty(q.shape, io), empty(k.shape, io)
+        qw, kw = empty((d,)), empty((d,))
+        status = self.lib.ssm_qk_norm_fwd(pointer(q), None, pointer(k), None, *map(pointer, shared), eps, flags,
+                                          pointer(qo), pointer(ko), *sizes, None)
+        assert status == ssm.SSM_OK
+        need = self.lib.ssm_qk_norm_bwd_workspace_bytes(*sizes[:6], flags)
+        ws, at = self._workspace(need)
+        status = self.lib.ssm_qk_norm_bwd(
+            pointer(q), None, pointer(k), None, pointer(dq_out), None, pointer(dk_out), None, *map(pointer, shared), eps,
+            flags, pointer(dq), pointer(dk), pointer(qw), pointer(kw), at, need, *sizes, None)
+        assert status == ssm.SSM_OK
+        return [widened(x) for x in (qo, ko, dq, dk, qw, kw)]
