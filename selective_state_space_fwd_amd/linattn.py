@@ -145,7 +145,7 @@ def _decays(g, lead, heads, dev):
 
 
 def _scale(scale, dk) -> float:
-    return dk ** -0.5 if scale is None else float(scale)
+    return max(dk, 1) ** -0.5 if scale is None else float(scale)  # (dk 0 is refused by the library)
 
 
 class _Sizes:
