@@ -69,3 +69,16 @@ def test_gradients_of_decays(kernels, io, bad, index):
     args["g"][0, 70, index[2]] = -np.inf  # a reset after or before it does not hide it
     check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, "g", index, BAD[bad])
     check_forward(lambda **a: kernels.forward(io, **a), io, args, "g", index, BAD[bad])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("what,index", [("v", (0, 40, 1, 5)), ("k", (0, 40, 0, 3)), ("q", (0, 56, 0, 19)), ("dout", (0, 33, 1, 5)),
+                                        ("g", (0, 50, 1)), ("dfinal", (0, 0, 3, 4))])
+def test_before_the_end_of_a_row(kernels, io, what, index):
+    """A row of 57 of 90 steps, what lies behind its end NaN: only the value before the end is in the results."""
+    args, dout, dfinal = inputs(io, 90, 1, 2, 20, 36, 7)
+    for x in (args["q"], args["k"], args["v"], args["g"], dout):
+        x[:, 57:] = np.nan
+    check_backward(lambda **a: kernels.backward(io, **a), io, args, dout, dfinal, what, index, np.nan, [57])
+    if what in args:
+        check_forward(lambda **a: kernels.forward(io, **a), io, args, what, index, np.nan, [57])
