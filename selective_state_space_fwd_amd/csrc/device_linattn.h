@@ -187,19 +187,14 @@ __device__ __forceinline__ la_f32x4 get4(const float* p) { return *reinterpret_c
 // alone, plus one, carries into the sign's place where it is all ones.
 struct NotFinite {
   uint32_t seen = 0, signs = 0;
-  template <typename Elem>
-  __device__ __forceinline__ void add(const uint4& word) {
-    constexpr uint32_t kExponent = sizeof(Elem) == 2 ? 0x7f807f80u : 0x7f800000u;
-    constexpr uint32_t kOne = sizeof(Elem) == 2 ? 0x00800080u : 0x00800000u;
-    for (uint32_t w : {word.x, word.y, word.z, word.w}) seen |= (w & kExponent) + kOne;
-    signs = sizeof(Elem) == 2 ? 0x80008000u : 0x80000000u;
+  __device__ __forceinline__ void add(const Frag<uint16_t>& f) {
+    for (uint32_t w : {f.w.x, f.w.y, f.w.z, f.w.w}) seen |= (w & 0x7f807f80u) + 0x00800080u;
+    signs = 0x80008000u;
   }
-  __device__ __forceinline__ void add(const Frag<uint16_t>& f) { add<uint16_t>(f.w); }
   __device__ __forceinline__ void add(const Frag<float>& f) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4)
-      add<float>(make_uint4(__float_as_uint(f.v[i]), __float_as_uint(f.v[i + 1]), __float_as_uint(f.v[i + 2]),
-                            __float_as_uint(f.v[i + 3])));
+    for (int i = 0; i < 8; ++i) seen |= (__float_as_uint(f.v[i]) & 0x7f800000u) + 0x00800000u;
+    signs = 0x80000000u;
   }
   // In any lane of the wave.
   __device__ __forceinline__ bool any() const { return __ballot((seen & signs) != 0) != 0; }
@@ -270,10 +265,6 @@ struct TileLoad {
         w[i] = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
-  }
-  __device__ __forceinline__ void look(NotFinite& odd) const {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) odd.template add<Elem>(w[i]);
   }
   __device__ __forceinline__ void store(Elem* tile) const {
 #pragma unroll

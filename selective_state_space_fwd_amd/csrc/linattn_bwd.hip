@@ -96,18 +96,18 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   constexpr int T = C / 16, SB = C / 32, KB = KP / 32, VB = VP / 32;
   constexpr uint32_t E = sizeof(Elem);
   // The largest sizes keep fewer operands at a time, for want of registers.
-  static constexpr int kUnroll = KB + VB > 8 ? 1 : 8;
+  constexpr int kUnroll = KB + VB > 8 ? 1 : 8;
   // The 16-wide column tiles of dk and dv that a wave owns, for all steps; where there are only four,
   // one for half of the steps.
   constexpr bool kHalfK = KP < 128, kHalfV = VP < 128;
   constexpr int NK = kHalfK ? 1 : KP / 128, NV = kHalfV ? 1 : VP / 128;
   constexpr int TK = kHalfK ? T / 2 : T, TV = kHalfV ? T / 2 : T;
-  // The states' operands are loaded ahead of the pairs where registers are left for them (b4 8 heads of
-  // 128 for 32 of 64, 2048 steps: 147 us against 155); 128 x 128 has none to spare.
+  // The states' operands are loaded ahead of the pairs where registers are left for them (b4, 8 heads of 128 for 32
+  // of 64, 2048 steps, the whole gradient: 263 us, 273 with each where it is used); 128 x 128 has none to spare.
   constexpr bool kAhead = NK * VB <= 2;
   // Where they are not, two blocks of them at a time in bf16: b1, 16 heads of 128 x 128, 16384 steps, the whole
   // gradient: 584 us; all four, with 80 bytes a lane spilled, 660. (fp32, without spills: all, 623 against 635.)
-  static constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
+  constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];
   __shared__ __attribute__((aligned(16))) Elem sP[C * PP], sD[C * PP];  // weights by rows s: scale D qk, scale D dov
@@ -223,7 +223,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
       }
     };
     const bool any_dg = p.dg || p.dg_sums;
-    NotFinite odd;  // of this thread's values of q, k and dout
+    unsigned long long met = 0;  // lanes with results that are not finite
+    auto look = [&](float x) { met |= __ballot(!(__builtin_fabsf(x) < __builtin_inff())); };
     float gate = 0.0f;
     auto begin = [&] {
       gate = gate_of(1);
@@ -238,8 +239,6 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
       lk.load(static_cast<const Elem*>(p.k.p) + b * p.k.batch + hk * p.k.head + t0 * p.k.step,
               uint32_t(p.k.step) * E, live, p.dk);
       fetch(0);
-      lq.look(odd);
-      lk.look(odd);
       lq.store(sQ);
       lk.store(sK);
     }
@@ -257,6 +256,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
     auto heads = [&](auto one_by_one, int r, int g) {
       constexpr bool alone = decltype(one_by_one)::value;
       const bool want_dg = !alone && any_dg;
+      // (The second form is to be small: it is hardly ever run.)
+      constexpr bool ahead = kAhead && !alone, column_ahead = NV * KB <= 4 && !alone;
+      constexpr int unroll = alone ? 1 : kUnroll, state_unroll = alone ? 1 : kStateUnroll;
       for (int hh = 0; hh < p.group; ++hh) {
         const int h = hk * p.group + hh;
         const int64_t state = ((b * p.heads + h) * p.chunks + c) * p.state_floats;
@@ -268,16 +270,15 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           const int k = 16 * (kt + n) + r, v = 32 * vb + 8 * g;
           return k < p.kpad && v < p.vpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
         };
-        uint4 fs[kAhead ? NK : 1][VB][2], fr[kAhead ? NK : 1][VB][2];
+        uint4 fs[ahead ? NK : 1][VB][2], fr[ahead ? NK : 1][VB][2];
 
         lds_barrier();  // every wave has read the head before
-        if constexpr (!alone) lo.look(odd);
         lv.store(sV);
         lo.store(sO);
         lds_barrier();
         // (ahead of the loads, which it would wait for)
         if (w == 6 && hh + 1 < p.group) decays[(hh + 1) & 1].set_apart(gate);
-        if constexpr (kAhead && !alone) {
+        if constexpr (ahead) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -299,10 +300,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           const int i = mine.i;
           for (int j = mine.j0; j < mine.j1; ++j) {
             la_f32x4 a = {0, 0, 0, 0}, d = {0, 0, 0, 0};
-#pragma unroll kUnroll
+#pragma unroll unroll
             for (int kb = 0; kb < KB; ++kb)
               a = mma(row_frag(sQ, QP, 16 * i + r, 32 * kb), row_frag(sK, QP, 16 * j + r, 32 * kb), a);
-#pragma unroll kUnroll
+#pragma unroll unroll
             for (int vb = 0; vb < VB; ++vb)
               d = mma(row_frag(sO, OP, 16 * i + r, 32 * vb), row_frag(sV, OP, 16 * j + r, 32 * vb), d);
             const int s = 16 * j + r;
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
         lds_barrier();
 
         // Column v of R, values k of a block of 32: operands of dv.
-        float rk[NV * KB <= 4 ? NV : 1][KB][8];
+        float rk[column_ahead ? NV : 1][KB][8];
         auto load_column = [&](int n, int kb, float (&x)[8]) {
           const int v = 16 * (vt + n) + r, k = 32 * kb + 8 * g;
           const uint32_t off = v < p.vpad && k < p.kpad ? uint32_t(k * p.vpad + v) * 4u : kLaOob;
@@ -365,10 +366,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           la_f32x4 xq[TK], xk[TK];
 #pragma unroll
           for (int i = 0; i < TK; ++i) xq[i] = xk[i] = la_f32x4{0, 0, 0, 0};
-#pragma unroll kStateUnroll
+#pragma unroll state_unroll
           for (int vb = 0; vb < VB; ++vb) {
             uint4 words[2][2];
-            if constexpr (kAhead && !alone) {
+            if constexpr (ahead) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 words[0][e] = fs[n][vb][e];
@@ -404,11 +405,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
             }
           }
           // (by now the states' registers are free again)
-          if (NV * KB <= 4 && n == NK - 1) {
+          if (column_ahead && n == NK - 1) {
 #pragma unroll
             for (int m = 0; m < NV; ++m)
 #pragma unroll
-              for (int kb = 0; kb < KB; ++kb) load_column(m, kb, rk[NV * KB <= 4 ? m : 0][kb]);
+              for (int kb = 0; kb < KB; ++kb) load_column(m, kb, rk[column_ahead ? m : 0][kb]);
           }
 #pragma unroll
           for (int i = 0; i < TK; ++i) {
@@ -451,10 +452,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
           la_f32x4 av[TV];
 #pragma unroll
           for (int i = 0; i < TV; ++i) av[i] = la_f32x4{0, 0, 0, 0};
-#pragma unroll kUnroll
+#pragma unroll unroll
           for (int kb = 0; kb < KB; ++kb) {
             Pieces<Elem, 2> pr;
-            if constexpr (NV * KB <= 4) {
+            if constexpr (column_ahead) {
               pr.split(rk[n][kb]);
             } else {
               float x[8];
@@ -489,6 +490,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
               }
             }
           }
+          if constexpr (!alone) look((av[0][0] + av[0][1]) + (av[0][2] + av[0][3]));
 #pragma unroll
           for (int i = 0; i < TV; ++i) put(dv_of(h), v_step, iv + i, v0 + 4 * g, p.dv, av[i]);
         }
@@ -515,10 +517,17 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
     };
     heads(std::false_type{}, r, g);
     // The weights of the pairs above the diagonal are zeros, which a value of q, k or dout that is not finite turns to
-    // NaN in steps that it has no part in: a workgroup that met one forms dq, dk and dv again. (Afterwards, since a
-    // branch around the products took the registers of the loads on their way. b4, 8 heads of 128 for 32 of 64, 2048
-    // steps, the whole gradient: 262.8 us, 260.4 without this, 495 with the branch.)
-    if (odd.any() && l == 0) again = 1;
+    // NaN in steps that it has no part in: a workgroup that met one forms dq, dk and dv again. It shows in the results
+    // of the last steps (dq) or the first (dk, dv), whose sums are over all pairs. (Afterwards, since a branch around the
+    // products took the registers of the loads on their way, and by the results, which are fewer than the values. b4, 8
+    // heads of 128 for 32 of 64, 2048 steps, the whole gradient: 262.2 us, 260.4 without this, 495 with the branch.)
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NK; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += aq[n][TK - 1][e] + ak[n][0][e];
+    look(sum);
+    if (met != 0 && l == 0) again = 1;
     lds_barrier();
     if (any_dg && w == 7) finish(p.group - 1);
     if (__builtin_expect(__builtin_amdgcn_readfirstlane(again), 0)) {
