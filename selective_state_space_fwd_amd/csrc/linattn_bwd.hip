@@ -27,10 +27,10 @@
 // of the product, and in two in dv.
 //
 // Measured, bf16, this kernel | the walk that leaves S and R: b4, 8 heads of 128 for 32 of 64, 2048 steps
-// 155 | 129 us, reading 370 MB and writing 70 | 106 and 268; b1, 16 heads of 128 x 128, 16384 steps 328 | 200 (and 105
+// 157 | 127 us, reading 370 MB and writing 70 | 106 and 268; b1, 16 heads of 128 x 128, 16384 steps 306 | 195 (and 104
 // for a first walk that finds its segments' starts). The two pass S and R through memory, 8 bytes a value
-// each way; recomputing them in this kernel (several chunks a workgroup) was slower, 168 against 147, for want of
-// registers. What bounds it: no unit is full (matrix cores 15%, LDS 30%, VALU 36% of its cycles, memory at half of
+// each way; recomputing them in this kernel (several chunks a workgroup) was slower by a seventh, for want of
+// registers. What bounds it: no unit is full (matrix cores 14%, LDS 28%, VALU 38% of its cycles, memory at half of
 // a copy's rate); registers hold a CU to one workgroup, whose loads, pairs, states and stores follow one another.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void linattn_bwd_kernel(BwdParams p
   // of 64, 2048 steps, the whole gradient: 263 us, 273 with each where it is used); 128 x 128 has none to spare.
   constexpr bool kAhead = NK * VB <= 2;
   // Where they are not, two blocks of them at a time in bf16: b1, 16 heads of 128 x 128, 16384 steps, the whole
-  // gradient: 584 us; all four, with 80 bytes a lane spilled, 660. (fp32, without spills: all, 623 against 635.)
+  // gradient: 588 us; all four, which spill, 672. (fp32, 8192 steps: two 632, all 634.)
   constexpr int kStateUnroll = !kAhead && E == 2 && kUnroll > 2 ? 2 : kUnroll;
   constexpr int QP = la_pitch<Elem>(KP), OP = la_pitch<Elem>(VP), PP = la_pitch<Elem>(C);
   __shared__ __attribute__((aligned(16))) Elem sQ[C * QP], sK[C * QP], sV[C * OP], sO[C * OP];

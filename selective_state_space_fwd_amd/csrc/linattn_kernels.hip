@@ -23,11 +23,13 @@
 // the recurrence, although a chunk's product passes over all pairs of its steps. (The check of a chunk's values
 // costs the whole-row forms between -3% and +1%: b8, 32 heads of 128 x 64 113.4 -> 109.8 us, fp32 b4 178.8 -> 180.1.)
 //
-// Measured, bf16: b4, 8 heads of 128 for 32 of 64, 2048 steps 80.4 us in all, 51 the forward, 29 the segments'
+// Measured, bf16: b4, 8 heads of 128 for 32 of 64, 2048 steps 80.1 us in all, 52 the forward, 30 the segments'
 // states, 7 the join (must move 106 MB, 21 us at a copy's rate; the three launches move 226); b1, 16 heads of
-// 128 x 128, 65536 steps 433, of which 323, 166 and 14 where each runs alone (must move 1076 MB, 210 us; they move 1750,
+// 128 x 128, 65536 steps 428, of which 337, 167 and 14 where each runs alone (must move 1076 MB, 210 us; they move 1748,
 // 4.1 TB/s). The long one is near memory's rate on what a second pass over k and v costs; the short one waits: a
-// chunk's products, decays and stores follow one another, and registers hold it to two workgroups a CU.
+// chunk's products, decays and stores follow one another, and 214 registers and 55 KB of LDS hold it to two workgroups
+// a CU. Near half of the LDS cycles are bank conflicts, from the operands' 16 rows, four banks apart: at eight (32 bytes
+// between rows) a third of them go, and no time with them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

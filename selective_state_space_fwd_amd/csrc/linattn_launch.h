@@ -60,7 +60,8 @@ constexpr int64_t linattn_pad(int64_t n, int64_t to) { return (n + to - 1) / to 
 // base 128 (4096 steps) 200 | 160 in four; 192 241 | 265 in two; 256 (2048 steps) 139 | 163. And only sequences of
 // more than five chunks, whose walk takes as long as the two launches more. bf16, 16 heads of 128 x 128 and
 // 64 of 128 x 64: 256 steps 24.0 18.3 | 26.3 28.8; 384 steps 32.5 24.9 | 29.4 30.9; 512 steps 41.6 31.3 | 31.0 32.8;
-// fp32: 128 steps 31.7 21.5 | 29.3 28.6; 192 steps 43.9 29.2 | 31.4 33.4.
+// fp32: 128 steps 31.7 21.5 | 29.3 28.6; 192 steps 43.9 29.2 | 31.4 33.4. (One number for all, by the 128 columns, which
+// lose most: 64 columns, whose chunks take less time, would be 6 us faster whole at six chunks and near even at eight.)
 constexpr int64_t kLinattnGroups = 512;
 constexpr int64_t kLinattnWhole = 5;
 inline int64_t linattn_cuts(int64_t base, int64_t chunks) {
