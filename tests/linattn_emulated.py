@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import tempfile
 
 import numpy as np
 
@@ -13,8 +14,19 @@ from test_linattn_cpu import CLANG, CSRC, HERE, HOST, KERNELS, ROOT
 HEADERS = ("device_block.h", "device_linattn.h", "linattn_launch.h", "qk_launch.h", "heads.h")
 
 
-def build(folder, rules={}):
-    """The library in `folder`, with these launch rules in place of the headers'."""
+_built = {}  # by launch rules: (the library, its folder), for all test files of a process
+
+
+def kernels_of(rules):
+    """The library with these launch rules in place of the headers'."""
+    key = tuple(sorted(rules.items()))
+    if key not in _built:
+        folder = tempfile.TemporaryDirectory(prefix="linattn")
+        _built[key] = build(folder.name, rules), folder
+    return _built[key][0]
+
+
+def build(folder, rules):
     found = set()
     for name in (*KERNELS, *HOST, *HEADERS):  # copies: their includes find the CPU's device_math.h and device_scan.h
         text = open(os.path.join(CSRC, name)).read()

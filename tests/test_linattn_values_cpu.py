@@ -3,7 +3,7 @@ takes them to, and no step before them."""
 import numpy as np
 import pytest
 
-from linattn_emulated import CLANG, build, rounded
+from linattn_emulated import CLANG, kernels_of, rounded
 from linattn_values import BAD, check_backward, check_forward
 from test_linattn_cpu import LARGE
 
@@ -11,8 +11,8 @@ pytestmark = pytest.mark.skipif(CLANG is None, reason="clang++ not available")
 
 
 @pytest.fixture(scope="module", params=[{}, LARGE], ids=["small", "large"])
-def kernels(request, tmp_path_factory):
-    return build(str(tmp_path_factory.mktemp("linattn")), request.param)
+def kernels(request):
+    return kernels_of(request.param)
 
 
 def inputs(io, L, hk, h, dk, dv, seed):

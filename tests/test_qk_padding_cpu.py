@@ -3,7 +3,7 @@ and no gradient, with a rotation and without one."""
 import numpy as np
 import pytest
 
-from linattn_emulated import CLANG, build, rounded
+from linattn_emulated import CLANG, kernels_of, rounded
 from linattn_util import U
 from oracle import linattn as ol
 from test_linattn_cpu import LARGE
@@ -12,8 +12,8 @@ pytestmark = pytest.mark.skipif(CLANG is None, reason="clang++ not available")
 
 
 @pytest.fixture(scope="module", params=[{}, LARGE], ids=["small", "large"])
-def kernels(request, tmp_path_factory):
-    return build(str(tmp_path_factory.mktemp("qk")), request.param)
+def kernels(request):
+    return kernels_of(request.param)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
